@@ -365,7 +365,7 @@ def _own_norm(s, moe, backward):
     out = {"y": s["y"], "z": s["z"]}
     if not backward:
         return out
-    moe.moe_block_norm_backward(t, s["h"], s["y"], s["gate"], gate, s["w_post"], s["w_pre"], s["rstd"][0],
+    moe.moe_block_norm_backward(t, s["h"], s["residual"], s["gate"], gate, s["w_post"], s["w_pre"], s["rstd"][0],
                                 s["rstd"][1], s["dy"], s["dz"], T, H, s["scale"], 0.0, s["dres"], s["dh"],
                                 s["dgate"], s["dw_post"], s["dw_pre"], s["ws"], s["ws"].numel())
     out.update(dres=s["dres"], dh=s["dh"], dw_post=s["dw_post"], dw_pre=s["dw_pre"])
