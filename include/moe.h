@@ -459,6 +459,190 @@ int moe_align_sort_noalloc(const int32_t *topk_ids, const float *topk_weights, i
                            int32_t *sorted_expert_ids, int32_t *num_tokens_post_padded,
                            int32_t *expert_counts, void *stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Operators around the layer: the token exchange, the block-scaled FP8
+ * product and the norms around a block, for blocks that the fused layer does
+ * not cover (other expert functions, shared experts, FP8 training).
+ *
+ * Rows are bf16, fp16 or fp32 (row_type); arithmetic and sums are fp32, each
+ * result rounded once.  None of these entries uses floating-point atomics:
+ * results are bitwise reproducible.  Rows that start and end on 16-byte
+ * boundaries are moved 16 bytes at a time, others element by element.
+ */
+#define MOE_ROW_BF16 0
+#define MOE_ROW_FP16 1
+#define MOE_ROW_FP32 2
+
+/*
+ * moe_align_sort that also gives the inverse map: slot_pos (device) int32
+ * [T*k], the sorted position of each slot, -1 for a slot left out because its
+ * id is outside [0, E).  Everything else as moe_align_sort (same ws).
+ */
+int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
+                       int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
+                       int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/*
+ * Rows to the experts' order: xs[slot_pos[t*k + j]] = x[t].
+ *   x (device) [T] rows of H elements at a pitch of ld_x >= H elements;
+ *   slot_pos (device) int32 [T*k]; a position outside [0, P) is skipped;
+ *   xs (device) [P][H].
+ * zero_padding = 1 also writes zeros to the padding rows (p <
+ * *num_tokens_post_padded with sorted_ids[p] >= T*k; both device pointers,
+ * ignored and may be NULL when 0).  Other rows of xs are left as they are.
+ * Limits: 1 <= k <= 32, T*k <= 2^30, P < 2^31.
+ */
+int moe_permute(int row_type, const void *x, int64_t ld_x, const int32_t *slot_pos, const int32_t *sorted_ids,
+                const int32_t *num_tokens_post_padded, int T, int k, int H, int64_t P, int zero_padding, void *xs,
+                void *stream);
+
+/*
+ * The same for bf16 rows, quantised per 1x128 group as moe_quantize_fp8_act
+ * does: q (device) e4m3 [P][H], s (device) fp32 [H/128][P] (by block: the
+ * a_scale_by_block = 1 form of moe_gemm_fp8_block).  A padding row that is
+ * zeroed has scale 1.  H % 128 == 0, ld_x % 8 == 0, x and q on 16-byte
+ * boundaries.
+ */
+int moe_permute_fp8(const void *x, int64_t ld_x, const int32_t *slot_pos, const int32_t *sorted_ids,
+                    const int32_t *num_tokens_post_padded, int T, int k, int H, int64_t P, int zero_padding,
+                    uint8_t *q, float *s, void *stream);
+
+/* Gradient of moe_permute: dx[t] = sum over j of dxs[slot_pos[t*k + j]] (j
+ * ascending).  dxs (device) [P][H]; dx (device) [T] rows at pitch ld_dx. */
+int moe_permute_backward(int row_type, const void *dxs, const int32_t *slot_pos, int T, int k, int H, int64_t P,
+                         void *dx, int64_t ld_dx, void *stream);
+
+/*
+ * Rows back to the tokens with the weights applied: out[t] = sum over j of
+ * topk_weights[t][j] * ys[slot_pos[t*k + j]] (j ascending, one rounding).
+ *   ys (device) [P][H]; topk_weights (device) fp32 [T][k], NULL = all 1;
+ *   out (device) [T] rows at pitch ld_out >= H.  A token with no position in
+ *   [0, P) gets a zero row.
+ */
+int moe_unpermute(int row_type, const void *ys, const int32_t *slot_pos, const float *topk_weights, int T, int k,
+                  int H, int64_t P, void *out, int64_t ld_out, void *stream);
+
+/*
+ * Gradient of moe_unpermute: dys[slot_pos[t*k + j]] = topk_weights[t][j] *
+ * dout[t] and dweights[t][j] = dout[t] . ys[slot_pos[t*k + j]] (0 for a
+ * skipped position).  dout (device) [T] rows at pitch ld_dout; ys, dys
+ * (device) [P][H]; dweights (device) fp32 [T][k]; zero_padding as in
+ * moe_permute, for dys.  dys may be ys (each row is read before it is
+ * written).
+ */
+int moe_unpermute_backward(int row_type, const void *dout, int64_t ld_dout, const void *ys, const int32_t *slot_pos,
+                           const float *topk_weights, const int32_t *sorted_ids,
+                           const int32_t *num_tokens_post_padded, int T, int k, int H, int64_t P, int zero_padding,
+                           void *dys, float *dweights, void *stream);
+
+/* Bytes of the workspace of moe_gemm_fp8_block and moe_wgrad_fp8_block: a
+ * status word that the caller zeroes once before the first call; a call whose
+ * wait runs out leaves MOE_ERR_TIMEOUT in it (read with moe_workspace_status). */
+#define MOE_GEMM_BLOCK_WS_BYTES 64
+
+/*
+ * Matrix product of e4m3 operands with an fp32 scale per block of 128:
+ *   D[m][n] = sum over b of a_scale[m, b] * b_scale[e][n/128][b] *
+ *             sum over k in [128 b, 128 b + 128) of A[m][k] * B[e][n][k]
+ * Dense (sorted_expert_ids and num_tokens_post_padded NULL, E = 1, block_m =
+ * 0): all M rows, e = 0.  Grouped: rows in the order of moe_align_sort, e =
+ * sorted_expert_ids[m / block_m], rows m < *num_tokens_post_padded (padding
+ * rows included; later rows of D are left as they are); block_m 16, 32, 64 or
+ * a multiple of 128.
+ *   A (device) e4m3 [M][K]; a_scale (device) fp32 [M][ceil(K/128)]
+ *   (a_scale_by_block = 0, as moe_quantize_fp8_act gives it) or
+ *   [ceil(K/128)][M] (1, as moe_permute_fp8 gives it);
+ *   B (device) e4m3 [E][N][K]; b_scale (device) fp32
+ *   [E][ceil(N/128)][ceil(K/128)];
+ *   D (device) rows of N at a pitch of ld_d, bf16 or fp32 (out_type);
+ *   ws (device) MOE_GEMM_BLOCK_WS_BYTES.
+ * K % 16 == 0; A and B on 16-byte boundaries; any M and N.  The gradient with
+ * respect to A is the same product with B transposed.
+ */
+int moe_gemm_fp8_block(const uint8_t *A, const float *a_scale, int a_scale_by_block, const uint8_t *B,
+                       const float *b_scale, int64_t M, int N, int K, int E, int block_m,
+                       const int32_t *sorted_expert_ids, const int32_t *num_tokens_post_padded, int out_type, void *D,
+                       int64_t ld_d, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Weight gradient: for every expert e over its sorted rows p (whole blocks of
+ * 128: expert e's rows start after ceil(expert_counts / 128) blocks of each
+ * expert before it),
+ *   D[e][m][n] (+)= sum over p of a_scale[p/128][m] A[m][p] * b_scale[p/128][n] B[n][p]
+ *   A (device) e4m3 [M][P], a_scale (device) fp32 [P/128][M];
+ *   B (device) e4m3 [N][P], b_scale (device) fp32 [P/128][N] (both as
+ *   moe_quantize_fp8_act_t gives them: padding rows are zero codes);
+ *   expert_counts (device) int32 [E], or NULL with E = 1: all P rows;
+ *   D (device) fp32 [E][M][N]; accumulate = 1 adds to D, 0 overwrites it (an
+ *   expert without rows gets zeros).
+ * P % 128 == 0, N % 4 == 0, E <= 1024, b_scale on a 16-byte boundary.
+ */
+int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B, const float *b_scale, int64_t P,
+                        int M, int N, int E, const int32_t *expert_counts, float *D, int accumulate, void *ws,
+                        size_t ws_bytes, void *stream);
+
+/*
+ * Transposing quantiser for moe_wgrad_fp8_block: per column c and 128 rows,
+ * scale = amax / 448 (1 if zero) and codes as moe_quantize_fp8_act.
+ *   X (device) bf16 rows of C at a pitch of ld_x; with sorted_ids (device,
+ *   int32 [R]) row p is X's row sorted_ids[p] / k, zero where sorted_ids[p] is
+ *   outside [0, S) (padding); NULL: row p of X;
+ *   num_rows (device) int32 or NULL: rows in use, at most R; rows past it
+ *   inside its last block of 128 are zeros, later blocks are not written;
+ *   q (device) e4m3 [C] rows at a pitch of ld_q >= ceil(R/128)*128;
+ *   s (device) fp32 [ceil(R/128)][C].
+ * C % 8 == 0, ld_x % 8 == 0, ld_q % 16 == 0, X and q on 16-byte boundaries.
+ */
+int moe_quantize_fp8_act_t(const void *X, int64_t ld_x, int64_t R, int C, const int32_t *sorted_ids, int S, int k,
+                           const int32_t *num_rows, uint8_t *q, int64_t ld_q, float *s, void *stream);
+
+#define MOE_GATE_NONE 0     /* no gate (1) */
+#define MOE_GATE_CHANNEL 1  /* [H]: one value per column */
+#define MOE_GATE_TOKEN 2    /* [T]: one value per row */
+#define MOE_GATE_FULL 3     /* [T][H] */
+
+/*
+ * The norms before and after a block, fused with its gate and residual scale:
+ *   n = h * rstd(h) * (w_post + weight_offset)    (n = h if w_post is NULL)
+ *   y = residual + scale * gate * n
+ *   z = y * rstd(y) * (w_pre + weight_offset)     (no z if w_pre is NULL)
+ * with rstd(v) = 1 / sqrt(mean(v^2) + eps) over the row.  h is a block's
+ * output, y the residual stream after it, z the next block's input (its
+ * w_pre).
+ *   h, residual, y, z (device) [T][H] of row_type; gate (device) of row_type,
+ *   shaped by gate_kind; w_post, w_pre (device) [H] of row_type; rstd_h,
+ *   rstd_y (device) fp32 [T] or NULL: kept for the backward.
+ * y may be residual, and z may be h (each row is read before it is written;
+ * the backward needs both, so not in training).
+ * H <= 16384.
+ */
+int moe_block_norm(int row_type, const void *h, const void *residual, const void *gate, int gate_kind,
+                   const void *w_post, const void *w_pre, int64_t T, int H, float scale, float weight_offset,
+                   float eps, void *y, void *z, float *rstd_h, float *rstd_y, void *stream);
+
+/* Workspace bytes of moe_block_norm_backward (0 on invalid input). */
+size_t moe_block_norm_workspace_size(int64_t T, int H);
+
+/*
+ * Gradients of moe_block_norm for loss = sum(dy * y) + sum(dz * z):
+ *   h, residual: the forward's inputs (residual with w_pre only; y is formed
+ *   from them again, unrounded); rstd_h, rstd_y as it gave them (each
+ *   required with its norm); dy (device) [T][H] or NULL (zero); dz
+ *   (device) [T][H], with w_pre only (without it, dy is required);
+ *   d_residual, dh (device) [T][H] of row_type;
+ *   dgate (device): fp32 [H] or [T], or row_type [T][H]; with a gate only;
+ *   dw_post, dw_pre (device) fp32 [H], each with its norm only;
+ *   ws (device) moe_block_norm_workspace_size bytes.
+ * d_residual may be dy, and dh may be h.
+ */
+int moe_block_norm_backward(int row_type, const void *h, const void *residual, const void *gate, int gate_kind,
+                            const void *w_post, const void *w_pre, const float *rstd_h, const float *rstd_y,
+                            const void *dy, const void *dz, int64_t T, int H, float scale, float weight_offset,
+                            void *d_residual, void *dh, void *dgate, float *dw_post, float *dw_pre, void *ws,
+                            size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,887 @@
+// The matrix product in 8-bit floating point with a scale for each block of 128, as an operator of
+// its own: dense or grouped by expert (the group GEMM of the AITER walk-through, section 3.2, with
+// its "per_1x128" quantisation), and the weight gradient over each expert's tokens.
+//
+//   product   D[m][n] = sum_b sa[m][b] sb[n/128][b] sum_{k in block b} A[m][k] B[n][k]
+//   gradient  D[e][m][n] = sum_{b of e} sum_{p in block b} (sa[b][m] A[m][p]) (sb[b][n] B[n][p])
+//
+// The scales are any fp32 values, not the power-of-two 32-element scales that the tensor core
+// applies itself, so every 128-wide block of K is accumulated on its own by tcgen05.mma
+// kind::f8f6f4 into a TMEM buffer, and promotion warps fold it into fp32 registers with its scales
+// while the tensor core fills the next buffer.  K need not be a multiple of 128: the copies zero-fill
+// past the end, and a zero code adds nothing.
+#include <cuda_bf16.h>
+
+#include "gemm_common.cuh"
+#include "moe_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+namespace blockgemm {
+
+struct Args {
+    CUtensorMap tm_a;  // token operand (wgrad: rows of D)
+    CUtensorMap tm_b;  // weight operand (wgrad: columns of D)
+    const float *sa;
+    int64_t sa_row, sa_blk;  // strides of sa: per row, per 128-block of K
+    const float *sb;         // product: [E][ceil(N/128)][KB]; wgrad: [KB][N]
+    const int32_t *expert_ids;  // expert of each block_m rows, or null (dense)
+    const int32_t *npp;         // rows in use (device), or null: M
+    const int32_t *counts;      // wgrad: tokens of each expert, or null (one segment: all of K)
+    int64_t M;
+    int N, K, E, block_m;
+    void *d;
+    int64_t ld_d;
+    int out_f32, accumulate;
+    int wide;  // rows of D start and end on 16-byte boundaries
+    int *status;
+};
+
+__device__ __forceinline__ int64_t rows_in_use(const Args &a)
+{
+    if (!a.npp)
+        return a.M;
+    const int64_t n = *a.npp;
+    return n < 0 ? 0 : n < a.M ? n : a.M;
+}
+
+__device__ __forceinline__ int expert_of(const Args &a, int64_t row)
+{
+    if (!a.expert_ids)
+        return 0;
+    const int e = __ldg(a.expert_ids + row / a.block_m);
+    return (unsigned)e < (unsigned)a.E ? e : 0;
+}
+
+// acc[0..1] += v[0..1] * f[0..1]
+__device__ __forceinline__ void ffma2v(float &acc0, float &acc1, float v0, float v1, float f0, float f1)
+{
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(acc0), "+f"(acc1)
+        : "f"(v0), "f"(v1), "f"(f0), "f"(f1));
+}
+
+// ------------------------------------------------------------ many rows
+//
+// A tile is 128 rows of A x TN rows of B.  Warps: 0 TMA producer, 1 TMEM allocation and MMA issue,
+// 2..9 promotion and epilogue (two per TMEM lane quadrant, half of the columns each).
+
+template <int TN, bool WG>
+struct Cfg {
+    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 6 : 8;
+    static constexpr int kABytes = 128 * 128, kBBytes = TN * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kBufs = TN == 256 ? 2 : 4;  // TMEM accumulators
+    static constexpr int kScaleSlots = WG ? 4 : 1;
+};
+
+constexpr int kPromoWarps = 8;
+constexpr int kThreads = 64 + 32 * kPromoWarps;
+constexpr int kGroupM = 16;  // row tiles that walk the column tiles together
+constexpr int kMaxE = 1024;
+
+template <int TN, bool WG>
+struct __align__(1024) Smem {
+    using C = Cfg<TN, WG>;
+    uint8_t stage[C::kStages][C::kStageBytes];
+    float sb[C::kScaleSlots][WG ? TN : 4];  // wgrad: the block's column scales
+    float4 ep_out[kPromoWarps][32][4];      // a warp's 32 rows x 64 bytes on their way to D
+    uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t tfull[C::kBufs], tempty[C::kBufs];
+    uint64_t sfull[C::kScaleSlots], sempty[C::kScaleSlots];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int off[WG ? kMaxE + 1 : 1];  // wgrad: first 128-block of each expert
+};
+
+struct Tile {
+    int e;
+    int64_t row0;
+    int col0;
+    int kb0, kb1;
+};
+
+template <int TN, bool WG>
+__global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_constant__ Args a)
+{
+    using C = Cfg<TN, WG>;
+    extern __shared__ uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<Smem<TN, WG> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort_flag = &sm.abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < C::kBufs; ++i) {
+            mbar_init(&sm.tfull[i], 1);
+            mbar_init(&sm.tempty[i], kPromoWarps);
+        }
+        for (int i = 0; i < C::kScaleSlots; ++i) {
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.sempty[i], kPromoWarps);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&a.tm_a);
+        tma_prefetch_desc(&a.tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, C::kBufs * TN);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    if (WG && warp == 2) {
+        // first block of each expert: a running sum of ceil(count / 128) over the experts
+        int run = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = !a.counts ? a.K : e < a.E ? a.counts[e] : 0;
+            int v = e < a.E && c > 0 ? (c + 127) / 128 : 0;
+            int incl = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d)
+                    incl += o;
+            }
+            if (e < a.E)
+                sm.off[e] = run + incl - v;
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0)
+            sm.off[a.E] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = sm.tmem_base;
+    const int KB = (a.K + 127) / 128;
+    const int64_t rows = rows_in_use(a);
+    const int nmt = (int)((rows + 127) / 128);
+    const int nnt = (a.N + TN - 1) / TN;
+    const int64_t ntiles = (int64_t)nmt * nnt * (WG ? a.E : 1);
+
+    auto get_tile = [&](int64_t t) {
+        Tile tl;
+        int within = (int)(WG ? t % ((int64_t)nmt * nnt) : t);
+        const int group = within / (kGroupM * nnt);
+        within -= group * kGroupM * nnt;
+        const int gsize = min(kGroupM, nmt - group * kGroupM);
+        tl.row0 = (int64_t)(group * kGroupM + within % gsize) * 128;
+        tl.col0 = within / gsize * TN;
+        if (WG) {
+            tl.e = (int)(t / ((int64_t)nmt * nnt));
+            tl.kb0 = min(sm.off[tl.e], KB);
+            tl.kb1 = min(sm.off[tl.e + 1], KB);
+        } else {
+            tl.e = expert_of(a, tl.row0);
+            tl.kb0 = 0;
+            tl.kb1 = KB;
+        }
+        return tl;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_b = l2_policy_evict_normal();
+            const uint64_t pol_a = l2_policy_evict_last();
+            int s = 0, ss = 0;
+            uint32_t ph = 0, sph = 0;
+            uint32_t issued = 0;  // stages with a copy issued, and its phase
+            uint32_t issued_ph = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+                const Tile tl = get_tile(t);
+                const int brow = WG ? tl.col0 : tl.e * a.N + tl.col0;
+                for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
+                    if (!mbar_wait(&sm.empty[s], ph ^ 1, a.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = sm.stage[s];
+                    mbar_arrive_expect_tx(&sm.full[s], C::kStageBytes);
+                    tma_load_2d(dst, &a.tm_a, kb * 128, (int)tl.row0, &sm.full[s], pol_a);
+#pragma unroll
+                    for (int i = 0; i < (TN + 127) / 128; ++i)
+                        tma_load_2d(dst + C::kABytes + i * 128 * 128, &a.tm_b, kb * 128, brow + i * 128, &sm.full[s],
+                                    pol_b);
+                    issued |= 1u << s;
+                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    if (WG) {
+                        if (!mbar_wait(&sm.sempty[ss], sph ^ 1, a.status, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bytes = (uint32_t)min(TN, a.N - tl.col0) * 4;
+                        mbar_arrive_expect_tx(&sm.sfull[ss], bytes);
+                        bulk_load(sm.sb[ss], a.sb + (int64_t)kb * a.N + tl.col0, bytes, &sm.sfull[ss]);
+                        if (++ss == C::kScaleSlots) {
+                            ss = 0;
+                            sph ^= 1;
+                        }
+                    }
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {  // let the copies in flight land before the shared memory is given up
+                for (int i = 0; i < C::kStages; ++i)
+                    if (issued >> i & 1) {
+                        const unsigned long long t0 = global_timer_ns();
+                        while (!mbar_try_wait(&sm.full[i], issued_ph >> i & 1) &&
+                               global_timer_ns() - t0 < 100000000ull) {
+                        }
+                    }
+                if (WG) {  // the scale copies, each 1 KB or less, given a bounded moment
+                    const unsigned long long t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 20000000ull) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true, any = false;
+            const uint32_t idesc = make_idesc(0, 0, 128, TN);
+            for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+                const Tile tl = get_tile(t);
+                for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
+                    if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag) ||
+                        !mbar_wait(&sm.tempty[buf], bph ^ 1, a.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t *as = sm.stage[s], *bs = sm.stage[s] + C::kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_fp8(tmem_base + buf * TN, smem_desc_sw128(as + kk * 32), smem_desc_sw128(bs + kk * 32),
+                                idesc, kk > 0 ? 1u : 0u);
+                    any = true;
+                    mma_commit(&sm.empty[s]);
+                    mma_commit(&sm.tfull[buf]);
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    if (++buf == C::kBufs) {
+                        buf = 0;
+                        bph ^= 1;
+                    }
+                }
+            }
+            if (!ok && any) {
+                mma_commit(&sm.drain);
+                const unsigned long long t0 = global_timer_ns();
+                while (!mbar_try_wait(&sm.drain, 0) && global_timer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3;           // TMEM lane quadrant
+        const int sub = (warp - 2) >> 2;  // half of the columns
+        constexpr int kCols = TN / 2;
+        constexpr int kLd = kCols >= 32 ? 16 : 8;
+        const int row = q * 32 + lane;
+        int buf = 0, ss = 0;
+        uint32_t bph = 0, sph = 0;
+        bool ok = true;
+        const int nsb = (a.N + 127) / 128;
+        for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+            const Tile tl = get_tile(t);
+            const int64_t grow = tl.row0 + row;
+            const int64_t srow = grow < a.M ? grow : a.M - 1;  // a row past M is never stored
+            const float *sa = a.sa + srow * a.sa_row;
+            const int nb = min((tl.col0 + sub * kCols) / 128, nsb - 1);
+            const float *sb = WG ? nullptr : a.sb + ((int64_t)tl.e * nsb + nb) * KB;
+            float acc[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+                acc[i] = 0.0f;
+            float sa_n = 0.0f, sb_n = 1.0f;
+            if (tl.kb0 < tl.kb1) {
+                sa_n = sa[tl.kb0 * a.sa_blk];
+                sb_n = WG ? 1.0f : sb[tl.kb0];
+            }
+            for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
+                const float f = sa_n * sb_n;
+                if (kb + 1 < tl.kb1) {  // fetched while this block is on the tensor core
+                    sa_n = sa[(kb + 1) * a.sa_blk];
+                    sb_n = WG ? 1.0f : sb[kb + 1];
+                }
+                bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
+                if (WG)
+                    w_ok = w_ok && mbar_wait(&sm.sfull[ss], sph, a.status, abort_flag);
+                if (!__all_sync(0xffffffffu, w_ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * TN + sub * kCols;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2 * kLd) {
+                    float v[kLd], u[kLd];
+                    tmem_ld_nowait(tb + c, v);
+                    tmem_ld_nowait(tb + c + kLd, u);
+                    tmem_wait_ld(v, u);
+                    if (WG) {
+                        const float4 *s4 = reinterpret_cast<const float4 *>(sm.sb[ss] + sub * kCols + c);
+#pragma unroll
+                        for (int i = 0; i < kLd; i += 4) {
+                            const float4 x = s4[i / 4], y = s4[(i + kLd) / 4];
+                            ffma2v(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f * x.x, f * x.y);
+                            ffma2v(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f * x.z, f * x.w);
+                            ffma2v(acc[c + kLd + i], acc[c + kLd + i + 1], u[i], u[i + 1], f * y.x, f * y.y);
+                            ffma2v(acc[c + kLd + i + 2], acc[c + kLd + i + 3], u[i + 2], u[i + 3], f * y.z, f * y.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kLd; i += 2) {
+                            ffma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
+                            ffma2(acc[c + kLd + i], acc[c + kLd + i + 1], u[i], u[i + 1], f);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.tempty[buf]);
+                    if (WG)
+                        mbar_arrive(&sm.sempty[ss]);
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+                if (WG && ++ss == C::kScaleSlots) {
+                    ss = 0;
+                    sph ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            // Each lane holds one row.  Pieces of 64 bytes a row go through a per-warp shared block
+            // (16-byte slot j of row r at j ^ ((r >> 1) & 3): no bank conflicts either way) and
+            // leave as 8 rows x 64 contiguous bytes per store.
+            float4(*ep)[4] = sm.ep_out[warp - 2];
+            const int rr = lane >> 2, cq = lane & 3;
+            const int n0 = tl.col0 + sub * kCols;
+            const int64_t base = (WG ? (int64_t)tl.e * a.M : 0) + tl.row0 + q * 32;  // D row of lane 0
+            const int64_t left = a.M - tl.row0 - q * 32;                             // rows of D from there
+            auto flush = [&](int col, int per) {  // columns col.. of D, `per` elements per 16 bytes
+                __syncwarp();
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int r = 8 * it + rr;
+                    float4 o = ep[r][cq ^ ((r >> 1) & 3)];
+                    const int n = col + per * cq;
+                    if (r >= left || n >= a.N)
+                        continue;
+                    const int64_t at = (base + r) * a.ld_d + n;
+                    if (a.out_f32) {
+                        float *d = static_cast<float *>(a.d) + at;
+                        if (a.wide) {
+                            if (a.accumulate) {
+                                const float4 p = *reinterpret_cast<float4 *>(d);
+                                o = make_float4(o.x + p.x, o.y + p.y, o.z + p.z, o.w + p.w);
+                            }
+                            *reinterpret_cast<float4 *>(d) = o;
+                        } else {
+                            const float e4[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (n + i < a.N)
+                                    d[i] = a.accumulate ? d[i] + e4[i] : e4[i];
+                        }
+                    } else {
+                        __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.d) + at;
+                        if (a.wide) {
+                            *reinterpret_cast<float4 *>(d) = o;
+                        } else {
+                            const uint32_t e4[4] = {__float_as_uint(o.x), __float_as_uint(o.y), __float_as_uint(o.z),
+                                                    __float_as_uint(o.w)};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (n + i < a.N)
+                                    reinterpret_cast<uint16_t *>(d)[i] = (uint16_t)(e4[i / 2] >> (16 * (i & 1)));
+                        }
+                    }
+                }
+                __syncwarp();
+            };
+            if (a.out_f32) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ep[lane][j ^ ((lane >> 1) & 3)] =
+                            make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
+                    flush(n0 + c, 4);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ep[lane][j ^ ((lane >> 1) & 3)] = pack_bf16x8(acc + c + 8 * j, 1.0f);
+                    flush(n0 + c, 8);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, C::kBufs * TN);
+}
+
+// ------------------------------------------------------------- few rows
+//
+// Up to NP rows per expert: the weights take the tensor core's 128-row side and the NP rows of A its
+// columns, so a tile streams 128 weight rows once.  A ring of 16 KB weight stages keeps the HBM
+// requests in flight.  A cluster of S CTAs shares one tile, each taking a part of K; the parts are
+// added through distributed shared memory in the order of the CTAs' ranks.
+
+template <int NP>
+struct FewCfg {
+    static constexpr int kWBytes = 128 * 128;
+    static constexpr int kXBytes = NP * 128;
+    static constexpr int kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = NP == 64 ? 7 : NP == 32 ? 9 : 10;
+    static constexpr int kBufs = 4;
+    static constexpr int kTmem = kBufs * NP < 32 ? 32 : kBufs * NP;
+};
+constexpr int kFewThreads = 192;
+constexpr int kFewWarps = 4;
+
+template <int NP>
+struct __align__(1024) FewSmem {
+    using C = FewCfg<NP>;
+    uint8_t stage[C::kStages][C::kStageBytes];
+    float red[NP * 128];                 // the parts of this CTA's rows: [source][column][row]
+    float f[kFewWarps][2][NP];           // a warp's column factors, alternating between blocks
+    uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t tfull[C::kBufs], tempty[C::kBufs];
+    uint64_t red_full, red_free;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int NP>
+__global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __grid_constant__ Args a, int S)
+{
+    using C = FewCfg<NP>;
+    extern __shared__ uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<FewSmem<NP> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    volatile int *abort_flag = &sm.abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < C::kBufs; ++i) {
+            mbar_init(&sm.tfull[i], 1);
+            mbar_init(&sm.tempty[i], kFewWarps);
+        }
+        mbar_init(&sm.red_full, S > kFewWarps ? S : kFewWarps);
+        mbar_init(&sm.red_free, S * kFewWarps);
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&a.tm_a);
+        tma_prefetch_desc(&a.tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, C::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (S > 1)
+        cluster_sync();  // every CTA's barriers exist before a peer signals them
+    tc_fence_after();
+    const uint32_t tmem_base = sm.tmem_base;
+    pdl_wait();
+    const int KB = (a.K + 127) / 128;
+    const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
+    const int64_t rows = rows_in_use(a);
+    const int nblk = (int)((rows + NP - 1) / NP);
+    const int nwt = (a.N + 127) / 128;
+    const int64_t ntiles = (int64_t)nblk * nwt;
+    const int first = blockIdx.x / S, step = gridDim.x / S;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = nblk > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+            const uint64_t pol_x = l2_policy_evict_last();
+            int s = 0;
+            uint32_t ph = 0, issued = 0, issued_ph = 0;
+            bool ok = true;
+            for (int64_t t = first; ok && t < ntiles; t += step) {
+                const int b = (int)(t % nblk), wt = (int)(t / nblk);
+                const int wrow = expert_of(a, (int64_t)b * NP) * a.N + wt * 128;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&sm.empty[s], ph ^ 1, a.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sm.full[s], C::kStageBytes);
+                    tma_load_2d(sm.stage[s], &a.tm_b, kb * 128, wrow, &sm.full[s], pol_w);
+                    tma_load_2d(sm.stage[s] + C::kWBytes, &a.tm_a, kb * 128, b * NP, &sm.full[s], pol_x);
+                    issued |= 1u << s;
+                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok)
+                for (int i = 0; i < C::kStages; ++i)
+                    if (issued >> i & 1) {
+                        const unsigned long long t0 = global_timer_ns();
+                        while (!mbar_try_wait(&sm.full[i], issued_ph >> i & 1) &&
+                               global_timer_ns() - t0 < 100000000ull) {
+                        }
+                    }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true, any = false;
+            const uint32_t idesc = make_idesc(0, 0, 128, NP);
+            for (int64_t t = first; ok && t < ntiles; t += step)
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag) ||
+                        !mbar_wait(&sm.tempty[buf], bph ^ 1, a.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t *w = sm.stage[s], *x = sm.stage[s] + C::kWBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_fp8(tmem_base + buf * NP, smem_desc_sw128(w + kk * 32), smem_desc_sw128(x + kk * 32),
+                                idesc, kk > 0 ? 1u : 0u);
+                    any = true;
+                    mma_commit(&sm.empty[s]);
+                    mma_commit(&sm.tfull[buf]);
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    if (++buf == C::kBufs) {
+                        buf = 0;
+                        bph ^= 1;
+                    }
+                }
+            if (!ok && any) {
+                mma_commit(&sm.drain);
+                const unsigned long long t0 = global_timer_ns();
+                while (!mbar_try_wait(&sm.drain, 0) && global_timer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3, pw = warp - 2;
+        const int row = q * 32 + lane;  // weight row of the tile
+        int buf = 0;
+        uint32_t bph = 0, rph = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < ntiles; t += step) {
+            const int b = (int)(t % nblk), wt = (int)(t / nblk);
+            const int64_t x0 = (int64_t)b * NP;
+            const int e = expert_of(a, x0);
+            const float *sb = a.sb + ((int64_t)e * nwt + wt) * KB;
+            float acc[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                acc[i] = 0.0f;
+            // lane c holds the scales of columns c and c + 32 of the next block
+            constexpr int kPer = (NP + 31) / 32;
+            float sx[kPer], sw = 0.0f;
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int64_t r = x0 + lane + 32 * i;
+                    sx[i] = lane + 32 * i < NP && r < a.M ? a.sa[r * a.sa_row + kb * a.sa_blk] : 0.0f;
+                }
+                sw = sb[kb];
+            };
+            if (kb0 < kb1)
+                fetch(kb0);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                float *f = sm.f[pw][kb & 1];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (lane + 32 * i < NP)
+                        f[lane + 32 * i] = sx[i] * sw;
+                if (kb + 1 < kb1)
+                    fetch(kb + 1);
+                const bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
+                if (!__all_sync(0xffffffffu, w_ok)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * NP;
+#pragma unroll
+                for (int c = 0; c < NP; c += 16) {
+                    float v[8], u[8];
+                    tmem_ld_nowait(tb + c, v);
+                    tmem_ld_nowait(tb + c + 8, u);
+                    tmem_wait_ld(v, u);
+                    const float4 *f4 = reinterpret_cast<const float4 *>(f + c);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 x = f4[i / 4], y = f4[2 + i / 4];
+                        ffma2v(acc[c + i], acc[c + i + 1], v[i], v[i + 1], x.x, x.y);
+                        ffma2v(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], x.z, x.w);
+                        ffma2v(acc[c + 8 + i], acc[c + 9 + i], u[i], u[i + 1], y.x, y.y);
+                        ffma2v(acc[c + 10 + i], acc[c + 11 + i], u[i + 2], u[i + 3], y.z, y.w);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.tempty[buf]);
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            auto store = [&](int c, int n, float v) {
+                if (x0 + c < rows && n < a.N) {
+                    const int64_t at = (x0 + c) * a.ld_d + n;
+                    if (a.out_f32)
+                        static_cast<float *>(a.d)[at] = v;
+                    else
+                        static_cast<__nv_bfloat16 *>(a.d)[at] = __float2bfloat16_rn(v);
+                }
+            };
+            if (S == 1) {
+#pragma unroll
+                for (int c = 0; c < NP; ++c)
+                    store(c, wt * 128 + row, acc[c]);
+                continue;
+            }
+            // CTA o of the cluster adds up the tile's rows [o * own, (o + 1) * own)
+            const int own = 128 / S, owner = row / own;
+            const bool free_ok = mbar_wait_cluster(&sm.red_free, rph ^ 1, a.status, abort_flag);
+            if (!__all_sync(0xffffffffu, free_ok)) {
+                ok = false;
+                break;
+            }
+            const uint32_t dst = cluster_map(sm.red, owner) + (uint32_t)((rank * NP * own + row % own) * 4);
+#pragma unroll
+            for (int c = 0; c < NP; ++c)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)(c * own * 4)), "f"(acc[c])
+                             : "memory");
+            __syncwarp();
+            if (lane == 0 || (own < 32 && lane == own))
+                mbar_arrive_cluster(cluster_map(&sm.red_full, owner));
+            const bool full_ok = mbar_wait_cluster(&sm.red_full, rph, a.status, abort_flag);
+            if (!__all_sync(0xffffffffu, full_ok)) {
+                ok = false;
+                break;
+            }
+            for (int i = pw * 32 + lane; i < own * NP; i += 128) {
+                float v = 0.0f;
+                for (int s2 = 0; s2 < S; ++s2)
+                    v += sm.red[s2 * NP * own + i];
+                store(i / own, wt * 128 + rank * own + i % own, v);
+            }
+            __syncwarp();
+            if (lane < S)
+                mbar_arrive_cluster(cluster_map(&sm.red_free, lane));
+            rph ^= 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (S > 1)
+        cluster_sync();  // no CTA leaves while a peer may still write to it
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, C::kTmem);
+}
+
+// ------------------------------------------------------------- launches
+
+template <int TN, bool WG>
+cudaError_t launch_many(const Args &a, int64_t max_tiles, int sms, cudaStream_t st)
+{
+    auto kern = gemm_block_kernel<TN, WG>;
+    constexpr size_t smem = sizeof(Smem<TN, WG>) + 1024;
+    static_assert(smem <= 227 * 1024, "a CTA has at most 227 KB of shared memory");
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    const int grid = (int)(max_tiles < sms ? max_tiles : sms);
+    return launch_kernel(false, kern, dim3(grid), dim3(kThreads), smem, st, a);
+}
+
+template <int NP>
+cudaError_t launch_few(const Args &a, int64_t max_tiles, int sms, cudaStream_t st)
+{
+    auto kern = gemm_block_few_kernel<NP>;
+    constexpr size_t smem = sizeof(FewSmem<NP>) + 1024;
+    static_assert(smem <= 227 * 1024, "a CTA has at most 227 KB of shared memory");
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    const int KB = (a.K + 127) / 128;
+    int S = 1;
+    while (S < 8 && max_tiles * 2 * S <= sms && KB / (2 * S) >= 4)
+        S *= 2;
+    const int64_t clusters = max_tiles < sms / S ? max_tiles : sms / S;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * S));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, S);
+}
+
+int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+}  // namespace blockgemm
+
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::blockgemm;
+
+extern "C" {
+
+int moe_gemm_fp8_block(const uint8_t *A, const float *a_scale, int a_scale_by_block, const uint8_t *B,
+                       const float *b_scale, int64_t M, int N, int K, int E, int block_m,
+                       const int32_t *sorted_expert_ids, const int32_t *num_tokens_post_padded, int out_type, void *D,
+                       int64_t ld_d, void *ws, size_t ws_bytes, void *stream)
+{
+    if (M < 0 || N <= 0 || K <= 0 || E <= 0 || !A || !a_scale || !B || !b_scale || !D || !ws || ld_d < N ||
+        a_scale_by_block < 0 || a_scale_by_block > 1 || (out_type != MOE_ROW_BF16 && out_type != MOE_ROW_FP32))
+        return MOE_ERR_INVALID_ARG;
+    const bool grouped = sorted_expert_ids != nullptr;
+    if (grouped != (num_tokens_post_padded != nullptr) || (!grouped && (E != 1 || block_m != 0)))
+        return MOE_ERR_INVALID_ARG;
+    const int es = out_type == MOE_ROW_FP32 ? 4 : 2;
+    if (misaligned(A, 16) || misaligned(B, 16) || misaligned(a_scale, 4) || misaligned(b_scale, 4) ||
+        misaligned(D, es) || misaligned(ws, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (K % 16 != 0 || K > 1 << 20 || N > 1 << 24 || (int64_t)E * N > 1 << 30 || M > 1 << 30)
+        return MOE_ERR_UNSUPPORTED;
+    if (grouped && block_m != 16 && block_m != 32 && block_m != 64 && (block_m <= 0 || block_m % 128 != 0))
+        return MOE_ERR_UNSUPPORTED;
+    if (ws_bytes < MOE_GEMM_BLOCK_WS_BYTES)
+        return MOE_ERR_WORKSPACE;
+    if (M == 0)
+        return MOE_OK;
+    const int sms = num_sms_current_device();
+    if (sms <= 0)
+        return MOE_ERR_CUDA;
+    Args a = {};
+    const int KB = (K + 127) / 128;
+    a.sa = a_scale;
+    a.sa_row = a_scale_by_block ? 1 : KB;
+    a.sa_blk = a_scale_by_block ? M : 1;
+    a.sb = b_scale;
+    a.expert_ids = sorted_expert_ids;
+    a.npp = num_tokens_post_padded;
+    a.M = M, a.N = N, a.K = K, a.E = E, a.block_m = grouped ? block_m : 128;
+    a.d = D, a.ld_d = ld_d, a.out_f32 = out_type == MOE_ROW_FP32;
+    a.wide = ((reinterpret_cast<uintptr_t>(D) | (uintptr_t)(ld_d * es) | (uintptr_t)((int64_t)N * es)) & 15) == 0;
+    a.status = static_cast<int *>(ws);
+    const auto st = static_cast<cudaStream_t>(stream);
+    const int few = grouped ? (block_m < 128 ? block_m : 0) : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 0;
+    const int64_t nmt = (M + 127) / 128;
+    // the widest column tile that still gives every SM a tile
+    const int tn = few ? 128 : nmt * ((N + 255) / 256) >= sms ? 256 : nmt * ((N + 127) / 128) >= sms ? 128 : 64;
+    if (!encode_tmap_2d(&a.tm_a, A, 1, K, M, 128, few ? few : 128) ||
+        !encode_tmap_2d(&a.tm_b, B, 1, K, (uint64_t)E * N, 128, tn < 128 ? tn : 128))
+        return MOE_ERR_CUDA;
+    if (few) {
+        const int64_t tiles = (M + few - 1) / few * ((N + 127) / 128);
+        return to_status(few == 16   ? launch_few<16>(a, tiles, sms, st)
+                         : few == 32 ? launch_few<32>(a, tiles, sms, st)
+                                     : launch_few<64>(a, tiles, sms, st));
+    }
+    const int64_t tiles = nmt * ((N + tn - 1) / tn);
+    return to_status(tn == 256   ? launch_many<256, false>(a, tiles, sms, st)
+                     : tn == 128 ? launch_many<128, false>(a, tiles, sms, st)
+                                 : launch_many<64, false>(a, tiles, sms, st));
+}
+
+int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B, const float *b_scale, int64_t P,
+                        int M, int N, int E, const int32_t *expert_counts, float *D, int accumulate, void *ws,
+                        size_t ws_bytes, void *stream)
+{
+    if (P < 0 || M <= 0 || N <= 0 || E <= 0 || !A || !a_scale || !B || !b_scale || !D || !ws || accumulate < 0 ||
+        accumulate > 1 || (!expert_counts && E != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (misaligned(A, 16) || misaligned(B, 16) || misaligned(a_scale, 4) || misaligned(b_scale, 16) ||
+        misaligned(D, 4) || misaligned(ws, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (E > kMaxE || P % 128 != 0 || N % 4 != 0 || P > 1 << 30 || M > 1 << 24 || N > 1 << 24)
+        return MOE_ERR_UNSUPPORTED;
+    if (ws_bytes < MOE_GEMM_BLOCK_WS_BYTES)
+        return MOE_ERR_WORKSPACE;
+    const int sms = num_sms_current_device();
+    if (sms <= 0)
+        return MOE_ERR_CUDA;
+    Args a = {};
+    a.sa = a_scale, a.sa_row = 1, a.sa_blk = M;
+    a.sb = b_scale;
+    a.counts = expert_counts;
+    a.M = M, a.N = N, a.K = (int)P, a.E = E;
+    a.d = D, a.ld_d = N, a.out_f32 = 1, a.accumulate = accumulate;
+    a.wide = !misaligned(D, 16);
+    a.status = static_cast<int *>(ws);
+    const auto st = static_cast<cudaStream_t>(stream);
+    const int64_t nmt = ((int64_t)M + 127) / 128;
+    const int tn = nmt * ((N + 255) / 256) * E >= sms ? 256 : nmt * ((N + 127) / 128) * E >= sms ? 128 : 64;
+    // P = 0: no block to read (the maps need at least one row)
+    const uint64_t inner = P > 0 ? P : 128;
+    if (!encode_tmap_2d(&a.tm_a, A, 1, inner, M, 128, 128) ||
+        !encode_tmap_2d(&a.tm_b, B, 1, inner, N, 128, tn < 128 ? tn : 128))
+        return MOE_ERR_CUDA;
+    const int64_t tiles = nmt * ((N + tn - 1) / tn) * E;
+    return to_status(tn == 256   ? launch_many<256, true>(a, tiles, sms, st)
+                     : tn == 128 ? launch_many<128, true>(a, tiles, sms, st)
+                                 : launch_many<64, true>(a, tiles, sms, st));
+}
+
+}  // extern "C"

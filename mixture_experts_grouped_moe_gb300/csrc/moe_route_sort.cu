@@ -829,6 +829,8 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t *__restr
         s_ids[e] = ids[e];
         s_w[e] = wts[e];  // staged so the per-expert scatter below waits on no global load
         bad_id = (unsigned)s_ids[e] >= (unsigned)E;
+        if (bad_id && o.slot_pos)
+            o.slot_pos[e] = -1;
     }
     // an id outside [0, E) matches no expert below, so its slot is left out; it is reported
     // through num_post_padded = -1
@@ -898,7 +900,10 @@ __global__ void __launch_bounds__(256) sort_few_kernel(const int32_t *__restrict
     for (int i = threadIdx.x; i < S; i += blockDim.x) {
         s_ids[i] = ids[i];
         s_w[i] = wts[i];
-        bad_id |= (unsigned)s_ids[i] >= (unsigned)E;  // matches no expert below: left out, reported
+        const bool bad = (unsigned)s_ids[i] >= (unsigned)E;  // matches no expert below: left out, reported
+        if (bad && o.slot_pos)
+            o.slot_pos[i] = -1;
+        bad_id |= bad;
     }
     const bool any_bad = __syncthreads_or(bad_id);
     if (threadIdx.x < 32) {
@@ -1081,6 +1086,8 @@ __global__ void __launch_bounds__(1024) sort_scatter_kernel(const int32_t *__res
         o.sorted_weights[pos] = wts[s];
         if (o.slot_pos)
             o.slot_pos[s] = pos;
+    } else if (s < S && o.slot_pos) {
+        o.slot_pos[s] = -1;
     }
 }
 

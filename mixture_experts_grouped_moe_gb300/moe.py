@@ -28,6 +28,15 @@ MOE_MXFP4 = 3
 MOE_MODE_GROUPED = 0
 MOE_MODE_SWAP = 1
 
+MOE_ROW_BF16 = 0
+MOE_ROW_FP16 = 1
+MOE_ROW_FP32 = 2
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+MOE_GEMM_BLOCK_WS_BYTES = 64
+
 EXPORTED = [
     "moe_status_string", "moe_version", "moe_align_sort_sizes", "moe_block_size_m_heuristic",
     "moe_ksplit_heuristic", "moe_plan", "moe_fused_workspace_size", "moe_workspace_layout",
@@ -35,7 +44,9 @@ EXPORTED = [
     "moe_quantize_fp8_act", "moe_quantize_fp8_weights", "moe_quantize_fp8_rows", "moe_fused_forward",
     "moe_host_staging_bytes", "moe_fused_forward_host", "moe_align_sort_noalloc", "moe_quantize_mxfp4",
     "moe_train_workspace_size", "moe_fused_forward_train", "moe_fused_backward", "moe_options_init",
-    "moe_fused_forward_ex",
+    "moe_fused_forward_ex", "moe_align_sort_map", "moe_permute", "moe_permute_fp8", "moe_permute_backward",
+    "moe_unpermute", "moe_unpermute_backward", "moe_gemm_fp8_block", "moe_wgrad_fp8_block",
+    "moe_quantize_fp8_act_t", "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
 ]
 
 
@@ -84,7 +95,7 @@ def load(build_if_missing: bool = False):
                                    "(run mixture_experts_grouped_moe_gb300.build.build())")
             _build.build()
         lib = ctypes.CDLL(_build.LIB)
-        P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+        P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         sig = {
             "moe_status_string": (ctypes.c_char_p, [I]),
             "moe_version": (I, []),
@@ -111,6 +122,18 @@ def load(build_if_missing: bool = False):
             "moe_fused_backward": (I, [P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, SZ, P, P]),
             "moe_quantize_mxfp4": (I, [P, I64, I, P, P, I, P]),
             "moe_align_sort_noalloc": (I, [P, P, I, I, I, I, P, P, P, P, P, P]),
+            "moe_align_sort_map": (I, [P, P, I, I, I, I, P, P, P, P, P, P, P, SZ, P]),
+            "moe_permute": (I, [I, P, I64, P, P, P, I, I, I, I64, I, P, P]),
+            "moe_permute_fp8": (I, [P, I64, P, P, P, I, I, I, I64, I, P, P, P]),
+            "moe_permute_backward": (I, [I, P, P, I, I, I, I64, P, I64, P]),
+            "moe_unpermute": (I, [I, P, P, P, I, I, I, I64, P, I64, P]),
+            "moe_unpermute_backward": (I, [I, P, I64, P, P, P, P, P, I, I, I, I64, I, P, P, P]),
+            "moe_gemm_fp8_block": (I, [P, P, I, P, P, I64, I, I, I, I, P, P, I, P, I64, P, SZ, P]),
+            "moe_wgrad_fp8_block": (I, [P, P, P, P, I64, I, I, I, P, P, I, P, SZ, P]),
+            "moe_quantize_fp8_act_t": (I, [P, I64, I64, I, P, I, I, P, P, I64, P, P]),
+            "moe_block_norm": (I, [I, P, P, P, I, P, P, I64, I, F, F, F, P, P, P, P, P]),
+            "moe_block_norm_workspace_size": (SZ, [I64, I]),
+            "moe_block_norm_backward": (I, [I, P, P, P, I, P, P, P, P, P, P, I64, I, F, F, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -324,6 +347,85 @@ def moe_fused_backward(x, W_router, router_bias, W_gate_up, W_down, dout, T, H, 
         _p(dW_gate_up), _p(dW_down), _p(dW_router), _p(dbias), _p(ws), ws_bytes, _opt(options), _stream(stream)))
 
 
+# ------------------------------------------------- operators around the layer
+
+def moe_align_sort_map(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
+                       num_tokens_post_padded, expert_counts, slot_pos, ws, ws_bytes, stream=None):
+    """moe_align_sort that also writes slot_pos, the sorted position of each slot."""
+    return _check("moe_align_sort_map", load().moe_align_sort_map(
+        _p(topk_ids), _p(topk_weights), T, k, E, block_m, _p(sorted_ids), _p(sorted_weights),
+        _p(sorted_expert_ids), _p(num_tokens_post_padded), _p(expert_counts), _p(slot_pos), _p(ws), ws_bytes,
+        _stream(stream)))
+
+
+def moe_permute(row_type, x, ld_x, slot_pos, sorted_ids, num_tokens_post_padded, T, k, H, P, zero_padding, xs,
+                stream=None):
+    return _check("moe_permute", load().moe_permute(
+        row_type, _p(x), ld_x, _p(slot_pos), _p(sorted_ids), _p(num_tokens_post_padded), T, k, H, P, zero_padding,
+        _p(xs), _stream(stream)))
+
+
+def moe_permute_fp8(x, ld_x, slot_pos, sorted_ids, num_tokens_post_padded, T, k, H, P, zero_padding, q, s,
+                    stream=None):
+    return _check("moe_permute_fp8", load().moe_permute_fp8(
+        _p(x), ld_x, _p(slot_pos), _p(sorted_ids), _p(num_tokens_post_padded), T, k, H, P, zero_padding, _p(q), _p(s),
+        _stream(stream)))
+
+
+def moe_permute_backward(row_type, dxs, slot_pos, T, k, H, P, dx, ld_dx, stream=None):
+    return _check("moe_permute_backward", load().moe_permute_backward(
+        row_type, _p(dxs), _p(slot_pos), T, k, H, P, _p(dx), ld_dx, _stream(stream)))
+
+
+def moe_unpermute(row_type, ys, slot_pos, topk_weights, T, k, H, P, out, ld_out, stream=None):
+    return _check("moe_unpermute", load().moe_unpermute(
+        row_type, _p(ys), _p(slot_pos), _p(topk_weights), T, k, H, P, _p(out), ld_out, _stream(stream)))
+
+
+def moe_unpermute_backward(row_type, dout, ld_dout, ys, slot_pos, topk_weights, sorted_ids, num_tokens_post_padded,
+                           T, k, H, P, zero_padding, dys, dweights, stream=None):
+    return _check("moe_unpermute_backward", load().moe_unpermute_backward(
+        row_type, _p(dout), ld_dout, _p(ys), _p(slot_pos), _p(topk_weights), _p(sorted_ids),
+        _p(num_tokens_post_padded), T, k, H, P, zero_padding, _p(dys), _p(dweights), _stream(stream)))
+
+
+def moe_gemm_fp8_block(A, a_scale, a_scale_by_block, B, b_scale, M, N, K, E, block_m, sorted_expert_ids,
+                       num_tokens_post_padded, out_type, D, ld_d, ws, ws_bytes, stream=None):
+    return _check("moe_gemm_fp8_block", load().moe_gemm_fp8_block(
+        _p(A), _p(a_scale), a_scale_by_block, _p(B), _p(b_scale), M, N, K, E, block_m, _p(sorted_expert_ids),
+        _p(num_tokens_post_padded), out_type, _p(D), ld_d, _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_wgrad_fp8_block(A, a_scale, B, b_scale, P, M, N, E, expert_counts, D, accumulate, ws, ws_bytes, stream=None):
+    return _check("moe_wgrad_fp8_block", load().moe_wgrad_fp8_block(
+        _p(A), _p(a_scale), _p(B), _p(b_scale), P, M, N, E, _p(expert_counts), _p(D), accumulate, _p(ws), ws_bytes,
+        _stream(stream)))
+
+
+def moe_quantize_fp8_act_t(X, ld_x, R, C, sorted_ids, S, k, num_rows, q, ld_q, s, stream=None):
+    return _check("moe_quantize_fp8_act_t", load().moe_quantize_fp8_act_t(
+        _p(X), ld_x, R, C, _p(sorted_ids), S, k, _p(num_rows), _p(q), ld_q, _p(s), _stream(stream)))
+
+
+def moe_block_norm(row_type, h, residual, gate, gate_kind, w_post, w_pre, T, H, scale, weight_offset, eps, y, z,
+                   rstd_h, rstd_y, stream=None):
+    return _check("moe_block_norm", load().moe_block_norm(
+        row_type, _p(h), _p(residual), _p(gate), gate_kind, _p(w_post), _p(w_pre), T, H, scale, weight_offset, eps,
+        _p(y), _p(z), _p(rstd_h), _p(rstd_y), _stream(stream)))
+
+
+def moe_block_norm_workspace_size(T, H) -> int:
+    return load().moe_block_norm_workspace_size(T, H)
+
+
+def moe_block_norm_backward(row_type, h, residual, gate, gate_kind, w_post, w_pre, rstd_h, rstd_y, dy, dz, T, H, scale,
+                            weight_offset, d_residual, dh, dgate, dw_post, dw_pre, ws, ws_bytes, stream=None):
+    return _check("moe_block_norm_backward", load().moe_block_norm_backward(
+        row_type, _p(h), _p(residual), _p(gate), gate_kind, _p(w_post), _p(w_pre), _p(rstd_h), _p(rstd_y), _p(dy), _p(dz),
+        T, H, scale, weight_offset, _p(d_residual), _p(dh), _p(dgate), _p(dw_post), _p(dw_pre), _p(ws), ws_bytes,
+        _stream(stream)))
+
+
 class MoETrain:
     """Owns the training workspace of one bf16 layer shape: forward(), then backward()."""
 
@@ -360,6 +462,100 @@ class MoETrain:
 
 
 # ------------------------------------------------------------- conveniences
+
+def _row_type(dtype):
+    import torch
+    return {torch.bfloat16: MOE_ROW_BF16, torch.float16: MOE_ROW_FP16, torch.float32: MOE_ROW_FP32}[dtype]
+
+
+class TokenExchange:
+    """Owns the maps of one routing shape (T tokens, k of E experts, blocks of block_m rows): sort(),
+    then rows to the experts' order and back, with gradients.
+
+    After sort(): sorted_ids, sorted_weights, expert_ids, num_tokens_post_padded, expert_counts and
+    slot_pos (see moe_align_sort_map in include/moe.h); P is the number of sorted rows to allocate.
+    """
+
+    def __init__(self, T, k, E, block_m=128, device="cuda"):
+        import torch
+        self.T, self.k, self.E, self.block_m = T, k, E, block_m
+        self.P, nb = moe_align_sort_sizes(T, k, E, block_m)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.sorted_ids, self.slot_pos = torch.empty(self.P, **i32), torch.empty(T * k, **i32)
+        self.expert_ids, self.expert_counts = torch.empty(nb, **i32), torch.empty(E, **i32)
+        self.num_tokens_post_padded = torch.empty(1, **i32)
+        self.sorted_weights = torch.empty(self.P, dtype=torch.float32, device=device)
+        self.ws_bytes = moe_align_sort_workspace_size(T, k, E)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.weights = None
+
+    def sort(self, topk_ids, topk_weights, stream=None):
+        moe_align_sort_map(topk_ids, topk_weights, self.T, self.k, self.E, self.block_m, self.sorted_ids,
+                           self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
+                           self.slot_pos, self.ws, self.ws_bytes, stream)
+        self.weights = topk_weights
+
+    def _rows(self, x):
+        if x.dim() != 2 or x.shape[0] != self.T or x.stride(1) != 1:
+            raise ValueError(f"expected {self.T} rows with contiguous elements, got {tuple(x.shape)}")
+        return x.shape[1], x.stride(0)
+
+    def _sorted(self, ys):
+        if ys.dim() != 2 or ys.shape[0] != self.P or not ys.is_contiguous():
+            raise ValueError(f"expected {self.P} contiguous sorted rows, got {tuple(ys.shape)}")
+        return ys.shape[1]
+
+    def permute(self, x, xs=None, zero_padding=True, stream=None):
+        """x [T][H] -> sorted rows [P][H]."""
+        import torch
+        H, ld = self._rows(x)
+        xs = torch.empty(self.P, H, dtype=x.dtype, device=x.device) if xs is None else xs
+        self._sorted(xs)
+        moe_permute(_row_type(x.dtype), x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T,
+                    self.k, H, self.P, int(zero_padding), xs, stream)
+        return xs
+
+    def permute_fp8(self, x, q=None, s=None, zero_padding=True, stream=None):
+        """x [T][H] bf16 -> e4m3 codes [P][H] (uint8) and scales by block [H/128][P]."""
+        import torch
+        H, ld = self._rows(x)
+        if x.dtype != torch.bfloat16:
+            raise TypeError("permute_fp8 takes bf16 rows")
+        q = torch.empty(self.P, H, dtype=torch.uint8, device=x.device) if q is None else q
+        s = torch.empty(H // 128, self.P, dtype=torch.float32, device=x.device) if s is None else s
+        moe_permute_fp8(x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T, self.k, H, self.P,
+                        int(zero_padding), q, s, stream)
+        return q, s
+
+    def unpermute(self, ys, out=None, weights=True, stream=None):
+        """Sorted rows [P][H] -> [T][H], each token's rows summed with its top-k weights (or 1)."""
+        import torch
+        H = self._sorted(ys)
+        out = torch.empty(self.T, H, dtype=ys.dtype, device=ys.device) if out is None else out
+        moe_unpermute(_row_type(ys.dtype), ys, self.slot_pos, self.weights if weights else None, self.T, self.k, H,
+                      self.P, out, self._rows(out)[1], stream)
+        return out
+
+    def unpermute_backward(self, dout, ys, zero_padding=True, stream=None):
+        """Gradients of unpermute: (dys [P][H], dweights [T][k] fp32)."""
+        import torch
+        H, ld = self._rows(dout)
+        self._sorted(ys)
+        dys = torch.empty_like(ys)
+        dw = torch.empty(self.T, self.k, dtype=torch.float32, device=ys.device)
+        moe_unpermute_backward(_row_type(ys.dtype), dout, ld, ys, self.slot_pos, self.weights, self.sorted_ids,
+                               self.num_tokens_post_padded, self.T, self.k, H, self.P, int(zero_padding), dys, dw,
+                               stream)
+        return dys, dw
+
+    def permute_backward(self, dxs, dx=None, stream=None):
+        """Gradient of permute: sorted rows [P][H] -> [T][H]."""
+        import torch
+        H = self._sorted(dxs)
+        dx = torch.empty(self.T, H, dtype=dxs.dtype, device=dxs.device) if dx is None else dx
+        moe_permute_backward(_row_type(dxs.dtype), dxs, self.slot_pos, self.T, self.k, H, self.P, dx,
+                             self._rows(dx)[1], stream)
+        return dx
 
 class FusedMoE:
     """Owns the workspace for one layer shape and calls moe_fused_forward.
