@@ -86,6 +86,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -152,11 +154,22 @@ def _p(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # () -> cudaStream_t of the current device's current stream
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if get is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            # without building a Stream object: 3.0 -> 0.4 us of every call's host time
+            _raw_stream = lambda: get(torch.cuda.current_device())  # noqa: E731
+    return _raw_stream()
 
 
 def _check(fn, rc):
