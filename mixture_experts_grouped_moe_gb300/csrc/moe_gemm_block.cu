@@ -34,7 +34,7 @@ struct Args {
     void *d;
     int64_t ld_d;
     int out_f32, accumulate;
-    int wide;  // rows of D start and end on 16-byte boundaries
+    int wide;  // rows of D start and end on 16-byte (wgrad: 32-byte) boundaries
     int *status;
 };
 
@@ -67,10 +67,82 @@ __device__ __forceinline__ void ffma2v(float &acc0, float &acc1, float v0, float
         : "f"(v0), "f"(v1), "f"(f0), "f"(f1));
 }
 
+// (acc0, acc1) += ((v0, v1) * (s0, s1)) * f, in pairs of fp32.
+__device__ __forceinline__ void scaled_ffma2(float &acc0, float &acc1, float v0, float v1, float2 s, float f)
+{
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 d, {%6, %6};\n\t"
+        "mov.b64 c, {%0, %1};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\t"
+        "fma.rn.f32x2 c, a, d, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(acc0), "+f"(acc1)
+        : "f"(v0), "f"(v1), "f"(s.x), "f"(s.y), "f"(f));
+}
+
+// 32 lanes x 32 columns of TMEM as two 16-lane halves, and the wait for them.  Lane l of the warp gets
+// of half h (v: TMEM lanes 0-15 from taddr on, u: lanes 16-31), group g of 8 columns: elements 4 g, 4 g + 1
+// at (row l / 4, columns 8 g + 2 (l % 4) and the next), 4 g + 2, 4 g + 3 eight rows below.
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&v)[16], float (&u)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15},"
+        " [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
+        " [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7]),
+          "=f"(u[8]), "=f"(u[9]), "=f"(u[10]), "=f"(u[11]), "=f"(u[12]), "=f"(u[13]), "=f"(u[14]), "=f"(u[15])
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
+}
+
+// Among the four lanes that share lane / 4: x[j] of lane l becomes x[l % 4] of lane j.
+__device__ __forceinline__ void transpose4(float2 (&x)[4], int lane)
+{
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = lane & b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (!(j & b)) {
+                const float2 give = up ? x[j] : x[j + b];
+                const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, give.x, b),
+                                               __shfl_xor_sync(0xffffffffu, give.y, b));
+                if (up)
+                    x[j] = got;
+                else
+                    x[j + b] = got;
+            }
+    }
+}
+
+// Eight floats to a 32-byte boundary in one store (or added to what is there).
+__device__ __forceinline__ void store8(float *d, float2 (&x)[4], int accumulate)
+{
+    if (accumulate) {
+        const float4 p = reinterpret_cast<const float4 *>(d)[0], q = reinterpret_cast<const float4 *>(d)[1];
+        x[0].x += p.x, x[0].y += p.y, x[1].x += p.z, x[1].y += p.w;
+        x[2].x += q.x, x[2].y += q.y, x[3].x += q.z, x[3].y += q.w;
+    }
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(x[0].x), "f"(x[0].y),
+                 "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y)
+                 : "memory");
+}
+
 // ------------------------------------------------------------ many rows
 //
-// A tile is 128 rows of A x TN rows of B.  Warps: 0 TMA producer, 1 TMEM allocation and MMA issue,
-// 2..9 promotion and epilogue (two per TMEM lane quadrant, half of the columns each).
+// A tile is 128 rows of A x TN rows of B.  Warps: 0 TMA producer, 1 TMEM allocation and MMA issue, then
+// eight for promotion and epilogue (two per TMEM lane quadrant, half of the columns each).  A weight
+// gradient has a second warp that copies the scales and a spare one (so that the promotion warps start
+// a group of four), and its first four warps hand registers to the other eight (setmaxnreg): 128
+// threads x 56 + 256 x 224 = 64512 = 384 x 168, all that the block is launched with.
 
 template <int TN, bool WG>
 struct Cfg {
@@ -78,11 +150,15 @@ struct Cfg {
     static constexpr int kABytes = 128 * 128, kBBytes = TN * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBufs = TN == 256 ? 2 : 4;  // TMEM accumulators
-    static constexpr int kScaleSlots = WG ? 4 : 1;
+    static constexpr int kScaleSlots = WG ? 8 : 1;
+    static constexpr int kFirstPromo = WG ? 4 : 2;
+    static constexpr int kThreads = 32 * (kFirstPromo + 8);
+    static constexpr int kSlot = WG ? 128 + TN : 4;  // floats: the rows' scales, then the columns'
 };
 
 constexpr int kPromoWarps = 8;
-constexpr int kThreads = 64 + 32 * kPromoWarps;
+constexpr int kFewRegs = 56, kPromoRegs = 224;
+static_assert(128 * kFewRegs + 32 * kPromoWarps * kPromoRegs <= 384 * 168, "within the launch's registers");
 constexpr int kGroupM = 16;  // row tiles that walk the column tiles together
 constexpr int kMaxE = 1024;
 
@@ -90,8 +166,8 @@ template <int TN, bool WG>
 struct __align__(1024) Smem {
     using C = Cfg<TN, WG>;
     uint8_t stage[C::kStages][C::kStageBytes];
-    float sb[C::kScaleSlots][WG ? TN : 4];  // wgrad: the block's column scales
-    float4 ep_out[kPromoWarps][32][4];      // a warp's 32 rows x 64 bytes on their way to D
+    float scale[C::kScaleSlots][C::kSlot];
+    float4 ep_out[WG ? 1 : kPromoWarps][32][4];  // a warp's 32 rows x 64 bytes on their way to D
     uint64_t full[C::kStages], empty[C::kStages];
     uint64_t tfull[C::kBufs], tempty[C::kBufs];
     uint64_t sfull[C::kScaleSlots], sempty[C::kScaleSlots];
@@ -109,9 +185,10 @@ struct Tile {
 };
 
 template <int TN, bool WG>
-__global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, 1) gemm_block_kernel(const __grid_constant__ Args a)
 {
     using C = Cfg<TN, WG>;
+    constexpr int kFirstPromo = C::kFirstPromo;
     extern __shared__ uint8_t smem_raw[];
     auto &sm = *reinterpret_cast<Smem<TN, WG> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
             mbar_init(&sm.tempty[i], kPromoWarps);
         }
         for (int i = 0; i < C::kScaleSlots; ++i) {
-            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.sfull[i], 32);
             mbar_init(&sm.sempty[i], kPromoWarps);
         }
         mbar_init(&sm.drain, 1);
@@ -170,18 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
     const int64_t rows = rows_in_use(a);
     const int nmt = (int)((rows + 127) / 128);
     const int nnt = (a.N + TN - 1) / TN;
-    const int64_t ntiles = (int64_t)nmt * nnt * (WG ? a.E : 1);
+    const int ntiles = nmt * nnt * (WG ? a.E : 1);  // (the host checks that the count fits)
 
-    auto get_tile = [&](int64_t t) {
+    auto get_tile = [&](int t) {
         Tile tl;
-        int within = (int)(WG ? t % ((int64_t)nmt * nnt) : t);
+        int within = WG ? t % (nmt * nnt) : t;
         const int group = within / (kGroupM * nnt);
         within -= group * kGroupM * nnt;
         const int gsize = min(kGroupM, nmt - group * kGroupM);
         tl.row0 = (int64_t)(group * kGroupM + within % gsize) * 128;
         tl.col0 = within / gsize * TN;
         if (WG) {
-            tl.e = (int)(t / ((int64_t)nmt * nnt));
+            tl.e = t / (nmt * nnt);
             tl.kb0 = min(sm.off[tl.e], KB);
             tl.kb1 = min(sm.off[tl.e + 1], KB);
         } else {
@@ -192,16 +269,247 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
         return tl;
     };
 
+    if (warp >= kFirstPromo) {
+        if (WG)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoRegs));
+        const int q = warp & 3;                     // TMEM lane quadrant
+        const int sub = (warp - kFirstPromo) >> 2;  // half of the columns
+        constexpr int kCols = TN / 2;
+        constexpr int kLd = 16;  // TMEM columns per load, two loads per wait
+        const int row = q * 32 + lane;
+        int buf = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        if constexpr (WG) {
+            int ss = 0;
+            uint32_t sph = 0;
+            // Here every column has a scale of its own.  Read as one row a lane, each would be one more
+            // shared-memory pass per 32 products (1024 cycles a block, more than the copies and the
+            // tensor core take); in the 16 x 256-bit shape a lane holds 4 rows x 32 of the 128 columns,
+            // so it reads 32 column scales, and its pairs of columns leave as whole 32-byte sectors
+            // without passing through shared memory.
+            const int r0 = q * 32 + (lane >> 2), c2 = 2 * (lane & 3);
+            for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
+                const Tile tl = get_tile(t);
+                float acc[2][kCols / 2];  // [half][4 g + i]
+#pragma unroll
+                for (int i = 0; i < kCols / 2; ++i)
+                    acc[0][i] = acc[1][i] = 0.0f;
+                for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
+                    const bool s_ok = mbar_wait(&sm.sfull[ss], sph, a.status, abort_flag);
+                    const float *scale = sm.scale[ss];
+                    float f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = scale[r0 + 8 * i];
+                    const float2 *s2 = reinterpret_cast<const float2 *>(scale + 128 + sub * kCols + c2);
+                    const bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
+                    if (!__all_sync(0xffffffffu, w_ok && s_ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * TN + sub * kCols;
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) {
+                        float v[16], u[16];
+                        float2 x[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            x[g] = s2[(c + 8 * g) / 2];
+                        tmem_ld_halves(tb + c, v, u);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int i = 4 * g, o = c / 2 + i;
+                            scaled_ffma2(acc[0][o], acc[0][o + 1], v[i], v[i + 1], x[g], f[0]);
+                            scaled_ffma2(acc[0][o + 2], acc[0][o + 3], v[i + 2], v[i + 3], x[g], f[1]);
+                            scaled_ffma2(acc[1][o], acc[1][o + 1], u[i], u[i + 1], x[g], f[2]);
+                            scaled_ffma2(acc[1][o + 2], acc[1][o + 3], u[i + 2], u[i + 3], x[g], f[3]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.tempty[buf]);
+                        mbar_arrive(&sm.sempty[ss]);
+                    }
+                    if (++buf == C::kBufs) {
+                        buf = 0;
+                        bph ^= 1;
+                    }
+                    if (++ss == C::kScaleSlots) {
+                        ss = 0;
+                        sph ^= 1;
+                    }
+                }
+                if (!ok)
+                    break;
+                const int n0 = tl.col0 + sub * kCols;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t r = tl.row0 + r0 + 8 * i;
+                    float *d = static_cast<float *>(a.d) + ((int64_t)tl.e * a.M + r) * a.N;
+#pragma unroll
+                    for (int g = 0; g < kCols / 8; g += 4) {
+                        float2 x[4];  // columns 8 (g + j) + c2 and the next of row r
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = make_float2(acc[i / 2][4 * (g + j) + 2 * (i & 1)],
+                                               acc[i / 2][4 * (g + j) + 2 * (i & 1) + 1]);
+                        if (a.wide) {  // (the same for every lane)
+                            transpose4(x, lane);  // now the 8 columns of group g + lane % 4
+                            const int n = n0 + 8 * (g + (lane & 3));
+                            if (r < a.M && n < a.N)
+                                store8(d + n, x, a.accumulate);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int n = n0 + 8 * (g + j) + c2;
+                                if (r < a.M && n < a.N) {  // (N % 4 == 0: a pair of columns is in or out)
+                                    d[n] = a.accumulate ? d[n] + x[j].x : x[j].x;
+                                    d[n + 1] = a.accumulate ? d[n + 1] + x[j].y : x[j].y;
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+        } else {
+        const int nsb = (a.N + 127) / 128;
+        for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
+            const float *sa, *sb;
+            {
+                const Tile tl = get_tile(t);
+                const int64_t grow = tl.row0 + row;
+                sa = a.sa + (grow < a.M ? grow : a.M - 1) * a.sa_row;  // a row past M is never stored
+                const int nb = min((tl.col0 + sub * kCols) / 128, nsb - 1);
+                sb = a.sb + ((int64_t)tl.e * nsb + nb) * KB;
+            }
+            float acc[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+                acc[i] = 0.0f;
+            float sa_n = __ldg(sa), sb_n = __ldg(sb);
+            for (int kb = 0; kb < KB; ++kb) {
+                const float f = sa_n * sb_n;
+                if (kb + 1 < KB) {  // fetched while this block is on the tensor core
+                    sa_n = __ldg(sa += a.sa_blk);
+                    sb_n = __ldg(++sb);
+                }
+                const bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
+                if (!__all_sync(0xffffffffu, w_ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * TN + sub * kCols;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2 * kLd) {
+                    float v[kLd], u[kLd];
+                    tmem_ld_nowait(tb + c, v);
+                    tmem_ld_nowait(tb + c + kLd, u);
+                    tmem_wait_ld(v, u);
+#pragma unroll
+                    for (int i = 0; i < kLd; i += 2) {
+                        ffma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
+                        ffma2(acc[c + kLd + i], acc[c + kLd + i + 1], u[i], u[i + 1], f);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.tempty[buf]);
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            asm volatile("" : "+r"(t));  // (the tile is formed again, not kept in registers over the K loop)
+            const Tile tl = get_tile(t);
+            // Each lane holds one row.  Pieces of 64 bytes a row go through a per-warp shared block
+            // (16-byte slot j of row r at j ^ ((r >> 1) & 3): no bank conflicts either way) and
+            // leave as 8 rows x 64 contiguous bytes per store: on the way out lane l holds 16 bytes
+            // at slot l % 4 of rows l / 4 + 8 i, whose addresses are formed once.
+            float4(*ep)[4] = sm.ep_out[warp - kFirstPromo];
+            const int rr = lane >> 2, cq = lane & 3;
+            const int n0 = tl.col0 + sub * kCols;
+            const int64_t left = a.M - tl.row0 - q * 32;  // rows of D from lane 0's
+            const int es = a.out_f32 ? 4 : 2, per = 16 / es;
+            uint8_t *dst[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = tl.row0 + q * 32 + 8 * i + rr;
+                dst[i] = 8 * i + rr < left ? static_cast<uint8_t *>(a.d) + (r * a.ld_d + n0 + per * cq) * es : nullptr;
+            }
+            const int n1 = n0 + per * cq;  // this lane's first column of a piece
+            auto flush = [&](int c) {      // the shared block holds columns n0 + c ..
+                __syncwarp();
+                if (a.wide) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 o = ep[8 * i + rr][cq ^ (((8 * i + rr) >> 1) & 3)];
+                        if (dst[i] && n1 + c < a.N)
+                            *reinterpret_cast<float4 *>(dst[i] + c * es) = o;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 o = ep[8 * i + rr][cq ^ (((8 * i + rr) >> 1) & 3)];
+                        if (8 * i + rr >= left)
+                            continue;
+                        uint8_t *d = dst[0] + (int64_t)8 * i * a.ld_d * es + c * es;
+                        const float e4[4] = {o.x, o.y, o.z, o.w};
+                        if (a.out_f32) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (n1 + c + j < a.N)
+                                    reinterpret_cast<float *>(d)[j] = e4[j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (n1 + c + j < a.N)
+                                    reinterpret_cast<uint16_t *>(d)[j] =
+                                        (uint16_t)(__float_as_uint(e4[j / 2]) >> (16 * (j & 1)));
+                        }
+                    }
+                }
+                __syncwarp();
+            };
+            if (a.out_f32) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ep[lane][j ^ ((lane >> 1) & 3)] =
+                            make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
+                    flush(c);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ep[lane][j ^ ((lane >> 1) & 3)] = pack_bf16x8(acc + c + 8 * j, 1.0f);
+                    flush(c);
+                }
+            }
+        }
+        }
+    } else {
+        if (WG)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_b = l2_policy_evict_normal();
             const uint64_t pol_a = l2_policy_evict_last();
-            int s = 0, ss = 0;
-            uint32_t ph = 0, sph = 0;
+            int s = 0;
+            uint32_t ph = 0;
             uint32_t issued = 0;  // stages with a copy issued, and its phase
             uint32_t issued_ph = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+            for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
                 const Tile tl = get_tile(t);
                 const int brow = WG ? tl.col0 : tl.e * a.N + tl.col0;
                 for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
@@ -218,19 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
                                     pol_b);
                     issued |= 1u << s;
                     issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
-                    if (WG) {
-                        if (!mbar_wait(&sm.sempty[ss], sph ^ 1, a.status, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bytes = (uint32_t)min(TN, a.N - tl.col0) * 4;
-                        mbar_arrive_expect_tx(&sm.sfull[ss], bytes);
-                        bulk_load(sm.sb[ss], a.sb + (int64_t)kb * a.N + tl.col0, bytes, &sm.sfull[ss]);
-                        if (++ss == C::kScaleSlots) {
-                            ss = 0;
-                            sph ^= 1;
-                        }
-                    }
                     if (++s == C::kStages) {
                         s = 0;
                         ph ^= 1;
@@ -245,11 +540,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
                                global_timer_ns() - t0 < 100000000ull) {
                         }
                     }
-                if (WG) {  // the scale copies, each 1 KB or less, given a bounded moment
-                    const unsigned long long t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 20000000ull) {
-                    }
-                }
             }
         }
     } else if (warp == 1) {
@@ -258,27 +548,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
             uint32_t ph = 0, bph = 0;
             bool ok = true, any = false;
             const uint32_t idesc = make_idesc(0, 0, 128, TN);
-            for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+            for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
                 const Tile tl = get_tile(t);
+                bool loaded = false;
                 for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
-                    if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag) ||
+                    if ((!loaded && !mbar_wait(&sm.full[s], ph, a.status, abort_flag)) ||
                         !mbar_wait(&sm.tempty[buf], bph ^ 1, a.status, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint8_t *as = sm.stage[s], *bs = sm.stage[s] + C::kABytes;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_fp8(tmem_base + buf * TN, smem_desc_sw128(as + kk * 32), smem_desc_sw128(bs + kk * 32),
-                                idesc, kk > 0 ? 1u : 0u);
-                    any = true;
-                    mma_commit(&sm.empty[s]);
-                    mma_commit(&sm.tfull[buf]);
+                    const int cur = s;
                     if (++s == C::kStages) {
                         s = 0;
                         ph ^= 1;
                     }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        // the next block's copies are looked at while the queue holds MMAs of this one
+                        if (kk == 2)
+                            loaded = kb + 1 < tl.kb1 && mbar_try_wait(&sm.full[s], ph);
+                        mma_fp8(tmem_base + buf * TN, smem_desc_sw128(as + kk * 32), smem_desc_sw128(bs + kk * 32),
+                                idesc, kk > 0 ? 1u : 0u);
+                    }
+                    any = true;
+                    mma_commit(&sm.tfull[buf]);
+                    mma_commit(&sm.empty[cur]);
                     if (++buf == C::kBufs) {
                         buf = 0;
                         bph ^= 1;
@@ -292,157 +588,44 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_block_kernel(const __grid_co
                 }
             }
         }
-    } else {
-        const int q = warp & 3;           // TMEM lane quadrant
-        const int sub = (warp - 2) >> 2;  // half of the columns
-        constexpr int kCols = TN / 2;
-        constexpr int kLd = kCols >= 32 ? 16 : 8;
-        const int row = q * 32 + lane;
-        int buf = 0, ss = 0;
-        uint32_t bph = 0, sph = 0;
+    } else if (WG && warp == 2) {
+        // Scales of each K block, copied ahead into a ring: fetched by the promotion warps a block
+        // ahead, their latency paced the K loop, where every block is a new line.
+        int ss = 0;
+        uint32_t sph = 0;
         bool ok = true;
-        const int nsb = (a.N + 127) / 128;
-        for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+        for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
             const Tile tl = get_tile(t);
-            const int64_t grow = tl.row0 + row;
-            const int64_t srow = grow < a.M ? grow : a.M - 1;  // a row past M is never stored
-            const float *sa = a.sa + srow * a.sa_row;
-            const int nb = min((tl.col0 + sub * kCols) / 128, nsb - 1);
-            const float *sb = WG ? nullptr : a.sb + ((int64_t)tl.e * nsb + nb) * KB;
-            float acc[kCols];
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-                acc[i] = 0.0f;
-            float sa_n = 0.0f, sb_n = 1.0f;
-            if (tl.kb0 < tl.kb1) {
-                sa_n = sa[tl.kb0 * a.sa_blk];
-                sb_n = WG ? 1.0f : sb[tl.kb0];
-            }
-            for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
-                const float f = sa_n * sb_n;
-                if (kb + 1 < tl.kb1) {  // fetched while this block is on the tensor core
-                    sa_n = sa[(kb + 1) * a.sa_blk];
-                    sb_n = WG ? 1.0f : sb[kb + 1];
-                }
-                bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
-                if (WG)
-                    w_ok = w_ok && mbar_wait(&sm.sfull[ss], sph, a.status, abort_flag);
-                if (!__all_sync(0xffffffffu, w_ok)) {
+            const float *sa = a.sa + (tl.row0 + lane) * a.sa_row + tl.kb0 * a.sa_blk;
+            const int left = (int)min((int64_t)128, a.M - tl.row0);
+            const float *sb = a.sb + tl.col0 + 4 * lane + (int64_t)tl.kb0 * a.N;
+            const int col = tl.col0 + 4 * lane;
+            for (int left_kb = tl.kb1 - tl.kb0; left_kb > 0; --left_kb) {
+                const bool e_ok = mbar_wait(&sm.sempty[ss], sph ^ 1, a.status, abort_flag);
+                if (!__all_sync(0xffffffffu, e_ok)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * TN + sub * kCols;
+                float *dst = sm.scale[ss];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 2 * kLd) {
-                    float v[kLd], u[kLd];
-                    tmem_ld_nowait(tb + c, v);
-                    tmem_ld_nowait(tb + c + kLd, u);
-                    tmem_wait_ld(v, u);
-                    if (WG) {
-                        const float4 *s4 = reinterpret_cast<const float4 *>(sm.sb[ss] + sub * kCols + c);
+                for (int i = 0; i < 4; ++i)
+                    if (lane + 32 * i < left)  // (rows past M are never stored)
+                        cp_async_4(dst + lane + 32 * i, sa + 32 * i * a.sa_row);
 #pragma unroll
-                        for (int i = 0; i < kLd; i += 4) {
-                            const float4 x = s4[i / 4], y = s4[(i + kLd) / 4];
-                            ffma2v(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f * x.x, f * x.y);
-                            ffma2v(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f * x.z, f * x.w);
-                            ffma2v(acc[c + kLd + i], acc[c + kLd + i + 1], u[i], u[i + 1], f * y.x, f * y.y);
-                            ffma2v(acc[c + kLd + i + 2], acc[c + kLd + i + 3], u[i + 2], u[i + 3], f * y.z, f * y.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kLd; i += 2) {
-                            ffma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
-                            ffma2(acc[c + kLd + i], acc[c + kLd + i + 1], u[i], u[i + 1], f);
-                        }
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.tempty[buf]);
-                    if (WG)
-                        mbar_arrive(&sm.sempty[ss]);
-                }
-                if (++buf == C::kBufs) {
-                    buf = 0;
-                    bph ^= 1;
-                }
-                if (WG && ++ss == C::kScaleSlots) {
+                for (int i = 0; i < (TN + 127) / 128; ++i)
+                    if (4 * lane + 128 * i < TN && col + 128 * i < a.N)  // (N % 4 == 0)
+                        cp_async_16_zfill(dst + 128 + 4 * lane + 128 * i, sb + 128 * i, true);
+                sa += a.sa_blk;
+                sb += a.N;
+                cp_async_arrive(&sm.sfull[ss]);
+                if (++ss == C::kScaleSlots) {
                     ss = 0;
                     sph ^= 1;
                 }
             }
-            if (!ok)
-                break;
-            // Each lane holds one row.  Pieces of 64 bytes a row go through a per-warp shared block
-            // (16-byte slot j of row r at j ^ ((r >> 1) & 3): no bank conflicts either way) and
-            // leave as 8 rows x 64 contiguous bytes per store.
-            float4(*ep)[4] = sm.ep_out[warp - 2];
-            const int rr = lane >> 2, cq = lane & 3;
-            const int n0 = tl.col0 + sub * kCols;
-            const int64_t base = (WG ? (int64_t)tl.e * a.M : 0) + tl.row0 + q * 32;  // D row of lane 0
-            const int64_t left = a.M - tl.row0 - q * 32;                             // rows of D from there
-            auto flush = [&](int col, int per) {  // columns col.. of D, `per` elements per 16 bytes
-                __syncwarp();
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const int r = 8 * it + rr;
-                    float4 o = ep[r][cq ^ ((r >> 1) & 3)];
-                    const int n = col + per * cq;
-                    if (r >= left || n >= a.N)
-                        continue;
-                    const int64_t at = (base + r) * a.ld_d + n;
-                    if (a.out_f32) {
-                        float *d = static_cast<float *>(a.d) + at;
-                        if (a.wide) {
-                            if (a.accumulate) {
-                                const float4 p = *reinterpret_cast<float4 *>(d);
-                                o = make_float4(o.x + p.x, o.y + p.y, o.z + p.z, o.w + p.w);
-                            }
-                            *reinterpret_cast<float4 *>(d) = o;
-                        } else {
-                            const float e4[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (n + i < a.N)
-                                    d[i] = a.accumulate ? d[i] + e4[i] : e4[i];
-                        }
-                    } else {
-                        __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.d) + at;
-                        if (a.wide) {
-                            *reinterpret_cast<float4 *>(d) = o;
-                        } else {
-                            const uint32_t e4[4] = {__float_as_uint(o.x), __float_as_uint(o.y), __float_as_uint(o.z),
-                                                    __float_as_uint(o.w)};
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (n + i < a.N)
-                                    reinterpret_cast<uint16_t *>(d)[i] = (uint16_t)(e4[i / 2] >> (16 * (i & 1)));
-                        }
-                    }
-                }
-                __syncwarp();
-            };
-            if (a.out_f32) {
-#pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ep[lane][j ^ ((lane >> 1) & 3)] =
-                            make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
-                    flush(n0 + c, 4);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ep[lane][j ^ ((lane >> 1) & 3)] = pack_bf16x8(acc + c + 8 * j, 1.0f);
-                    flush(n0 + c, 8);
-                }
-            }
         }
+        cp_async_wait_all();
+    }
     }
     tc_fence_before();
     __syncthreads();
@@ -742,7 +925,7 @@ cudaError_t launch_many(const Args &a, int64_t max_tiles, int sms, cudaStream_t 
     if (err != cudaSuccess)
         return err;
     const int grid = (int)(max_tiles < sms ? max_tiles : sms);
-    return launch_kernel(false, kern, dim3(grid), dim3(kThreads), smem, st, a);
+    return launch_kernel(false, kern, dim3(grid), dim3(Cfg<TN, WG>::kThreads), smem, st, a);
 }
 
 template <int NP>
@@ -840,6 +1023,8 @@ int moe_gemm_fp8_block(const uint8_t *A, const float *a_scale, int a_scale_by_bl
                                      : launch_few<64>(a, tiles, sms, st));
     }
     const int64_t tiles = nmt * ((N + tn - 1) / tn);
+    if (tiles > 1 << 30)
+        return MOE_ERR_UNSUPPORTED;
     return to_status(tn == 256   ? launch_many<256, false>(a, tiles, sms, st)
                      : tn == 128 ? launch_many<128, false>(a, tiles, sms, st)
                                  : launch_many<64, false>(a, tiles, sms, st));
@@ -868,7 +1053,7 @@ int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B
     a.counts = expert_counts;
     a.M = M, a.N = N, a.K = (int)P, a.E = E;
     a.d = D, a.ld_d = N, a.out_f32 = 1, a.accumulate = accumulate;
-    a.wide = !misaligned(D, 16);
+    a.wide = !misaligned(D, 32) && N % 8 == 0;
     a.status = static_cast<int *>(ws);
     const auto st = static_cast<cudaStream_t>(stream);
     const int64_t nmt = ((int64_t)M + 127) / 128;
@@ -879,6 +1064,8 @@ int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B
         !encode_tmap_2d(&a.tm_b, B, 1, inner, N, 128, tn < 128 ? tn : 128))
         return MOE_ERR_CUDA;
     const int64_t tiles = nmt * ((N + tn - 1) / tn) * E;
+    if (tiles > 1 << 30)
+        return MOE_ERR_UNSUPPORTED;
     return to_status(tn == 256   ? launch_many<256, true>(a, tiles, sms, st)
                      : tn == 128 ? launch_many<128, true>(a, tiles, sms, st)
                                  : launch_many<64, true>(a, tiles, sms, st));
