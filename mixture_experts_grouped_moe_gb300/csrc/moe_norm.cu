@@ -19,8 +19,14 @@
 // dgate) are
 // kept in registers over the rows that a block walks and written as one partial row per block;
 // a second launch adds the partial rows in order, so the gradients are bitwise reproducible.
+//
+// A row's two sums are a chain of barriers, so a block that loads its next row only after this one
+// leaves HBM idle most of the time.  The blocks are persistent and copy the next rows ahead into
+// shared memory (cp.async; each thread copies exactly the pieces that it will read itself, so no
+// barrier guards the ring): kAhead of them @MEASURE@.
 #include "moe_internal.h"
 #include "rows.cuh"
+#include "sm100_ptx.cuh"
 
 namespace moe {
 
@@ -41,7 +47,66 @@ struct NormArgs {
     // backward
     const void *dy, *dz;
     void *dres, *dh, *dgate;
-    float *part;  // [blocks][3][H]: dw_post, dw_pre, dgate (per column)
+    float *part;  // [blocks][2][H]: the blocks' column sums
+    int slots;    // rows of the ring in shared memory
+};
+
+// The rows that a block walks (blockIdx.x, + gridDim.x, ...), each of N arrays, a thread's pieces of
+// them.  RING: copied ahead into shared memory; otherwise loaded when wanted.
+template <typename V, int NV, int N, bool RING>
+struct RowRing {
+    const V *src[N];  // null: not read
+    V *ring;
+    int64_t T;
+    int units, slots, slot;
+
+    __device__ __forceinline__ void init(int64_t rows, int nunits, int nslots)
+    {
+        extern __shared__ __align__(16) uint8_t smem[];
+        ring = reinterpret_cast<V *>(smem);
+        T = rows, units = nunits, slots = nslots, slot = 0;
+        if (RING)
+            for (int i = 0; i < slots; ++i)
+                fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    }
+    __device__ __forceinline__ void fetch(int64_t t, int to)
+    {
+        if (t < T)
+#pragma unroll
+            for (int a = 0; a < N; ++a)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int u = threadIdx.x + i * blockDim.x;
+                    if (src[a] && u < units)
+                        cp_async_16_zfill(ring + (to * N + a) * units + u, src[a] + t * units + u, true);
+                }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Wait for this thread's pieces of the block's next row.
+    __device__ __forceinline__ void wait()
+    {
+        if (RING) {
+            if (slots == 2)  // every copy but the slots - 1 newer ones
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+        }
+    }
+    // Piece i of array a of that row (row t).
+    __device__ __forceinline__ V at(int64_t t, int a, int i) const
+    {
+        const int u = threadIdx.x + i * blockDim.x;
+        return RING ? ring[(slot * N + a) * units + u] : src[a][t * units + u];
+    }
+    // Row t's pieces have been read: its place takes the row `slots` further on.
+    __device__ __forceinline__ void next(int64_t t)
+    {
+        if (RING) {
+            fetch(t + (int64_t)slots * gridDim.x, slot);
+            if (++slot == slots)
+                slot = 0;
+        }
+    }
 };
 
 // Sum of v over the block's threads (every thread gets it); `buf` alternates between calls.
@@ -58,45 +123,61 @@ __device__ __forceinline__ float block_sum(float v, float (*buf)[kMaxWarps], int
     return warp_sum(s);
 }
 
-// Gate of element c of the piece (row t, piece u); gate pieces are loaded once per row or column.
+// The gate of a piece's elements (row t, piece u); row_gate where it is the same for the whole row.
 template <typename T, int VEC>
-__device__ __forceinline__ float gate_of(const NormArgs &a, float row_gate, const Piece<T, VEC> &g, int c)
-{
-    return a.gate_kind == MOE_GATE_NONE || a.gate_kind == MOE_GATE_TOKEN ? row_gate : row_to_f(g.e[c]);
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ Piece<T, VEC> gate_piece(const NormArgs &a, int64_t t, int units, int u)
+__device__ __forceinline__ void gate_piece(const NormArgs &a, int64_t t, int units, int u, float row_gate,
+                                           float (&g)[VEC])
 {
     using V = Piece<T, VEC>;
-    if (a.gate_kind == MOE_GATE_CHANNEL)
-        return static_cast<const V *>(a.gate)[u];
-    if (a.gate_kind == MOE_GATE_FULL)
-        return static_cast<const V *>(a.gate)[t * units + u];
-    return V{};
+    if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
+        const V p = static_cast<const V *>(a.gate)[a.gate_kind == MOE_GATE_FULL ? t * units + u : u];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            g[c] = row_to_f(p.e[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            g[c] = row_gate;
+    }
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a)
+// weight + offset of a piece's elements, 1 without a weight
+template <typename T, int VEC>
+__device__ __forceinline__ void weight_piece(const void *w, float offset, int u, float (&f)[VEC])
+{
+    using V = Piece<T, VEC>;
+    if (w) {
+        const V p = static_cast<const V *>(w)[u];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            f[c] = row_to_f(p.e[c]) + offset;
+    } else {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            f[c] = 1.0f;
+    }
+}
+
+template <typename T, int VEC, int NV, bool RING>
+__global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const NormArgs a)
 {
     using V = Piece<T, VEC>;
     __shared__ float s_buf[2][kMaxWarps];
     const int units = a.H / VEC;
     const float inv_h = 1.0f / (float)a.H;
+    RowRing<V, NV, 2, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.residual)}};
     pdl_wait();
+    in.init(a.T, units, a.slots);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const V *hr = static_cast<const V *>(a.h) + t * units;
-        const V *rr = static_cast<const V *>(a.residual) + t * units;
+        in.wait();
         V h[NV], r[NV];
-        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
-            if (u < units) {
-                h[i] = hr[u];
-                r[i] = rr[u];
+        for (int i = 0; i < NV; ++i)
+            if (threadIdx.x + i * blockDim.x < units) {
+                h[i] = in.at(t, 0, i);
+                r[i] = in.at(t, 1, i);
             }
-        }
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (threadIdx.x + i * blockDim.x < units)
@@ -109,6 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a)
         float r_h = 1.0f;
         if (a.w_post)
             r_h = rsqrtf(fmaf(block_sum(sum, s_buf, 0), inv_h, a.eps));
+        in.next(t);
         float y[NV][VEC];
         float ysum = 0.0f;
 #pragma unroll
@@ -116,15 +198,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a)
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
-            const V w = a.w_post ? static_cast<const V *>(a.w_post)[u] : V{};
-            const V g = gate_piece<T, VEC>(a, t, units, u);
+            float w[VEC], g[VEC];
+            weight_piece<T, VEC>(a.w_post, a.offset, u, w);
+            gate_piece<T, VEC>(a, t, units, u, row_gate, g);
             V o;
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                float n = row_to_f(h[i].e[c]);
-                if (a.w_post)
-                    n = n * r_h * (row_to_f(w.e[c]) + a.offset);
-                y[i][c] = fmaf(a.scale * gate_of<T, VEC>(a, row_gate, g, c), n, row_to_f(r[i].e[c]));
+                y[i][c] = fmaf(a.scale * g[c] * w[c], row_to_f(h[i].e[c]) * r_h, row_to_f(r[i].e[c]));
                 ysum = fmaf(y[i][c], y[i][c], ysum);
                 o.e[c] = row_from_f<T>(y[i][c]);
             }
@@ -139,11 +219,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a)
                 const int u = threadIdx.x + i * blockDim.x;
                 if (u >= units)
                     continue;
-                const V w = static_cast<const V *>(a.w_pre)[u];
+                float w[VEC];
+                weight_piece<T, VEC>(a.w_pre, a.offset, u, w);
                 V o;
 #pragma unroll
                 for (int c = 0; c < VEC; ++c)
-                    o.e[c] = row_from_f<T>(y[i][c] * r_y * (row_to_f(w.e[c]) + a.offset));
+                    o.e[c] = row_from_f<T>(y[i][c] * r_y * w[c]);
                 static_cast<V *>(a.z)[t * units + u] = o;
             }
             if (threadIdx.x == 0 && a.r_y)
@@ -156,63 +237,55 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a)
     }
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
+template <typename T, int VEC, int NV, bool RING>
+__global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_bwd_kernel(const NormArgs a)
 {
     using V = Piece<T, VEC>;
     __shared__ float s_buf[2][kMaxWarps];
     __shared__ float s_gate[kMaxWarps];
     const int units = a.H / VEC;
     const float inv_h = 1.0f / (float)a.H;
-    float c_post[NV][VEC], c_pre[NV][VEC], c_gate[NV][VEC];
+    // Column sums.  c_post is of scale * gate * D * hh; with a gate per column, of scale * D * hh, which
+    // gives both dw_post (times the gate) and dgate (times the weight).
+    float c_post[NV][VEC], c_pre[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < VEC; ++c)
-            c_post[i][c] = c_pre[i][c] = c_gate[i][c] = 0.0f;
+            c_post[i][c] = c_pre[i][c] = 0.0f;
+    RowRing<V, NV, 4, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.w_pre ? a.residual : nullptr),
+                                   static_cast<const V *>(a.dy), static_cast<const V *>(a.dz)}};
     pdl_wait();
+    in.init(a.T, units, a.slots);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * units;
-        V h[NV], r[NV], dy[NV], dz[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
-            if (u < units) {
-                h[i] = static_cast<const V *>(a.h)[row + u];
-                dy[i] = a.dy ? static_cast<const V *>(a.dy)[row + u] : piece_zero<T, VEC>();
-                if (a.w_pre) {
-                    r[i] = static_cast<const V *>(a.residual)[row + u];
-                    dz[i] = static_cast<const V *>(a.dz)[row + u];
-                }
-            }
-        }
+        in.wait();
         const float r_h = a.w_post ? a.r_h[t] : 1.0f;
+        const float r_y = a.w_pre ? a.r_y[t] : 0.0f;
         const float row_gate = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
-        float r_y = 0.0f, m1 = 0.0f;
-        float yh[NV][VEC];  // y * r_y, from the same operations as the forward's y
+        // (y is formed in both passes: kept in registers next to the column sums it would spill)
+        float m1 = 0.0f;
         if (a.w_pre) {
-            r_y = a.r_y[t];
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int u = threadIdx.x + i * blockDim.x;
                 if (u >= units)
                     continue;
-                const V w = static_cast<const V *>(a.w_pre)[u];
-                const V wo = a.w_post ? static_cast<const V *>(a.w_post)[u] : V{};
-                const V g = gate_piece<T, VEC>(a, t, units, u);
+                const V h = in.at(t, 0, i), r = in.at(t, 1, i), dz = in.at(t, 3, i);
+                float w[VEC], g[VEC], wi[VEC];
+                weight_piece<T, VEC>(a.w_post, a.offset, u, w);
+                weight_piece<T, VEC>(a.w_pre, a.offset, u, wi);
+                gate_piece<T, VEC>(a, t, units, u, row_gate, g);
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
-                    float n = row_to_f(h[i].e[c]);
-                    if (a.w_post)
-                        n = n * r_h * (row_to_f(wo.e[c]) + a.offset);
-                    yh[i][c] = fmaf(a.scale * gate_of<T, VEC>(a, row_gate, g, c), n, row_to_f(r[i].e[c])) * r_y;
-                    const float d = row_to_f(dz[i].e[c]);
-                    c_pre[i][c] = fmaf(d, yh[i][c], c_pre[i][c]);
-                    sum = fmaf(d * (row_to_f(w.e[c]) + a.offset), yh[i][c], sum);
+                    const float yh = fmaf(a.scale * g[c] * w[c], row_to_f(h.e[c]) * r_h, row_to_f(r.e[c])) * r_y;
+                    const float p = row_to_f(dz.e[c]) * yh;
+                    c_pre[i][c] += p;
+                    sum = fmaf(p, wi[c], sum);
                 }
             }
-            m1 = block_sum(sum, s_buf, 0) * inv_h;
+            m1 = block_sum(sum, s_buf, 0) * inv_h * r_y;
         }
         float v[NV][VEC];
         float sum = 0.0f, gsum = 0.0f;
@@ -221,27 +294,37 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
-            const V wi = a.w_pre ? static_cast<const V *>(a.w_pre)[u] : V{};
-            const V wo = a.w_post ? static_cast<const V *>(a.w_post)[u] : V{};
-            const V g = gate_piece<T, VEC>(a, t, units, u);
+            const V h = in.at(t, 0, i);
+            const V dy = a.dy ? in.at(t, 2, i) : piece_zero<T, VEC>();
+            float w[VEC], g[VEC];
+            weight_piece<T, VEC>(a.w_post, a.offset, u, w);
+            gate_piece<T, VEC>(a, t, units, u, row_gate, g);
+            float D[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c)
+                D[c] = row_to_f(dy.e[c]);
+            if (a.w_pre) {
+                const V r = in.at(t, 1, i), dz = in.at(t, 3, i);
+                float wi[VEC];
+                weight_piece<T, VEC>(a.w_pre, a.offset, u, wi);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    const float yh = fmaf(a.scale * g[c] * w[c], row_to_f(h.e[c]) * r_h, row_to_f(r.e[c])) * r_y;
+                    D[c] += fmaf(r_y * row_to_f(dz.e[c]), wi[c], -yh * m1);
+                }
+            }
             V o, dg;
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                float D = row_to_f(dy[i].e[c]);
-                if (a.w_pre)
-                    D += r_y * (row_to_f(dz[i].e[c]) * (row_to_f(wi.e[c]) + a.offset) - yh[i][c] * m1);
-                o.e[c] = row_from_f<T>(D);
-                const float hh = row_to_f(h[i].e[c]) * r_h;
-                const float w = a.w_post ? row_to_f(wo.e[c]) + a.offset : 1.0f;
-                const float dn = a.scale * gate_of<T, VEC>(a, row_gate, g, c) * D;
-                const float ge = a.scale * hh * w * D;
-                c_post[i][c] = fmaf(dn, hh, c_post[i][c]);
-                if (a.gate_kind == MOE_GATE_CHANNEL)
-                    c_gate[i][c] += ge;
-                gsum += ge;
+                o.e[c] = row_from_f<T>(D[c]);
+                const float hh = row_to_f(h.e[c]) * r_h;
+                const float sD = a.scale * D[c];
+                c_post[i][c] = fmaf(a.gate_kind == MOE_GATE_CHANNEL ? sD : sD * g[c], hh, c_post[i][c]);
+                const float ge = sD * w[c] * hh;
                 dg.e[c] = row_from_f<T>(ge);
-                v[i][c] = dn * w;
-                sum = fmaf(v[i][c], hh, sum);
+                gsum += ge;
+                v[i][c] = sD * w[c] * g[c];
+                sum = fmaf(g[c], ge, sum);
             }
             static_cast<V *>(a.dres)[row + u] = o;
             if (a.gate_kind == MOE_GATE_FULL)
@@ -255,14 +338,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
+            const V h = in.at(t, 0, i);
             V o;
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                const float hh = row_to_f(h[i].e[c]) * r_h;
+                const float hh = row_to_f(h.e[c]) * r_h;
                 o.e[c] = row_from_f<T>(a.w_post ? r_h * (v[i][c] - hh * m2) : v[i][c]);
             }
             static_cast<V *>(a.dh)[row + u] = o;
         }
+        in.next(t);
         if (a.gate_kind == MOE_GATE_TOKEN) {
             gsum = warp_sum(gsum);
             if ((threadIdx.x & 31) == 0)
@@ -277,7 +362,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
         }
         __syncthreads();  // the row's shared sums have been read
     }
-    float *p = a.part + (int64_t)blockIdx.x * 3 * a.H;
+    float *p = a.part + (int64_t)blockIdx.x * 2 * a.H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int u = threadIdx.x + i * blockDim.x;
@@ -287,34 +372,41 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
         for (int c = 0; c < VEC; ++c) {
             p[u * VEC + c] = c_post[i][c];
             p[a.H + u * VEC + c] = c_pre[i][c];
-            p[2 * a.H + u * VEC + c] = c_gate[i][c];
         }
     }
 }
 
-// out[c] = sum over the blocks' partial rows: 8 strided sums of a column, then added in order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ part, int nblocks, int H,
+// The blocks' partial rows added up: 8 strided sums of a column, then those in order.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ part, int nblocks, const NormArgs a,
                                                          float *dw_post, float *dw_pre, float *dgate)
 {
     __shared__ float s[8][33];
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float *out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dw_pre : dgate;
-    if (!out)
-        return;
     float acc = 0.0f;
-    if (c < H)
+    if (c < a.H)
+#pragma unroll 8
         for (int b = w; b < nblocks; b += 8)
-            acc += part[((int64_t)b * 3 + blockIdx.y) * H + c];
+            acc += part[((int64_t)b * 2 + blockIdx.y) * a.H + c];
     s[w][lane] = acc;
     __syncthreads();
-    if (w == 0 && c < H) {
+    if (w == 0 && c < a.H) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             sum += s[i][lane];
-        out[c] = sum;
+        if (blockIdx.y == 1) {
+            if (dw_pre)
+                dw_pre[c] = sum;
+        } else {
+            const bool ch = a.gate_kind == MOE_GATE_CHANNEL;
+            if (dw_post)
+                dw_post[c] = ch ? row_to_f(static_cast<const T *>(a.gate)[c]) * sum : sum;
+            if (ch)
+                dgate[c] = (a.w_post ? row_to_f(static_cast<const T *>(a.w_post)[c]) + a.offset : 1.0f) * sum;
+        }
     }
 }
 
@@ -325,22 +417,52 @@ int row_size(int row_type)
 
 int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// Partial rows of the backward: at most two blocks per SM (304 on 152 SMs).
-constexpr int kBwdBlocks = 304;
+// Blocks of the backward, one partial row each: as many as an SM's registers hold of rows this wide
+// (at most eight), so that the partial rows stay below 10 MB.
+int bwd_blocks(int64_t T, int H)
+{
+    const int64_t n = (int64_t)152 * 8192 / H;
+    const int64_t most = n < 152 ? 152 : n > 1216 ? 1216 : n;
+    return (int)(T < most ? T : most);
+}
+
+constexpr int kRingBytes = 224 * 1024;  // shared memory of an SM for the rings of its blocks
+
+template <typename T, int VEC, int NV, bool RING>
+cudaError_t run_ring(NormArgs a, bool bwd, int threads, int per_sm, cudaStream_t st)
+{
+    auto kern = bwd ? norm_bwd_kernel<T, VEC, NV, RING> : norm_kernel<T, VEC, NV, RING>;
+    size_t smem = 0;
+    if (RING) {
+        smem = (size_t)a.slots * (bwd ? 4 : 2) * a.H * sizeof(T);
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess)
+            return err;
+    }
+    const int64_t most = bwd ? bwd_blocks(a.T, a.H) : (int64_t)152 * per_sm;
+    return launch_kernel(false, kern, dim3((unsigned)(a.T < most ? a.T : most)), dim3(threads), smem, st, a);
+}
 
 template <typename T, int VEC, int NV>
-cudaError_t run(const NormArgs &a, bool bwd, cudaStream_t st)
+cudaError_t run(NormArgs a, bool bwd, cudaStream_t st)
 {
     const int units = a.H / VEC;
-    int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
+    const int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
     if (threads > kMaxThreads)
         return cudaErrorInvalidValue;
-    if (bwd) {
-        const int grid = (int)(a.T < kBwdBlocks ? a.T : kBwdBlocks);
-        return launch_kernel(false, norm_bwd_kernel<T, VEC, NV>, dim3(grid), dim3(threads), 0, st, a);
+    // Copied ahead where an SM's blocks have two or three rows each in its shared memory.
+    int per_sm = 1024 / threads;
+    if (bwd && NV > 1)
+        per_sm = per_sm > 1 ? per_sm / 2 : 1;
+    const int64_t slot = (int64_t)(bwd ? 4 : 2) * a.H * sizeof(T);
+    while (per_sm > 1 && per_sm * 2 * slot > kRingBytes)
+        --per_sm;
+    if (VEC * sizeof(T) == 16) {
+        a.slots = per_sm * 3 * slot <= kRingBytes ? 3 : 2;
+        if (a.slots * slot <= kRingBytes)
+            return run_ring<T, VEC, NV, VEC * sizeof(T) == 16>(a, bwd, threads, per_sm, st);
     }
-    const int64_t grid = a.T < 152 * 16 ? a.T : 152 * 16;
-    return launch_kernel(false, norm_kernel<T, VEC, NV>, dim3((unsigned)grid), dim3(threads), 0, st, a);
+    return run_ring<T, VEC, NV, false>(a, bwd, threads, 16, st);
 }
 
 // Pieces a thread holds: the fewest that cover the row with at most kMaxThreads threads.
@@ -348,9 +470,9 @@ template <typename T, int VEC>
 cudaError_t run_nv(const NormArgs &a, bool bwd, cudaStream_t st)
 {
     const int units = a.H / VEC;
-    if (units <= 256)
+    if (units <= kMaxThreads)
         return run<T, VEC, 1>(a, bwd, st);
-    if (units <= 2 * 256)
+    if (units <= 2 * kMaxThreads)
         return run<T, VEC, 2>(a, bwd, st);
     if constexpr (VEC * 4 * kMaxThreads >= kMaxH) {
         return run<T, VEC, 4>(a, bwd, st);
@@ -430,7 +552,7 @@ size_t moe_block_norm_workspace_size(int64_t T, int H)
 {
     if (T < 0 || H <= 0 || H > kMaxH)
         return 0;
-    return (size_t)(T < kBwdBlocks ? (T > 0 ? T : 1) : kBwdBlocks) * 3 * H * sizeof(float);
+    return (size_t)(T > 0 ? bwd_blocks(T, H) : 1) * 2 * H * sizeof(float);
 }
 
 int moe_block_norm_backward(int row_type, const void *h, const void *residual, const void *gate, int gate_kind,
@@ -469,16 +591,18 @@ int moe_block_norm_backward(int row_type, const void *h, const void *residual, c
     a.dres = d_residual, a.dh = dh, a.dgate = dgate, a.part = static_cast<float *>(ws);
     const bool wide = ((rows | (uintptr_t)((int64_t)H * es)) & 15) == 0;
     cudaError_t err = cudaSuccess;
-    const int nblocks = (int)(T < kBwdBlocks ? T : kBwdBlocks);
+    const int nblocks = bwd_blocks(T, H);
     if (T > 0)
         err = run_type(row_type, a, true, wide, st);
     if (err != cudaSuccess)
         return MOE_ERR_CUDA;
-    // T = 0: no partial rows, every sum is zero
-    float *dg = gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr;
-    return to_status(launch_kernel(false, norm_reduce_kernel, dim3((H + 31) / 32, 3), dim3(256), 0, st,
-                                   static_cast<const float *>(a.part), nblocks, H, w_post ? dw_post : nullptr,
-                                   w_pre ? dw_pre : nullptr, dg));
+    // (T = 0: no partial rows, every sum is zero)
+    auto reduce = row_type == MOE_ROW_BF16   ? norm_reduce_kernel<__nv_bfloat16>
+                  : row_type == MOE_ROW_FP16 ? norm_reduce_kernel<__half>
+                                             : norm_reduce_kernel<float>;
+    return to_status(launch_kernel(false, reduce, dim3((H + 31) / 32, 2), dim3(256), 0, st,
+                                   static_cast<const float *>(a.part), nblocks, a, dw_post, dw_pre,
+                                   gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr));
 }
 
 }  // extern "C"
