@@ -128,6 +128,26 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const RowArgs a, int6
     }
 }
 
+// v / sc for many v by one divisor, correctly rounded: q = fma(fma(-q0, sc, v), r, q0) with q0 = v r and r
+// = 1 / sc correctly rounded (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), three instructions instead of a division.  It needs the remainder
+// v - q0 sc to be exact, which holds for every quotient that does not encode to zero (|q| >= 2^-11) while
+// sc >= 2^-90; other divisors take the division.
+struct GroupDivide {
+    float sc, r;
+    bool fast;
+    __device__ __forceinline__ explicit GroupDivide(float s) : sc(s), r(1.0f / s), fast(s >= 0x1p-90f && s <= 0x1p120f)
+    {
+    }
+    __device__ __forceinline__ float operator()(float v) const
+    {
+        if (!fast)
+            return v / sc;
+        const float q0 = v * r;
+        return fmaf(fmaf(-q0, sc, v), r, q0);
+    }
+};
+
 // A warp quantises 512 columns of one token's row (a group of 128 columns on 8 lanes, 16 columns
 // per lane), once, and writes the codes and scales to the token's k positions.
 __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
@@ -155,13 +175,11 @@ __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.src) +
                                                                t * a.ld_src) + 2 * u;
             uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
-            const __nv_bfloat162 *h2 = reinterpret_cast<const __nv_bfloat162 *>(raw);
+            const uint32_t w8[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 p2 = __bfloat1622float2(h2[i]);
-                f[2 * i] = p2.x;
-                f[2 * i + 1] = p2.y;
-                amax = fmaxf(amax, fmaxf(fabsf(p2.x), fabsf(p2.y)));
+                unpack_word(w8[i], f[2 * i], f[2 * i + 1], __nv_bfloat16{});
+                amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
             }
         }
 #pragma unroll
@@ -170,11 +188,12 @@ __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
         const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
         uint32_t w[4];
         if (u < units) {
+            const GroupDivide div(sc);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] / sc, f[4 * i + 1] / sc),
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(div(f[4 * i]), div(f[4 * i + 1])),
                                                              __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] / sc, f[4 * i + 3] / sc),
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(div(f[4 * i + 2]), div(f[4 * i + 3])),
                                                              __NV_SATFINITE, __NV_E4M3);
                 w[i] = lo | (hi << 16);
             }
@@ -224,22 +243,18 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const RowArgs a, in
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 if (u0 + 32 * i < units) {
-                    const V v = row[u0 + 32 * i];
+                    float f[VEC];
+                    unpack<T, VEC>(row[u0 + 32 * i], f);
 #pragma unroll
                     for (int c = 0; c < VEC; ++c)
-                        acc[i][c] = fmaf(w, row_to_f(v.e[c]), acc[i][c]);
+                        acc[i][c] = fmaf(w, f[c], acc[i][c]);
                 }
         }
         V *out = static_cast<V *>(a.dst) + t * ld_units;
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (u0 + 32 * i < units) {
-                V v;
-#pragma unroll
-                for (int c = 0; c < VEC; ++c)
-                    v.e[c] = row_from_f<T>(acc[i][c]);
-                out[u0 + 32 * i] = v;
-            }
+            if (u0 + 32 * i < units)
+                out[u0 + 32 * i] = pack<T, VEC>(acc[i]);
     }
 }
 
@@ -295,14 +310,15 @@ __global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(const RowArgs a
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i)
                         if (u0 + 32 * WPT * i < units) {
-                            V o;
+                            float df[VEC], yf[VEC];
+                            unpack<T, VEC>(d[i], df);
+                            unpack<T, VEC>(y[i], yf);
 #pragma unroll
                             for (int c = 0; c < VEC; ++c) {
-                                const float df = row_to_f(d[i].e[c]);
-                                dot = fmaf(df, row_to_f(y[i].e[c]), dot);
-                                o.e[c] = row_from_f<T>(wj * df);
+                                dot = fmaf(df[c], yf[c], dot);
+                                df[c] *= wj;
                             }
-                            dr[u0 + 32 * WPT * i] = o;
+                            dr[u0 + 32 * WPT * i] = pack<T, VEC>(df);
                         }
                     dot = warp_sum(dot);
                     if (lane == 0)

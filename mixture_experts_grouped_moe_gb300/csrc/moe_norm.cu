@@ -123,34 +123,15 @@ __device__ __forceinline__ float block_sum(float v, float (*buf)[kMaxWarps], int
     return warp_sum(s);
 }
 
-// The gate of a piece's elements (row t, piece u); row_gate where it is the same for the whole row.
-template <typename T, int VEC>
-__device__ __forceinline__ void gate_piece(const NormArgs &a, int64_t t, int units, int u, float row_gate,
-                                           float (&g)[VEC])
-{
-    using V = Piece<T, VEC>;
-    if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
-        const V p = static_cast<const V *>(a.gate)[a.gate_kind == MOE_GATE_FULL ? t * units + u : u];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-            g[c] = row_to_f(p.e[c]);
-    } else {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-            g[c] = row_gate;
-    }
-}
-
 // weight + offset of a piece's elements, 1 without a weight
 template <typename T, int VEC>
 __device__ __forceinline__ void weight_piece(const void *w, float offset, int u, float (&f)[VEC])
 {
-    using V = Piece<T, VEC>;
     if (w) {
-        const V p = static_cast<const V *>(w)[u];
+        unpack<T, VEC>(static_cast<const Piece<T, VEC> *>(w)[u], f);
 #pragma unroll
         for (int c = 0; c < VEC; ++c)
-            f[c] = row_to_f(p.e[c]) + offset;
+            f[c] += offset;
     } else {
 #pragma unroll
         for (int c = 0; c < VEC; ++c)
@@ -158,8 +139,23 @@ __device__ __forceinline__ void weight_piece(const void *w, float offset, int u,
     }
 }
 
-template <typename T, int VEC, int NV, bool RING>
-__global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const NormArgs a)
+// What multiplies h * rstd(h) (and a row's or an element's gate) in y: scale * (w_post + offset) and, with
+// a gate per column, that gate.  The same for every row: a thread keeps its columns' in registers.
+template <typename T, int VEC>
+__device__ __forceinline__ void branch_factor(const NormArgs &a, int u, float (&k)[VEC])
+{
+    weight_piece<T, VEC>(a.w_post, a.offset, u, k);
+    float g[VEC];
+    if (a.gate_kind == MOE_GATE_CHANNEL)
+        unpack<T, VEC>(static_cast<const Piece<T, VEC> *>(a.gate)[u], g);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c)
+        k[c] *= a.gate_kind == MOE_GATE_CHANNEL ? a.scale * g[c] : a.scale;
+}
+
+// FULL: a gate per element.
+template <typename T, int VEC, int NV, bool RING, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_kernel(const NormArgs a)
 {
     using V = Piece<T, VEC>;
     __shared__ float s_buf[2][kMaxWarps];
@@ -168,8 +164,18 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const N
     RowRing<V, NV, 2, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.residual)}};
     pdl_wait();
     in.init(a.T, units, a.slots);
+    float k[NV][VEC], wi[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int u = threadIdx.x + i * blockDim.x;
+        if (u < units) {
+            branch_factor<T, VEC>(a, u, k[i]);
+            weight_piece<T, VEC>(a.w_pre, a.offset, u, wi[i]);
+        }
+    }
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         in.wait();
+        float f = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
         V h[NV], r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -177,20 +183,22 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const N
                 h[i] = in.at(t, 0, i);
                 r[i] = in.at(t, 1, i);
             }
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (threadIdx.x + i * blockDim.x < units)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    const float f = row_to_f(h[i].e[c]);
-                    sum = fmaf(f, f, sum);
-                }
-        const float row_gate = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
         float r_h = 1.0f;
-        if (a.w_post)
+        if (a.w_post) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (threadIdx.x + i * blockDim.x < units) {
+                    float x[VEC];
+                    unpack<T, VEC>(h[i], x);
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c)
+                        sum = fmaf(x[c], x[c], sum);
+                }
             r_h = rsqrtf(fmaf(block_sum(sum, s_buf, 0), inv_h, a.eps));
+        }
         in.next(t);
+        f *= r_h;
         float y[NV][VEC];
         float ysum = 0.0f;
 #pragma unroll
@@ -198,17 +206,17 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const N
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
-            float w[VEC], g[VEC];
-            weight_piece<T, VEC>(a.w_post, a.offset, u, w);
-            gate_piece<T, VEC>(a, t, units, u, row_gate, g);
-            V o;
+            float x[VEC], res[VEC], g[VEC];
+            unpack<T, VEC>(h[i], x);
+            unpack<T, VEC>(r[i], res);
+            if (FULL)
+                unpack<T, VEC>(static_cast<const V *>(a.gate)[t * units + u], g);
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                y[i][c] = fmaf(a.scale * g[c] * w[c], row_to_f(h[i].e[c]) * r_h, row_to_f(r[i].e[c]));
+                y[i][c] = fmaf(k[i][c], FULL ? x[c] * f * g[c] : x[c] * f, res[c]);
                 ysum = fmaf(y[i][c], y[i][c], ysum);
-                o.e[c] = row_from_f<T>(y[i][c]);
             }
-            static_cast<V *>(a.y)[t * units + u] = o;
+            static_cast<V *>(a.y)[t * units + u] = pack<T, VEC>(y[i]);
         }
         if (threadIdx.x == 0 && a.r_h)
             a.r_h[t] = r_h;
@@ -219,13 +227,10 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const N
                 const int u = threadIdx.x + i * blockDim.x;
                 if (u >= units)
                     continue;
-                float w[VEC];
-                weight_piece<T, VEC>(a.w_pre, a.offset, u, w);
-                V o;
 #pragma unroll
                 for (int c = 0; c < VEC; ++c)
-                    o.e[c] = row_from_f<T>(y[i][c] * r_y * w[c]);
-                static_cast<V *>(a.z)[t * units + u] = o;
+                    y[i][c] *= r_y * wi[i][c];
+                static_cast<V *>(a.z)[t * units + u] = pack<T, VEC>(y[i]);
             }
             if (threadIdx.x == 0 && a.r_y)
                 a.r_y[t] = r_y;
@@ -237,129 +242,128 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const N
     }
 }
 
-template <typename T, int VEC, int NV, bool RING>
-__global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_bwd_kernel(const NormArgs a)
+// With hh = h r_h and, per row or element, hg = gate * hh (a gate per column is part of k):
+//   y = residual + k hg       D = dy + r_y dz wi - y r_y^2 mean(dz wi y r_y)
+//   t = k D    (v = gate t)   mean of v hh, and a row's dgate, from the sum of t hh
+//   column sums  c_post += D hg, c_pre += dz y r_y
+// dw_post and a column's dgate are c_post times what is left of scale, gate and weight.
+template <typename T, int VEC, int NV, bool RING, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
 {
     using V = Piece<T, VEC>;
     __shared__ float s_buf[2][kMaxWarps];
-    __shared__ float s_gate[kMaxWarps];
     const int units = a.H / VEC;
     const float inv_h = 1.0f / (float)a.H;
-    // Column sums.  c_post is of scale * gate * D * hh; with a gate per column, of scale * D * hh, which
-    // gives both dw_post (times the gate) and dgate (times the weight).
-    float c_post[NV][VEC], c_pre[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-            c_post[i][c] = c_pre[i][c] = 0.0f;
     RowRing<V, NV, 4, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.w_pre ? a.residual : nullptr),
                                    static_cast<const V *>(a.dy), static_cast<const V *>(a.dz)}};
     pdl_wait();
     in.init(a.T, units, a.slots);
+    float c_post[NV][VEC], c_pre[NV][VEC], k[NV][VEC], wi[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int u = threadIdx.x + i * blockDim.x;
+        if (u < units) {
+            branch_factor<T, VEC>(a, u, k[i]);
+            weight_piece<T, VEC>(a.w_pre, a.offset, u, wi[i]);
+        }
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            c_post[i][c] = c_pre[i][c] = 0.0f;
+    }
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * units;
         in.wait();
         const float r_h = a.w_post ? a.r_h[t] : 1.0f;
         const float r_y = a.w_pre ? a.r_y[t] : 0.0f;
-        const float row_gate = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
+        const float gate = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
         // (y is formed in both passes: kept in registers next to the column sums it would spill)
         float m1 = 0.0f;
         if (a.w_pre) {
+            const float f = r_h * gate;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int u = threadIdx.x + i * blockDim.x;
                 if (u >= units)
                     continue;
-                const V h = in.at(t, 0, i), r = in.at(t, 1, i), dz = in.at(t, 3, i);
-                float w[VEC], g[VEC], wi[VEC];
-                weight_piece<T, VEC>(a.w_post, a.offset, u, w);
-                weight_piece<T, VEC>(a.w_pre, a.offset, u, wi);
-                gate_piece<T, VEC>(a, t, units, u, row_gate, g);
+                float h[VEC], r[VEC], dz[VEC], g[VEC];
+                unpack<T, VEC>(in.at(t, 0, i), h);
+                unpack<T, VEC>(in.at(t, 1, i), r);
+                unpack<T, VEC>(in.at(t, 3, i), dz);
+                if (FULL)
+                    unpack<T, VEC>(static_cast<const V *>(a.gate)[row + u], g);
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
-                    const float yh = fmaf(a.scale * g[c] * w[c], row_to_f(h.e[c]) * r_h, row_to_f(r.e[c])) * r_y;
-                    const float p = row_to_f(dz.e[c]) * yh;
-                    c_pre[i][c] += p;
-                    sum = fmaf(p, wi[c], sum);
+                    const float p = dz[c] * fmaf(k[i][c], FULL ? h[c] * f * g[c] : h[c] * f, r[c]);
+                    c_pre[i][c] = fmaf(p, r_y, c_pre[i][c]);
+                    sum = fmaf(p, wi[i][c], sum);
                 }
             }
-            m1 = block_sum(sum, s_buf, 0) * inv_h * r_y;
+            m1 = block_sum(sum, s_buf, 0) * inv_h * r_y * r_y * r_y;
         }
         float v[NV][VEC];
-        float sum = 0.0f, gsum = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
-            const V h = in.at(t, 0, i);
-            const V dy = a.dy ? in.at(t, 2, i) : piece_zero<T, VEC>();
-            float w[VEC], g[VEC];
-            weight_piece<T, VEC>(a.w_post, a.offset, u, w);
-            gate_piece<T, VEC>(a, t, units, u, row_gate, g);
-            float D[VEC];
+            float hh[VEC], hg[VEC], D[VEC], g[VEC];
+            unpack<T, VEC>(in.at(t, 0, i), hh);
+            if (FULL)
+                unpack<T, VEC>(static_cast<const V *>(a.gate)[row + u], g);
+            unpack<T, VEC>(a.dy ? in.at(t, 2, i) : piece_zero<T, VEC>(), D);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c)
-                D[c] = row_to_f(dy.e[c]);
+            for (int c = 0; c < VEC; ++c) {
+                hh[c] *= r_h;
+                hg[c] = hh[c] * (FULL ? g[c] : gate);
+            }
             if (a.w_pre) {
-                const V r = in.at(t, 1, i), dz = in.at(t, 3, i);
-                float wi[VEC];
-                weight_piece<T, VEC>(a.w_pre, a.offset, u, wi);
+                float r[VEC], dz[VEC];
+                unpack<T, VEC>(in.at(t, 1, i), r);
+                unpack<T, VEC>(in.at(t, 3, i), dz);
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    const float yh = fmaf(a.scale * g[c] * w[c], row_to_f(h.e[c]) * r_h, row_to_f(r.e[c])) * r_y;
-                    D[c] += fmaf(r_y * row_to_f(dz.e[c]), wi[c], -yh * m1);
+                for (int c = 0; c < VEC; ++c)
+                    D[c] = fmaf(r_y * dz[c], wi[i][c], fmaf(-fmaf(k[i][c], hg[c], r[c]), m1, D[c]));
+            }
+            static_cast<V *>(a.dres)[row + u] = pack<T, VEC>(D);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                c_post[i][c] = fmaf(D[c], hg[c], c_post[i][c]);
+                v[i][c] = k[i][c] * D[c];
+                D[c] = v[i][c] * hh[c];
+                if (FULL) {
+                    sum = fmaf(D[c], g[c], sum);
+                    v[i][c] *= g[c];
+                } else {
+                    sum += D[c];
                 }
             }
-            V o, dg;
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                o.e[c] = row_from_f<T>(D[c]);
-                const float hh = row_to_f(h.e[c]) * r_h;
-                const float sD = a.scale * D[c];
-                c_post[i][c] = fmaf(a.gate_kind == MOE_GATE_CHANNEL ? sD : sD * g[c], hh, c_post[i][c]);
-                const float ge = sD * w[c] * hh;
-                dg.e[c] = row_from_f<T>(ge);
-                gsum += ge;
-                v[i][c] = sD * w[c] * g[c];
-                sum = fmaf(g[c], ge, sum);
-            }
-            static_cast<V *>(a.dres)[row + u] = o;
-            if (a.gate_kind == MOE_GATE_FULL)
-                static_cast<V *>(a.dgate)[row + u] = dg;
+            if (FULL)
+                static_cast<V *>(a.dgate)[row + u] = pack<T, VEC>(D);
         }
         float m2 = 0.0f;
-        if (a.w_post)
-            m2 = block_sum(sum, s_buf, 1) * inv_h;
+        if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) {
+            sum = block_sum(sum, s_buf, 1);
+            if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0)
+                static_cast<float *>(a.dgate)[t] = sum;
+            if (a.w_post)
+                m2 = sum * inv_h * gate * r_h * r_h;
+        }
+        const float f = r_h * gate;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = threadIdx.x + i * blockDim.x;
             if (u >= units)
                 continue;
-            const V h = in.at(t, 0, i);
-            V o;
+            float h[VEC];
+            unpack<T, VEC>(in.at(t, 0, i), h);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float hh = row_to_f(h.e[c]) * r_h;
-                o.e[c] = row_from_f<T>(a.w_post ? r_h * (v[i][c] - hh * m2) : v[i][c]);
-            }
-            static_cast<V *>(a.dh)[row + u] = o;
+            for (int c = 0; c < VEC; ++c)
+                h[c] = fmaf(v[i][c], f, -h[c] * m2);
+            static_cast<V *>(a.dh)[row + u] = pack<T, VEC>(h);
         }
         in.next(t);
-        if (a.gate_kind == MOE_GATE_TOKEN) {
-            gsum = warp_sum(gsum);
-            if ((threadIdx.x & 31) == 0)
-                s_gate[threadIdx.x >> 5] = gsum;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float s = 0.0f;
-                for (int i = 0; i < (int)(blockDim.x >> 5); ++i)
-                    s += s_gate[i];
-                static_cast<float *>(a.dgate)[t] = s;
-            }
-        }
         __syncthreads();  // the row's shared sums have been read
     }
     float *p = a.part + (int64_t)blockIdx.x * 2 * a.H;
@@ -376,32 +380,34 @@ __global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_bwd
     }
 }
 
-// The blocks' partial rows added up: 8 strided sums of a column, then those in order.
+// The blocks' partial rows added up: 32 strided sums of a column (few loads after one another: with 8
+// it took 10.7 us for 304 partial rows of 4096), then those in order.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ part, int nblocks, const NormArgs a,
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int nblocks, const NormArgs a,
                                                          float *dw_post, float *dw_pre, float *dgate)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float acc = 0.0f;
     if (c < a.H)
-#pragma unroll 8
-        for (int b = w; b < nblocks; b += 8)
+#pragma unroll 10
+        for (int b = w; b < nblocks; b += 32)
             acc += part[((int64_t)b * 2 + blockIdx.y) * a.H + c];
     s[w][lane] = acc;
     __syncthreads();
     if (w == 0 && c < a.H) {
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 32; ++i)
             sum += s[i][lane];
         if (blockIdx.y == 1) {
             if (dw_pre)
                 dw_pre[c] = sum;
         } else {
             const bool ch = a.gate_kind == MOE_GATE_CHANNEL;
+            sum *= a.scale;
             if (dw_post)
                 dw_post[c] = ch ? row_to_f(static_cast<const T *>(a.gate)[c]) * sum : sum;
             if (ch)
@@ -418,11 +424,11 @@ int row_size(int row_type)
 int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // Blocks of the backward, one partial row each: as many as an SM's registers hold of rows this wide
-// (at most eight), so that the partial rows stay below 10 MB.
+// (at most four), so that the partial rows stay below 10 MB.
 int bwd_blocks(int64_t T, int H)
 {
     const int64_t n = (int64_t)152 * 8192 / H;
-    const int64_t most = n < 152 ? 152 : n > 1216 ? 1216 : n;
+    const int64_t most = n < 152 ? 152 : n > 608 ? 608 : n;
     return (int)(T < most ? T : most);
 }
 
@@ -431,7 +437,9 @@ constexpr int kRingBytes = 224 * 1024;  // shared memory of an SM for the rings 
 template <typename T, int VEC, int NV, bool RING>
 cudaError_t run_ring(NormArgs a, bool bwd, int threads, int per_sm, cudaStream_t st)
 {
-    auto kern = bwd ? norm_bwd_kernel<T, VEC, NV, RING> : norm_kernel<T, VEC, NV, RING>;
+    const bool full = a.gate_kind == MOE_GATE_FULL;
+    auto kern = bwd ? (full ? norm_bwd_kernel<T, VEC, NV, RING, true> : norm_bwd_kernel<T, VEC, NV, RING, false>)
+                    : (full ? norm_kernel<T, VEC, NV, RING, true> : norm_kernel<T, VEC, NV, RING, false>);
     size_t smem = 0;
     if (RING) {
         smem = (size_t)a.slots * (bwd ? 4 : 2) * a.H * sizeof(T);
@@ -451,9 +459,7 @@ cudaError_t run(NormArgs a, bool bwd, cudaStream_t st)
     if (threads > kMaxThreads)
         return cudaErrorInvalidValue;
     // Copied ahead where an SM's blocks have two or three rows each in its shared memory.
-    int per_sm = 1024 / threads;
-    if (bwd && NV > 1)
-        per_sm = per_sm > 1 ? per_sm / 2 : 1;
+    int per_sm = (bwd || NV > 1 ? 512 : 1024) / threads;  // (by registers: up to 128 and 64 a thread)
     const int64_t slot = (int64_t)(bwd ? 4 : 2) * a.H * sizeof(T);
     while (per_sm > 1 && per_sm * 2 * slot > kRingBytes)
         --per_sm;
@@ -470,9 +476,12 @@ template <typename T, int VEC>
 cudaError_t run_nv(const NormArgs &a, bool bwd, cudaStream_t st)
 {
     const int units = a.H / VEC;
-    if (units <= kMaxThreads)
+    // (single elements, and the backward: fewer, fuller threads, whose columns' factors and sums stay in
+    // registers)
+    const int most = VEC == 1 || bwd ? 256 : kMaxThreads;
+    if (units <= most)
         return run<T, VEC, 1>(a, bwd, st);
-    if (units <= 2 * kMaxThreads)
+    if (units <= 2 * most)
         return run<T, VEC, 2>(a, bwd, st);
     if constexpr (VEC * 4 * kMaxThreads >= kMaxH) {
         return run<T, VEC, 4>(a, bwd, st);
@@ -600,7 +609,7 @@ int moe_block_norm_backward(int row_type, const void *h, const void *residual, c
     auto reduce = row_type == MOE_ROW_BF16   ? norm_reduce_kernel<__nv_bfloat16>
                   : row_type == MOE_ROW_FP16 ? norm_reduce_kernel<__half>
                                              : norm_reduce_kernel<float>;
-    return to_status(launch_kernel(false, reduce, dim3((H + 31) / 32, 2), dim3(256), 0, st,
+    return to_status(launch_kernel(false, reduce, dim3((H + 31) / 32, 2), dim3(1024), 0, st,
                                    static_cast<const float *>(a.part), nblocks, a, dw_post, dw_pre,
                                    gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr));
 }

@@ -21,19 +21,79 @@ __device__ __forceinline__ __half row_from_f<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ float row_from_f<float>(float v) { return v; }
 
-// VEC consecutive elements, moved by one load or store (VEC * sizeof(T) of 2, 4 or 16 bytes).
+// VEC consecutive elements, moved by one load or store: 16 bytes, or one element.  (The 16 bytes are
+// kept as words: as an array of elements the compiler moves them one by one.)
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Piece {
-    T e[VEC];
+struct Piece {
+    static_assert(VEC * sizeof(T) == 16, "16 bytes, or one element");
+    uint4 w;
 };
+template <typename T>
+struct Piece<T, 1> {
+    T e;
+};
+
+__device__ __forceinline__ void unpack_word(uint32_t w, float &lo, float &hi, __nv_bfloat16)
+{
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float &lo, float &hi, __half)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = f.x, hi = f.y;
+}
+__device__ __forceinline__ uint32_t pack_word(float lo, float hi, __nv_bfloat16)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t pack_word(float lo, float hi, __half)
+{
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Piece<T, VEC> &p, float (&f)[VEC])
+{
+    if constexpr (VEC == 1) {
+        f[0] = row_to_f(p.e);
+    } else if constexpr (sizeof(T) == 4) {
+        f[0] = __uint_as_float(p.w.x), f[1] = __uint_as_float(p.w.y);
+        f[2] = __uint_as_float(p.w.z), f[3] = __uint_as_float(p.w.w);
+    } else {
+        unpack_word(p.w.x, f[0], f[1], T{});
+        unpack_word(p.w.y, f[2], f[3], T{});
+        unpack_word(p.w.z, f[4], f[5], T{});
+        unpack_word(p.w.w, f[6], f[7], T{});
+    }
+}
+
+// Each element rounded to nearest even.
+template <typename T, int VEC>
+__device__ __forceinline__ Piece<T, VEC> pack(const float (&f)[VEC])
+{
+    Piece<T, VEC> p;
+    if constexpr (VEC == 1) {
+        p.e = row_from_f<T>(f[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        p.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+        p.w = make_uint4(pack_word(f[0], f[1], T{}), pack_word(f[2], f[3], T{}), pack_word(f[4], f[5], T{}),
+                         pack_word(f[6], f[7], T{}));
+    }
+    return p;
+}
 
 template <typename T, int VEC>
 __device__ __forceinline__ Piece<T, VEC> piece_zero()
 {
     Piece<T, VEC> p;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        p.e[i] = row_from_f<T>(0.0f);
+    if constexpr (VEC == 1)
+        p.e = row_from_f<T>(0.0f);
+    else
+        p.w = make_uint4(0, 0, 0, 0);
     return p;
 }
 
