@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const RowArgs a, int6
     constexpr int seg = 32 * kUnits;
     V *dst = static_cast<V *>(a.dst);
     pdl_wait();
+    pdl_trigger();
     if (blockIdx.x >= a.token_blocks) {
         const int64_t npp = *a.npp;
         zero_padding(a.sorted_ids, npp < a.P ? npp : a.P, a.T * a.k, units, seg, dst, zero,
@@ -133,20 +134,21 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const RowArgs a, int6
 // System/6000 processor", 1990), three instructions instead of a division.  It needs the remainder
 // v - q0 sc to be exact, which holds for every quotient that does not encode to zero (|q| >= 2^-11) while
 // sc >= 2^-90; other divisors take the division.
-struct GroupDivide {
-    float sc, r;
-    bool fast;
-    __device__ __forceinline__ explicit GroupDivide(float s) : sc(s), r(1.0f / s), fast(s >= 0x1p-90f && s <= 0x1p120f)
-    {
+__device__ __forceinline__ void divide16(float (&f)[16], float sc)
+{
+    if (sc >= 0x1p-90f && sc <= 0x1p120f) {
+        const float r = 1.0f / sc;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float q0 = f[i] * r;
+            f[i] = fmaf(fmaf(-q0, sc, f[i]), r, q0);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            f[i] /= sc;
     }
-    __device__ __forceinline__ float operator()(float v) const
-    {
-        if (!fast)
-            return v / sc;
-        const float q0 = v * r;
-        return fmaf(fmaf(-q0, sc, v), r, q0);
-    }
-};
+}
 
 // A warp quantises 512 columns of one token's row (a group of 128 columns on 8 lanes, 16 columns
 // per lane), once, and writes the codes and scales to the token's k positions.
@@ -155,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
+    pdl_trigger();
     const int64_t units = a.H / 16;
     if (blockIdx.x >= a.token_blocks) {
         const int64_t npp = *a.npp;
@@ -188,13 +191,13 @@ __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
         const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
         uint32_t w[4];
         if (u < units) {
-            const GroupDivide div(sc);
+            divide16(f, sc);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(div(f[4 * i]), div(f[4 * i + 1])),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(div(f[4 * i + 2]), div(f[4 * i + 3])),
-                                                             __NV_SATFINITE, __NV_E4M3);
+                const uint32_t lo =
+                    __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi =
+                    __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
                 w[i] = lo | (hi << 16);
             }
         }
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const RowArgs a, in
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
+    pdl_trigger();
     const int64_t nseg = (units + seg - 1) / seg;
     const int64_t total = nseg * a.T;
     const V *ys = static_cast<const V *>(a.ys);
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const RowArgs a, in
 // row's chunk of ys, add to the slot's dot product and write the weighted row.  A warp's partial
 // dot products live in its own row of s_dot; the token's warps are summed in order at the end.
 template <typename T, int VEC, int WPT>
-__global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(const RowArgs a, int64_t units, int64_t ld_units)
+__global__ void __launch_bounds__(kThreads, 4) unpermute_bwd_kernel(const RowArgs a, int64_t units, int64_t ld_units)
 {
     using V = Piece<T, VEC>;
     constexpr int TPB = kWarps / WPT;  // tokens a block works on at once
@@ -272,6 +276,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(const RowArgs a
     const int wt_in = w % WPT, tok = w / WPT;
     V *dys = static_cast<V *>(a.dst);
     pdl_wait();
+    pdl_trigger();
     if (blockIdx.x >= a.token_blocks) {
         const int64_t npp = *a.npp;
         zero_padding(a.sorted_ids, npp < a.P ? npp : a.P, a.T * a.k, units, 32 * kUnits, dys, piece_zero<T, VEC>(),
@@ -364,7 +369,7 @@ cudaError_t run_permute(RowArgs &a, int64_t row_bytes, int es, bool zero, cudaSt
     const int seg = 32 * kUnits;
     a.token_blocks = blocks_for((units + seg - 1) / seg * a.T);
     const int grid = (int)a.token_blocks + pad_blocks(zero, a.P, units, seg);
-    return launch_kernel(false, permute_kernel<V>, dim3(grid), dim3(kThreads), 0, st, a, units,
+    return launch_kernel(true, permute_kernel<V>, dim3(grid), dim3(kThreads), 0, st, a, units,
                          a.ld_src * es / (int64_t)sizeof(V), V{});
 }
 
@@ -373,7 +378,7 @@ cudaError_t run_unpermute(const RowArgs &a, cudaStream_t st)
 {
     const int64_t units = a.H / VEC;
     const int grid = blocks_for((units + 63) / 64 * a.T);
-    return launch_kernel(false, unpermute_kernel<T, VEC>, dim3(grid), dim3(kThreads), 0, st, a, units,
+    return launch_kernel(true, unpermute_kernel<T, VEC>, dim3(grid), dim3(kThreads), 0, st, a, units,
                          a.ld_dst / VEC);
 }
 
@@ -383,7 +388,7 @@ cudaError_t run_bwd_w(RowArgs &a, bool zero, cudaStream_t st)
     const int64_t units = a.H / VEC;
     a.token_blocks = blocks_for((int64_t)a.T * WPT);
     const int grid = (int)a.token_blocks + pad_blocks(zero, a.P, units, 32 * kUnits);
-    return launch_kernel(false, unpermute_bwd_kernel<T, VEC, WPT>, dim3(grid), dim3(kThreads), 0, st, a, units,
+    return launch_kernel(true, unpermute_bwd_kernel<T, VEC, WPT>, dim3(grid), dim3(kThreads), 0, st, a, units,
                          a.ld_src / VEC);
 }
 
@@ -441,7 +446,7 @@ int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T
     so.slot_pos = slot_pos;
     // as moe_align_sort lays its scratch out: chunk histograms, then the E + 1 padded offsets
     so.expert_offsets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + need - (size_t)(E + 1) * 4);
-    return to_status(launch_align_sort(topk_ids, topk_weights, T, k, E, block_m, so, ws, false, true,
+    return to_status(launch_align_sort(topk_ids, topk_weights, T, k, E, block_m, so, ws, true, true,
                                        static_cast<cudaStream_t>(stream)));
 }
 
@@ -495,7 +500,7 @@ int moe_permute_fp8(const void *x, int64_t ld_x, const int32_t *slot_pos, const 
     a.T = T, a.k = k, a.H = H, a.P = P, a.q = q, a.s = s;
     a.token_blocks = blocks_for((H / 16 + 31) / 32 * (int64_t)T);
     const int grid = (int)a.token_blocks + pad_blocks(zero_padding, P, H / 16, 32 * kUnits);
-    return to_status(launch_kernel(false, permute_fp8_kernel, dim3(grid), dim3(kThreads), 0,
+    return to_status(launch_kernel(true, permute_fp8_kernel, dim3(grid), dim3(kThreads), 0,
                                    static_cast<cudaStream_t>(stream), a));
 }
 

@@ -146,7 +146,10 @@ __device__ __forceinline__ void store8(float *d, float2 (&x)[4], int accumulate)
 
 template <int TN, bool WG>
 struct Cfg {
-    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 6 : 8;
+    // 64-column products share an SM between two CTAs: small problems are bound by the chain of a block,
+    // and one's hides behind the other's.
+    static constexpr int kCtas = TN == 64 && !WG ? 2 : 1;
+    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 6 : WG ? 8 : 3;
     static constexpr int kABytes = 128 * 128, kBBytes = TN * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBufs = TN == 256 ? 2 : 4;  // TMEM accumulators
@@ -185,7 +188,7 @@ struct Tile {
 };
 
 template <int TN, bool WG>
-__global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, 1) gemm_block_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gemm_block_kernel(const __grid_constant__ Args a)
 {
     using C = Cfg<TN, WG>;
     constexpr int kFirstPromo = C::kFirstPromo;
@@ -218,6 +221,7 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, 1) gemm_block_kernel(co
         tmem_relinquish();
     }
     pdl_wait();
+    pdl_trigger();
     if (WG && warp == 2) {
         // first block of each expert: a running sum of ceil(count / 128) over the experts
         int run = 0;
@@ -649,16 +653,18 @@ struct FewCfg {
     static constexpr int kStages = NP == 64 ? 7 : NP == 32 ? 9 : 10;
     static constexpr int kBufs = 4;
     static constexpr int kTmem = kBufs * NP < 32 ? 32 : kBufs * NP;
+    // promotion warps: one per TMEM lane quadrant, or two that share its columns
+    static constexpr int kWarps = NP == 64 ? 8 : 4;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr int kCols = NP * 4 / kWarps;  // columns of a warp
 };
-constexpr int kFewThreads = 192;
-constexpr int kFewWarps = 4;
 
 template <int NP>
 struct __align__(1024) FewSmem {
     using C = FewCfg<NP>;
     uint8_t stage[C::kStages][C::kStageBytes];
     float red[NP * 128];                 // the parts of this CTA's rows: [source][column][row]
-    float f[kFewWarps][2][NP];           // a warp's column factors, alternating between blocks
+    float f[C::kWarps][2][C::kCols];     // a warp's column factors, alternating between blocks
     uint64_t full[C::kStages], empty[C::kStages];
     uint64_t tfull[C::kBufs], tempty[C::kBufs];
     uint64_t red_full, red_free;
@@ -668,7 +674,7 @@ struct __align__(1024) FewSmem {
 };
 
 template <int NP>
-__global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __grid_constant__ Args a, int S)
+__global__ void __launch_bounds__(FewCfg<NP>::kThreads, 1) gemm_block_few_kernel(const __grid_constant__ Args a, int S)
 {
     using C = FewCfg<NP>;
     extern __shared__ uint8_t smem_raw[];
@@ -684,10 +690,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
         }
         for (int i = 0; i < C::kBufs; ++i) {
             mbar_init(&sm.tfull[i], 1);
-            mbar_init(&sm.tempty[i], kFewWarps);
+            mbar_init(&sm.tempty[i], C::kWarps);
         }
-        mbar_init(&sm.red_full, S > kFewWarps ? S : kFewWarps);
-        mbar_init(&sm.red_free, S * kFewWarps);
+        mbar_init(&sm.red_full, (S > 4 ? S : 4) * (C::kWarps / 4));
+        mbar_init(&sm.red_free, S * C::kWarps);
         mbar_init(&sm.drain, 1);
         sm.abort = 0;
         fence_mbarrier_init();
@@ -700,11 +706,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
     }
     tc_fence_before();
     __syncthreads();
-    if (S > 1)
-        cluster_sync();  // every CTA's barriers exist before a peer signals them
+    if (S > 1)  // (the wait for it comes before the first write to a peer)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
     pdl_wait();
+    pdl_trigger();
     const int KB = (a.K + 127) / 128;
     const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
     const int64_t rows = rows_in_use(a);
@@ -787,7 +794,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
             }
         }
     } else {
+        constexpr int kCols = C::kCols;
         const int q = warp & 3, pw = warp - 2;
+        const int col0 = pw / 4 * kCols;  // this warp's columns
+        bool met = S == 1;  // the cluster's CTAs have all started
         const int row = q * 32 + lane;  // weight row of the tile
         int buf = 0;
         uint32_t bph = 0, rph = 0;
@@ -797,29 +807,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
             const int64_t x0 = (int64_t)b * NP;
             const int e = expert_of(a, x0);
             const float *sb = a.sb + ((int64_t)e * nwt + wt) * KB;
-            float acc[NP];
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
+            for (int i = 0; i < kCols; ++i)
                 acc[i] = 0.0f;
-            // lane c holds the scales of columns c and c + 32 of the next block
-            constexpr int kPer = (NP + 31) / 32;
-            float sx[kPer], sw = 0.0f;
+            // lane c holds the next block's scale of column col0 + c
+            static_assert(kCols <= 32, "a lane per column");
+            float sx = 0.0f, sw = 0.0f;
+            const int64_t xr = x0 + col0 + lane;
+            const bool has = lane < kCols && xr < a.M;
             auto fetch = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int64_t r = x0 + lane + 32 * i;
-                    sx[i] = lane + 32 * i < NP && r < a.M ? a.sa[r * a.sa_row + kb * a.sa_blk] : 0.0f;
-                }
+                if (has)
+                    sx = a.sa[xr * a.sa_row + kb * a.sa_blk];
                 sw = sb[kb];
             };
             if (kb0 < kb1)
                 fetch(kb0);
             for (int kb = kb0; kb < kb1; ++kb) {
                 float *f = sm.f[pw][kb & 1];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (lane + 32 * i < NP)
-                        f[lane + 32 * i] = sx[i] * sw;
+                if (lane < kCols)
+                    f[lane] = sx * sw;
                 if (kb + 1 < kb1)
                     fetch(kb + 1);
                 const bool w_ok = mbar_wait(&sm.tfull[buf], bph, a.status, abort_flag);
@@ -829,9 +836,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
                 }
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * NP;
+                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * NP + col0;
 #pragma unroll
-                for (int c = 0; c < NP; c += 16) {
+                for (int c = 0; c < kCols; c += 16) {
                     float v[8], u[8];
                     tmem_ld_nowait(tb + c, v);
                     tmem_ld_nowait(tb + c + 8, u);
@@ -868,20 +875,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
             };
             if (S == 1) {
 #pragma unroll
-                for (int c = 0; c < NP; ++c)
-                    store(c, wt * 128 + row, acc[c]);
+                for (int c = 0; c < kCols; ++c)
+                    store(col0 + c, wt * 128 + row, acc[c]);
                 continue;
             }
             // CTA o of the cluster adds up the tile's rows [o * own, (o + 1) * own)
             const int own = 128 / S, owner = row / own;
+            if (!met) {
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                met = true;
+            }
             const bool free_ok = mbar_wait_cluster(&sm.red_free, rph ^ 1, a.status, abort_flag);
             if (!__all_sync(0xffffffffu, free_ok)) {
                 ok = false;
                 break;
             }
-            const uint32_t dst = cluster_map(sm.red, owner) + (uint32_t)((rank * NP * own + row % own) * 4);
+            const uint32_t dst = cluster_map(sm.red, owner) + (uint32_t)(((rank * NP + col0) * own + row % own) * 4);
 #pragma unroll
-            for (int c = 0; c < NP; ++c)
+            for (int c = 0; c < kCols; ++c)
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)(c * own * 4)), "f"(acc[c])
                              : "memory");
             __syncwarp();
@@ -892,7 +903,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
                 ok = false;
                 break;
             }
-            for (int i = pw * 32 + lane; i < own * NP; i += 128) {
+            for (int i = pw * 32 + lane; i < own * NP; i += 32 * C::kWarps) {
                 float v = 0.0f;
                 for (int s2 = 0; s2 < S; ++s2)
                     v += sm.red[s2 * NP * own + i];
@@ -903,6 +914,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block_few_kernel(const __
                 mbar_arrive_cluster(cluster_map(&sm.red_free, lane));
             rph ^= 1;
         }
+        if (!met)
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    if (S > 1 && warp < 2) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -924,8 +941,9 @@ cudaError_t launch_many(const Args &a, int64_t max_tiles, int sms, cudaStream_t 
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
-    const int grid = (int)(max_tiles < sms ? max_tiles : sms);
-    return launch_kernel(false, kern, dim3(grid), dim3(Cfg<TN, WG>::kThreads), smem, st, a);
+    const int64_t most = (int64_t)sms * Cfg<TN, WG>::kCtas;
+    const int grid = (int)(max_tiles < most ? max_tiles : most);
+    return launch_kernel(true, kern, dim3(grid), dim3(Cfg<TN, WG>::kThreads), smem, st, a);
 }
 
 template <int NP>
@@ -944,16 +962,18 @@ cudaError_t launch_few(const Args &a, int64_t max_tiles, int sms, cudaStream_t s
     const int64_t clusters = max_tiles < sms / S ? max_tiles : sms / S;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * S));
-    cfg.blockDim = dim3(kFewThreads);
+    cfg.blockDim = dim3(FewCfg<NP>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = S;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a, S);
 }
 

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_ker
     const float inv_h = 1.0f / (float)a.H;
     RowRing<V, NV, 2, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.residual)}};
     pdl_wait();
+    pdl_trigger();
     in.init(a.T, units, a.slots);
     float k[NV][VEC], wi[NV][VEC];
 #pragma unroll
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
     RowRing<V, NV, 4, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.w_pre ? a.residual : nullptr),
                                    static_cast<const V *>(a.dy), static_cast<const V *>(a.dz)}};
     pdl_wait();
+    pdl_trigger();
     in.init(a.T, units, a.slots);
     float c_post[NV][VEC], c_pre[NV][VEC], k[NV][VEC], wi[NV][VEC];
 #pragma unroll
@@ -388,6 +390,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restri
 {
     __shared__ float s[32][33];
     pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float acc = 0.0f;
@@ -424,12 +427,14 @@ int row_size(int row_type)
 int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // Blocks of the backward, one partial row each: as many as an SM's registers hold of rows this wide
-// (at most four), so that the partial rows stay below 10 MB.
+// (at most eight an SM: the partial rows stay below 10 MB), with four rows each where that leaves
+// every SM a block.
 int bwd_blocks(int64_t T, int H)
 {
     const int64_t n = (int64_t)152 * 8192 / H;
-    const int64_t most = n < 152 ? 152 : n > 608 ? 608 : n;
-    return (int)(T < most ? T : most);
+    const int64_t most = n < 152 ? 152 : n > 1216 ? 1216 : n;
+    const int64_t some = T < 152 ? T : T / 4 < 152 ? 152 : T / 4;
+    return (int)(some < most ? some : most);
 }
 
 constexpr int kRingBytes = 224 * 1024;  // shared memory of an SM for the rings of its blocks
@@ -448,7 +453,7 @@ cudaError_t run_ring(NormArgs a, bool bwd, int threads, int per_sm, cudaStream_t
             return err;
     }
     const int64_t most = bwd ? bwd_blocks(a.T, a.H) : (int64_t)152 * per_sm;
-    return launch_kernel(false, kern, dim3((unsigned)(a.T < most ? a.T : most)), dim3(threads), smem, st, a);
+    return launch_kernel(true, kern, dim3((unsigned)(a.T < most ? a.T : most)), dim3(threads), smem, st, a);
 }
 
 template <typename T, int VEC, int NV>
@@ -481,7 +486,7 @@ cudaError_t run_nv(const NormArgs &a, bool bwd, cudaStream_t st)
     const int most = VEC == 1 || bwd ? 256 : kMaxThreads;
     if (units <= most)
         return run<T, VEC, 1>(a, bwd, st);
-    if (units <= 2 * most)
+    if (units <= (VEC == 1 ? 512 : 2 * kMaxThreads))
         return run<T, VEC, 2>(a, bwd, st);
     if constexpr (VEC * 4 * kMaxThreads >= kMaxH) {
         return run<T, VEC, 4>(a, bwd, st);
@@ -609,7 +614,7 @@ int moe_block_norm_backward(int row_type, const void *h, const void *residual, c
     auto reduce = row_type == MOE_ROW_BF16   ? norm_reduce_kernel<__nv_bfloat16>
                   : row_type == MOE_ROW_FP16 ? norm_reduce_kernel<__half>
                                              : norm_reduce_kernel<float>;
-    return to_status(launch_kernel(false, reduce, dim3((H + 31) / 32, 2), dim3(1024), 0, st,
+    return to_status(launch_kernel(true, reduce, dim3((H + 31) / 32, 2), dim3(1024), 0, st,
                                    static_cast<const float *>(a.part), nblocks, a, dw_post, dw_pre,
                                    gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr));
 }

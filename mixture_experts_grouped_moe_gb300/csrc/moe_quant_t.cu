@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(256) quant_t_kernel(const __nv_bfloat16 *__res
 {
     __shared__ __align__(16) uint16_t tile[128 * kPitch];
     pdl_wait();
+    pdl_trigger();
     int64_t rows = R;
     if (nrows) {
         const int64_t n = *nrows;
@@ -107,7 +108,7 @@ extern "C" int moe_quantize_fp8_act_t(const void *X, int64_t ld_x, int64_t R, in
         return MOE_OK;
     const int64_t nb = (R + 127) / 128;
     const cudaError_t err =
-        launch_kernel(false, quant_t_kernel, dim3((C + kCols - 1) / kCols, (unsigned)(nb < 65535 ? nb : 65535)),
+        launch_kernel(true, quant_t_kernel, dim3((C + kCols - 1) / kCols, (unsigned)(nb < 65535 ? nb : 65535)),
                       dim3(256), 0, static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16 *>(X), ld_x,
                       sorted_ids, S, k, num_rows, R, ld_q, C, q, s);
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
