@@ -45,7 +45,8 @@ struct RowArgs {
     uint8_t *q;               // FP8 codes [P][H]
     float *s;                 // FP8 scales [H/128][P]
     float *dw;                // [T][k]
-    int64_t token_blocks;     // blocks below this walk tokens, the others padding rows
+    int64_t token_blocks;     // blocks that walk tokens
+    int64_t pad_blocks;       // blocks before them that zero padding rows (first, so that both run at once)
 };
 
 // Lane j < k of the warp gets the position of the token's slot j (-1 for none).
@@ -93,15 +94,15 @@ template <typename V>
 __global__ void __launch_bounds__(kThreads) permute_kernel(const RowArgs a, int64_t units, int64_t ld_units, V zero)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t warp = (blockIdx.x - a.pad_blocks) * kWarps + (threadIdx.x >> 5);
     constexpr int seg = 32 * kUnits;
     V *dst = static_cast<V *>(a.dst);
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x >= a.token_blocks) {
+    if (warp < 0) {
         const int64_t npp = *a.npp;
         zero_padding(a.sorted_ids, npp < a.P ? npp : a.P, a.T * a.k, units, seg, dst, zero,
-                     warp - a.token_blocks * kWarps, ((int64_t)gridDim.x - a.token_blocks) * kWarps, lane);
+                     warp + a.pad_blocks * kWarps, a.pad_blocks * kWarps, lane);
         return;
     }
     const int64_t nseg = (units + seg - 1) / seg;
@@ -151,34 +152,57 @@ __device__ __forceinline__ void divide16(float (&f)[16], float sc)
 }
 
 // A warp quantises 512 columns of one token's row (a group of 128 columns on 8 lanes, 16 columns
-// per lane), once, and writes the codes and scales to the token's k positions.
-__global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
+// per lane), once, and writes the codes and scales to the token's k positions.  The next item's loads
+// are issued before this one is encoded.
+__global__ void __launch_bounds__(kThreads, 4) permute_fp8_kernel(const RowArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t warp = (blockIdx.x - a.pad_blocks) * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_trigger();
     const int64_t units = a.H / 16;
-    if (blockIdx.x >= a.token_blocks) {
+    if (warp < 0) {
         const int64_t npp = *a.npp;
         zero_padding(a.sorted_ids, npp < a.P ? npp : a.P, a.T * a.k, units, 32 * kUnits,
-                     reinterpret_cast<uint4 *>(a.q), make_uint4(0, 0, 0, 0), warp - a.token_blocks * kWarps,
-                     ((int64_t)gridDim.x - a.token_blocks) * kWarps, lane, a.s, a.P);
+                     reinterpret_cast<uint4 *>(a.q), make_uint4(0, 0, 0, 0), warp + a.pad_blocks * kWarps,
+                     a.pad_blocks * kWarps, lane, a.s, a.P);
         return;
     }
-    const int64_t nseg = (units + 31) / 32;
-    const int64_t total = nseg * a.T;
-    for (int64_t item = warp; item < total; item += a.token_blocks * kWarps) {
-        const int64_t t = item / nseg;
-        const int64_t u = item % nseg * 32 + lane;
-        const int pos = lane_pos(a, t, lane);
+    const int nseg = (int)((units + 31) / 32);
+    const int64_t step = a.token_blocks * kWarps;
+    int64_t t = warp / nseg;
+    int seg = (int)(warp % nseg);
+    const int64_t step_t = step / nseg;
+    const int step_seg = (int)(step % nseg);
+    uint4 raw[2] = {};
+    int pos = -1;
+    auto load = [&]() {
+        if (t >= a.T)
+            return;
+        const int64_t u = (int64_t)seg * 32 + lane;
+        pos = lane_pos(a, t, lane);
+        if (u < units) {
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.src) + t * a.ld_src) + 2 * u;
+            raw[0] = __ldg(src);
+            raw[1] = __ldg(src + 1);
+        }
+    };
+    load();
+    while (t < a.T) {
+        const int64_t u = (int64_t)seg * 32 + lane;
+        const uint32_t w8[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+        const int cur = pos;
+        t += step_t;
+        seg += step_seg;
+        if (seg >= nseg) {
+            seg -= nseg;
+            ++t;
+        }
+        load();
         float f[16];
         float amax = 0.0f;
         if (u < units) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.src) +
-                                                               t * a.ld_src) + 2 * u;
-            uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
-            const uint32_t w8[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 unpack_word(w8[i], f[2 * i], f[2 * i + 1], __nv_bfloat16{});
@@ -202,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) permute_fp8_kernel(const RowArgs a)
             }
         }
         for (int j = 0; j < a.k; ++j) {
-            const int p = __shfl_sync(0xffffffffu, pos, j);
+            const int p = __shfl_sync(0xffffffffu, cur, j);
             if (p < 0 || u >= units)
                 continue;
             *reinterpret_cast<uint4 *>(a.q + (int64_t)p * a.H + 16 * u) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -277,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 4) unpermute_bwd_kernel(const RowArg
     V *dys = static_cast<V *>(a.dst);
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x >= a.token_blocks) {
+    if (blockIdx.x < a.pad_blocks) {
         const int64_t npp = *a.npp;
         zero_padding(a.sorted_ids, npp < a.P ? npp : a.P, a.T * a.k, units, 32 * kUnits, dys, piece_zero<T, VEC>(),
-                     (blockIdx.x - a.token_blocks) * kWarps + w, ((int64_t)gridDim.x - a.token_blocks) * kWarps, lane);
+                     (int64_t)blockIdx.x * kWarps + w, a.pad_blocks * kWarps, lane);
         return;
     }
     const V *ys = static_cast<const V *>(a.ys);
-    for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.T; t0 += a.token_blocks * TPB) {
+    for (int64_t t0 = (blockIdx.x - a.pad_blocks) * TPB; t0 < a.T; t0 += a.token_blocks * TPB) {
         const int64_t t = t0 + tok;
         s_dot[w][lane] = 0.0f;
         __syncwarp();
@@ -368,7 +392,8 @@ cudaError_t run_permute(RowArgs &a, int64_t row_bytes, int es, bool zero, cudaSt
     const int64_t units = row_bytes / sizeof(V);
     const int seg = 32 * kUnits;
     a.token_blocks = blocks_for((units + seg - 1) / seg * a.T);
-    const int grid = (int)a.token_blocks + pad_blocks(zero, a.P, units, seg);
+    a.pad_blocks = pad_blocks(zero, a.P, units, seg);
+    const int grid = (int)(a.token_blocks + a.pad_blocks);
     return launch_kernel(true, permute_kernel<V>, dim3(grid), dim3(kThreads), 0, st, a, units,
                          a.ld_src * es / (int64_t)sizeof(V), V{});
 }
@@ -387,7 +412,8 @@ cudaError_t run_bwd_w(RowArgs &a, bool zero, cudaStream_t st)
 {
     const int64_t units = a.H / VEC;
     a.token_blocks = blocks_for((int64_t)a.T * WPT);
-    const int grid = (int)a.token_blocks + pad_blocks(zero, a.P, units, 32 * kUnits);
+    a.pad_blocks = pad_blocks(zero, a.P, units, 32 * kUnits);
+    const int grid = (int)(a.token_blocks + a.pad_blocks);
     return launch_kernel(true, unpermute_bwd_kernel<T, VEC, WPT>, dim3(grid), dim3(kThreads), 0, st, a, units,
                          a.ld_src / VEC);
 }
@@ -498,8 +524,10 @@ int moe_permute_fp8(const void *x, int64_t ld_x, const int32_t *slot_pos, const 
     RowArgs a = {};
     a.src = x, a.ld_src = ld_x, a.slot_pos = slot_pos, a.sorted_ids = sorted_ids, a.npp = num_tokens_post_padded;
     a.T = T, a.k = k, a.H = H, a.P = P, a.q = q, a.s = s;
-    a.token_blocks = blocks_for((H / 16 + 31) / 32 * (int64_t)T);
-    const int grid = (int)a.token_blocks + pad_blocks(zero_padding, P, H / 16, 32 * kUnits);
+    const int64_t blocks = blocks_for((H / 16 + 31) / 32 * (int64_t)T);
+    a.token_blocks = blocks < 152 * 4 ? blocks : 152 * 4;  // as many as are resident: the others' loads pipeline
+    a.pad_blocks = pad_blocks(zero_padding, P, H / 16, 32 * kUnits);
+    const int grid = (int)(a.token_blocks + a.pad_blocks);
     return to_status(launch_kernel(true, permute_fp8_kernel, dim3(grid), dim3(kThreads), 0,
                                    static_cast<cudaStream_t>(stream), a));
 }

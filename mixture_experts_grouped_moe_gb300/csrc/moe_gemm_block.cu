@@ -82,23 +82,17 @@ __device__ __forceinline__ void scaled_ffma2(float &acc0, float &acc1, float v0,
         : "f"(v0), "f"(v1), "f"(s.x), "f"(s.y), "f"(f));
 }
 
-// 32 lanes x 32 columns of TMEM as two 16-lane halves, and the wait for them.  Lane l of the warp gets
+// 32 lanes x 16 columns of TMEM as two 16-lane halves, and the wait for them.  Lane l of the warp gets
 // of half h (v: TMEM lanes 0-15 from taddr on, u: lanes 16-31), group g of 8 columns: elements 4 g, 4 g + 1
 // at (row l / 4, columns 8 g + 2 (l % 4) and the next), 4 g + 2, 4 g + 3 eight rows below.
-__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&v)[16], float (&u)[16])
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&v)[8], float (&u)[8])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15},"
-        " [%32];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
-        " [%33];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-          "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7]),
-          "=f"(u[8]), "=f"(u[9]), "=f"(u[10]), "=f"(u[11]), "=f"(u[12]), "=f"(u[13]), "=f"(u[14]), "=f"(u[15])
+          "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7])
         : "r"(taddr), "r"(taddr + (16u << 16))
         : "memory");
 }
@@ -148,7 +142,7 @@ __device__ __forceinline__ void cluster_meet()
 // eight for promotion and epilogue (two per TMEM lane quadrant, half of the columns each).  A weight
 // gradient has a second warp that copies the scales and a spare one (so that the promotion warps start
 // a group of four), and its first four warps hand registers to the other eight (setmaxnreg): 128
-// threads x 56 + 256 x 224 = 64512 = 384 x 168, all that the block is launched with.
+// threads x 72 + 256 x 216 = 64512 = 384 x 168, all that the block is launched with.
 
 template <int TN, bool WG>
 struct Cfg {
@@ -166,7 +160,7 @@ struct Cfg {
 };
 
 constexpr int kPromoWarps = 8;
-constexpr int kFewRegs = 56, kPromoRegs = 224;
+constexpr int kFewRegs = 72, kPromoRegs = 216;
 static_assert(128 * kFewRegs + 32 * kPromoWarps * kPromoRegs <= 384 * 168, "within the launch's registers");
 constexpr int kGroupM = 16;  // row tiles that walk the column tiles together
 constexpr int kMaxE = 1024;
@@ -265,21 +259,54 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
 
     auto get_tile = [&](int t) {
         Tile tl;
-        int within = WG ? t % (nmt * nnt) : t;
+        int within = t;
         const int group = within / (kGroupM * nnt);
         within -= group * kGroupM * nnt;
         const int gsize = min(kGroupM, nmt - group * kGroupM);
         tl.row0 = (int64_t)(group * kGroupM + within % gsize) * 128;
         tl.col0 = within / gsize * TN;
-        if (WG) {
-            tl.e = t / (nmt * nnt);
-            tl.kb0 = min(sm.off[tl.e], KB);
-            tl.kb1 = min(sm.off[tl.e + 1], KB);
-        } else {
-            tl.e = expert_of(a, tl.row0);
-            tl.kb0 = kSplits ? KB * rank / S : 0;
-            tl.kb1 = kSplits ? KB * (rank + 1) / S : KB;
+        tl.e = expert_of(a, tl.row0);
+        tl.kb0 = kSplits ? KB * rank / S : 0;
+        tl.kb1 = kSplits ? KB * (rank + 1) / S : KB;
+        return tl;
+    };
+
+    // The same order for a weight gradient, whose tiles are few blocks of K: a walk keeps its place instead of
+    // the tile's number, which taken apart by divisions costs every role about 1000 cycles a tile.
+    struct Walk {
+        int e, group, pos;
+    };
+    auto settle = [&](Walk &w) {  // carry pos over into the next groups and experts
+        for (;;) {
+            const int count = min(kGroupM, nmt - w.group * kGroupM) * nnt;
+            if (w.pos < count || w.e >= a.E)
+                return;
+            w.pos -= count;
+            if (++w.group * kGroupM >= nmt) {
+                w.group = 0;
+                ++w.e;
+            }
         }
+    };
+    auto start = [&]() {
+        Walk w = {0, 0, first};
+        if (ntiles > 0)
+            settle(w);
+        return w;
+    };
+    auto advance = [&](Walk &w) {
+        w.pos += step;
+        settle(w);
+    };
+    auto tile_at = [&](const Walk &w) {
+        Tile tl;
+        const int gsize = min(kGroupM, nmt - w.group * kGroupM);
+        const int col = gsize == kGroupM ? w.pos / kGroupM : w.pos / gsize;
+        tl.row0 = (int64_t)(w.group * kGroupM + w.pos - col * gsize) * 128;
+        tl.col0 = col * TN;
+        tl.e = w.e;
+        tl.kb0 = min(sm.off[tl.e], KB);
+        tl.kb1 = min(sm.off[tl.e + 1], KB);
         return tl;
     };
 
@@ -303,8 +330,9 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
             // so it reads 32 column scales, and its pairs of columns leave as whole 32-byte sectors
             // without passing through shared memory.
             const int r0 = q * 32 + (lane >> 2), c2 = 2 * (lane & 3);
-            for (int t = first; t < ntiles; t += step) {
-                const Tile tl = get_tile(t);
+            Walk w = start();
+            for (int t = first; t < ntiles; t += step, advance(w)) {
+                const Tile tl = tile_at(w);
                 float acc[2][kCols / 2];  // [half][4 g + i]
 #pragma unroll
                 for (int i = 0; i < kCols / 2; ++i)
@@ -325,15 +353,12 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
                     tc_fence_after();
                     const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * TN + sub * kCols;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32) {
-                        float v[16], u[16];
-                        float2 x[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            x[g] = s2[(c + 8 * g) / 2];
+                    for (int c = 0; c < kCols; c += 16) {
+                        float v[8], u[8];
+                        const float2 x[2] = {s2[c / 2], s2[c / 2 + 4]};
                         tmem_ld_halves(tb + c, v, u);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int g = 0; g < 2; ++g) {
                             const int i = 4 * g, o = c / 2 + i;
                             scaled_ffma2(acc[0][o], acc[0][o + 1], v[i], v[i + 1], x[g], f[0]);
                             scaled_ffma2(acc[0][o + 2], acc[0][o + 3], v[i + 2], v[i + 3], x[g], f[1]);
@@ -566,8 +591,17 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
             uint32_t issued = 0;  // stages with a copy issued, and its phase
             uint32_t issued_ph = 0;
             bool ok = true;
+            Walk w = {};
+            if (WG)
+                w = start();
             for (int t = first; ok && t < ntiles; t += step) {
-                const Tile tl = get_tile(t);
+                Tile tl;
+                if (WG) {
+                    tl = tile_at(w);
+                    advance(w);
+                } else {
+                    tl = get_tile(t);
+                }
                 const int brow = WG ? tl.col0 : tl.e * a.N + tl.col0;
                 for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
                     if (!mbar_wait(&sm.empty[s], ph ^ 1, a.status, abort_flag)) {
@@ -605,8 +639,17 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
             uint32_t ph = 0, bph = 0;
             bool ok = true, any = false;
             const uint32_t idesc = make_idesc(0, 0, 128, TN);
+            Walk w = {};
+            if (WG)
+                w = start();
             for (int t = first; ok && t < ntiles; t += step) {
-                const Tile tl = get_tile(t);
+                Tile tl;
+                if (WG) {
+                    tl = tile_at(w);
+                    advance(w);
+                } else {
+                    tl = get_tile(t);
+                }
                 bool loaded = false;
                 for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
                     if ((!loaded && !mbar_wait(&sm.full[s], ph, a.status, abort_flag)) ||
@@ -651,8 +694,9 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
         int ss = 0;
         uint32_t sph = 0;
         bool ok = true;
-        for (int t = first; ok && t < ntiles; t += step) {
-            const Tile tl = get_tile(t);
+        Walk w = start();
+        for (int t = first; ok && t < ntiles; t += step, advance(w)) {
+            const Tile tl = tile_at(w);
             const float *sa = a.sa + (tl.row0 + lane) * a.sa_row + tl.kb0 * a.sa_blk;
             const int left = (int)min((int64_t)128, a.M - tl.row0);
             const float *sb = a.sb + tl.col0 + 4 * lane + (int64_t)tl.kb0 * a.N;
