@@ -639,3 +639,120 @@ class FusedMoE:
 
     def status(self, stream=None) -> int:
         return moe_workspace_status(self.ws, stream)
+
+
+class FP8Weights:
+    """Block-quantised weights of one product, [E][N][K] (E = 1: a dense layer): the e4m3 codes and the
+    128 x 128 scales, and with `training` the transposed ones that the input gradient multiplies by.
+
+    N and K are multiples of 128 (moe_quantize_fp8_weights).  Owns the products' workspace."""
+
+    def __init__(self, W, training=False):
+        import torch
+        if W.dtype != torch.bfloat16 or W.dim() != 3 or not W.is_contiguous():
+            raise ValueError("expected contiguous bf16 weights [E][N][K]")
+        self.E, self.N, self.K = W.shape
+        self.ws = torch.zeros(MOE_GEMM_BLOCK_WS_BYTES, dtype=torch.uint8, device=W.device)
+        self.training = training
+        self.update(W)
+
+    @staticmethod
+    def _quantise(W):
+        import torch
+        E, N, K = W.shape
+        q = torch.empty(E, N, K, dtype=torch.uint8, device=W.device)
+        s = torch.empty(E, N // 128, K // 128, dtype=torch.float32, device=W.device)
+        moe_quantize_fp8_weights(W, E * N, K, q, s)
+        return q, s
+
+    def update(self, W):
+        """Quantise the weights anew (after an optimiser step)."""
+        self.q, self.s = self._quantise(W)
+        if self.training:  # the same blocks, transposed: the same codes and scales
+            self.qt = self.q.transpose(1, 2).contiguous()
+            self.st = self.s.transpose(1, 2).contiguous()
+
+    def _product(self, a, a_scale, by_block, q, s, N, K, exchange, out, out_dtype, stream):
+        import torch
+        if a.dim() != 2 or a.shape[1] != K or not a.is_contiguous():
+            raise ValueError(f"expected contiguous rows of {K} codes, got {tuple(a.shape)}")
+        M = a.shape[0]
+        if (exchange is None) != (self.E == 1) or (exchange is not None and M != exchange.P):
+            raise ValueError("several experts take sorted rows [P] and the exchange that sorted them")
+        if out is None:
+            out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=a.device)
+        g = (0, None, None) if exchange is None else (exchange.block_m, exchange.expert_ids,
+                                                      exchange.num_tokens_post_padded)
+        moe_gemm_fp8_block(a, a_scale, int(by_block), q, s, M, N, K, self.E, *g, _row_type(out.dtype), out,
+                           out.stride(0), self.ws, self.ws.numel(), stream)
+        return out
+
+    def product(self, a, a_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
+        """rows [M][K] (codes, scales) times W^T -> [M][N]; with several experts, each sorted row times its
+        expert's."""
+        return self._product(a, a_scale, by_block, self.q, self.s, self.N, self.K, exchange, out, out_dtype, stream)
+
+    def input_gradient(self, d, d_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
+        """rows [M][N] of an output gradient times W -> [M][K]."""
+        return self._product(d, d_scale, by_block, self.qt, self.st, self.K, self.N, exchange, out, out_dtype, stream)
+
+    def weight_gradient(self, d, d_scale, x, x_scale, exchange=None, out=None, accumulate=False, stream=None):
+        """(d [N][P], x [K][P], as moe_quantize_fp8_act_t gives them) -> fp32 [E][N][K]."""
+        import torch
+        if out is None:
+            out = torch.empty(self.E, self.N, self.K, dtype=torch.float32, device=d.device)
+        moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E,
+                            None if exchange is None else exchange.expert_counts, out, int(accumulate), self.ws,
+                            self.ws.numel(), stream)
+        return out
+
+    def status(self, stream=None) -> int:
+        return moe_workspace_status(self.ws, stream)
+
+
+class BlockNorm:
+    """The norms before and after one block, with its gate and residual scale, for rows of one shape:
+    forward(), then backward() (see moe_block_norm in include/moe.h).  Owns the kept statistics and the
+    backward's workspace."""
+
+    def __init__(self, T, H, gate_kind=MOE_GATE_NONE, scale=1.0, weight_offset=0.0, eps=1e-6, device="cuda"):
+        import torch
+        self.T, self.H, self.gate_kind = T, H, gate_kind
+        self.scale, self.weight_offset, self.eps = scale, weight_offset, eps
+        self.rstd_h, self.rstd_y = (torch.empty(T, dtype=torch.float32, device=device) for _ in range(2))
+        self.ws_bytes = moe_block_norm_workspace_size(T, H)
+        if self.ws_bytes == 0:
+            raise MoEError("moe_block_norm_workspace_size", MOE_ERR_INVALID_ARG)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    def _rows(self, **tensors):
+        for name, t in tensors.items():
+            if t is not None and (tuple(t.shape) != (self.T, self.H) or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous rows {(self.T, self.H)}, got {tuple(t.shape)}")
+
+    def forward(self, h, residual, w_post=None, w_pre=None, gate=None, y=None, z=None, stream=None):
+        """Returns (y, z): the residual stream after the block and the next block's input (None without w_pre)."""
+        import torch
+        y = torch.empty_like(h) if y is None else y
+        z = torch.empty_like(h) if z is None and w_pre is not None else z
+        self._rows(h=h, residual=residual, y=y, z=z)
+        moe_block_norm(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
+                       self.scale, self.weight_offset, self.eps, y, z, self.rstd_h, self.rstd_y, stream)
+        return y, z
+
+    def backward(self, h, residual, dy, dz, w_post=None, w_pre=None, gate=None, stream=None):
+        """Returns dict d_residual, dh, dgate, dw_post, dw_pre (None where there is no such input)."""
+        import torch
+        self._rows(h=h, residual=residual, dy=dy, dz=dz)
+        dev, f32 = h.device, torch.float32
+        shape = {MOE_GATE_NONE: None, MOE_GATE_CHANNEL: (self.H,), MOE_GATE_TOKEN: (self.T,),
+                 MOE_GATE_FULL: (self.T, self.H)}[self.gate_kind]
+        g = {"d_residual": torch.empty_like(h), "dh": torch.empty_like(h),
+             "dgate": None if shape is None else torch.empty(
+                 shape, dtype=h.dtype if self.gate_kind == MOE_GATE_FULL else f32, device=dev),
+             "dw_post": None if w_post is None else torch.empty(self.H, dtype=f32, device=dev),
+             "dw_pre": None if w_pre is None else torch.empty(self.H, dtype=f32, device=dev)}
+        moe_block_norm_backward(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
+                                self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
+                                g["dh"], g["dgate"], g["dw_post"], g["dw_pre"], self.ws, self.ws_bytes, stream)
+        return g
