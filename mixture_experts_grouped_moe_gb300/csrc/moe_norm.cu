@@ -272,12 +272,24 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
         for (int c = 0; c < VEC; ++c)
             c_post[i][c] = c_pre[i][c] = 0.0f;
     }
+    // the next row's statistics and gate, fetched a row ahead
+    float next_rh = 1.0f, next_ry = 0.0f, next_gate = 1.0f;
+    auto fetch_row = [&](int64_t t) {
+        if (t >= a.T)
+            return;
+        if (a.w_post)
+            next_rh = a.r_h[t];
+        if (a.w_pre)
+            next_ry = a.r_y[t];
+        if (a.gate_kind == MOE_GATE_TOKEN)
+            next_gate = row_to_f(static_cast<const T *>(a.gate)[t]);
+    };
+    fetch_row(blockIdx.x);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * units;
         in.wait();
-        const float r_h = a.w_post ? a.r_h[t] : 1.0f;
-        const float r_y = a.w_pre ? a.r_y[t] : 0.0f;
-        const float gate = a.gate_kind == MOE_GATE_TOKEN ? row_to_f(static_cast<const T *>(a.gate)[t]) : 1.0f;
+        const float r_h = next_rh, r_y = next_ry, gate = next_gate;
+        fetch_row(t + gridDim.x);
         // (y is formed in both passes: kept in registers next to the column sums it would spill)
         float m1 = 0.0f;
         if (a.w_pre) {
