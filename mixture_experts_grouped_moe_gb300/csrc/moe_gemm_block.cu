@@ -1037,6 +1037,26 @@ __global__ void __launch_bounds__(FewCfg<NP>::kThreads, 1) gemm_block_few_kernel
 
 // ------------------------------------------------------------- launches
 
+// What a 64-column product of `tiles` tiles costs, in 10 ns: a block of K about 0.33 us a wave at one CTA an SM
+// and 0.52 at two; the meeting of a split tile's CTAs 2.5 us.  *S: the CTAs that share a tile (each a part of
+// K, four blocks at least) at the lowest cost.  (128 x 4096 x 14336: 49.9 us without a split, 32.9 with two CTAs
+// a tile, 23.9 with four; 256 x 4096 x 4096: 15.3 without, 17.1 with two.)
+int64_t cost64(int64_t tiles, int KB, int sms, int *S)
+{
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 8; s *= 2) {
+        if (s > 1 && (tiles * s > 2 * sms || KB / s < 4))
+            break;
+        const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
+        const int64_t cost = waves * ((KB + s - 1) / s) * (tiles * s <= sms ? 33 : 52) + (s > 1 ? 250 : 0);
+        if (cost < best) {
+            best = cost;
+            *S = s;
+        }
+    }
+    return best;
+}
+
 // `clusters` clusters of S CTAs.
 cudaError_t launch_cluster(void (*kern)(Args, int), const Args &a, int S, int64_t clusters, int threads, size_t smem,
                            cudaStream_t st)
@@ -1069,12 +1089,8 @@ cudaError_t launch_many(const Args &a, int64_t max_tiles, int sms, cudaStream_t 
         return err;
     const int64_t most = (int64_t)sms * Cfg<TN, WG>::kCtas;
     if (TN == 64 && !WG) {
-        // few tiles: K split over as many CTAs as there are SMs, four blocks each at least (two an SM:
-        // 256 x 4096 x 4096 in 17.1 instead of 15.3 us)
-        const int KB = (a.K + 127) / 128;
         int S = 1;
-        while (S < 8 && max_tiles * 2 * S <= sms && KB / (2 * S) >= 4)
-            S *= 2;
+        cost64(max_tiles, (a.K + 127) / 128, sms, &S);
         return launch_cluster(kern, a, S, max_tiles < most / S ? max_tiles : most / S, Cfg<TN, WG>::kThreads, smem, st);
     }
     const int grid = (int)(max_tiles < most ? max_tiles : most);
@@ -1095,6 +1111,18 @@ cudaError_t launch_few(const Args &a, int64_t max_tiles, int sms, cudaStream_t s
     while (S < 8 && max_tiles * 2 * S <= sms && KB / (2 * S) >= 4)
         S *= 2;
     return launch_cluster(kern, a, S, max_tiles < sms / S ? max_tiles : sms / S, FewCfg<NP>::kThreads, smem, st);
+}
+
+// Columns of a tile.  A block of K costs a wave of tiles about 0.58 us with 256 columns and 0.40 with 128; 64 as
+// above.  The cheapest is taken.  (us at 256 / 128 / 64 columns: 1024 x 4096 x 4096 21.1 / 29.5 / 34.1,
+// 512 x 14336 x 4096 38.2 / 42.4 / 50.4, 1000 x 1416 x 2000 15.0 / 10.9 / 13.7.)
+int column_tile(int64_t row_tiles, int N, int KB, int sms)
+{
+    const auto waves = [&](int tn) { return (row_tiles * ((N + tn - 1) / tn) + sms - 1) / sms; };
+    const int64_t c256 = 58 * waves(256) * KB, c128 = 40 * waves(128) * KB;
+    int S;
+    const int64_t c64 = cost64(row_tiles * ((N + 63) / 64), KB, sms, &S);
+    return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
 }
 
 int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -1151,8 +1179,7 @@ int moe_gemm_fp8_block(const uint8_t *A, const float *a_scale, int a_scale_by_bl
     const auto st = static_cast<cudaStream_t>(stream);
     const int few = grouped ? (block_m < 128 ? block_m : 0) : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 0;
     const int64_t nmt = (M + 127) / 128;
-    // the widest column tile that still gives every SM a tile
-    const int tn = few ? 128 : nmt * ((N + 255) / 256) >= sms ? 256 : nmt * ((N + 127) / 128) >= sms ? 128 : 64;
+    const int tn = few ? 128 : column_tile(nmt, N, (K + 127) / 128, sms);
     if (!encode_tmap_2d(&a.tm_a, A, 1, K, M, 128, few ? few : 128) ||
         !encode_tmap_2d(&a.tm_b, B, 1, K, (uint64_t)E * N, 128, tn < 128 ? tn : 128))
         return MOE_ERR_CUDA;
@@ -1197,7 +1224,10 @@ int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B
     a.status = static_cast<int *>(ws);
     const auto st = static_cast<cudaStream_t>(stream);
     const int64_t nmt = ((int64_t)M + 127) / 128;
-    const int tn = nmt * ((N + 255) / 256) * E >= sms ? 256 : nmt * ((N + 127) / 128) * E >= sms ? 128 : 64;
+    // Wide tiles for many, narrower ones where those would leave SMs idle (us at 256 / 128 / 64 columns: 4096 x
+    // 14336 of eight experts 841 / 912 / 1356, 1024 x 2048 of eight 24.6 / 22.5 / 28.3, 512 x 1024 of four
+    // 8.2 / 6.2 / 6.8, 256 x 512 of one over 4000 tokens 28.0 / 17.7 / 16.4).
+    const int tn = nmt * ((N + 255) / 256) * E >= 4 * sms ? 256 : nmt * ((N + 127) / 128) * E >= sms / 2 ? 128 : 64;
     // P = 0: no block to read (the maps need at least one row)
     const uint64_t inner = P > 0 ? P : 128;
     if (!encode_tmap_2d(&a.tm_a, A, 1, inner, M, 128, 128) ||
