@@ -478,7 +478,40 @@ class MoETrain:
 
 def _row_type(dtype):
     import torch
-    return {torch.bfloat16: MOE_ROW_BF16, torch.float16: MOE_ROW_FP16, torch.float32: MOE_ROW_FP32}[dtype]
+    types = {torch.bfloat16: MOE_ROW_BF16, torch.float16: MOE_ROW_FP16, torch.float32: MOE_ROW_FP32}
+    if dtype not in types:
+        raise TypeError(f"rows are bf16, fp16 or fp32, not {dtype}")
+    return types[dtype]
+
+
+def _expect(name, t, shape, *dtypes):
+    """t (None passes) is contiguous, of that shape and of one of those types."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {tuple(shape)}, got {tuple(t.shape)} with strides {t.stride()}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+
+
+def _output(name, t, shape, dtype, device, stream):
+    """t after its checks, or a new tensor that belongs to the stream that will write it."""
+    import contextlib
+    import torch
+    if t is not None:
+        _expect(name, t, shape, dtype)
+        return t
+    if stream is None:
+        scope = contextlib.nullcontext()
+    else:
+        scope = torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    with scope:
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _codes():
+    import torch
+    return torch.uint8, torch.float8_e4m3fn
 
 
 class TokenExchange:
@@ -503,15 +536,29 @@ class TokenExchange:
         self.weights = None
 
     def sort(self, topk_ids, topk_weights, stream=None):
+        """topk_ids int32 [T][k] (outside [0, E): the slot is left out), topk_weights fp32 [T][k]: kept, for
+        unpermute and its gradient."""
+        import torch
+        _expect("topk_ids", topk_ids, (self.T, self.k), torch.int32)
+        _expect("topk_weights", topk_weights, (self.T, self.k), torch.float32)
         moe_align_sort_map(topk_ids, topk_weights, self.T, self.k, self.E, self.block_m, self.sorted_ids,
                            self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
                            self.slot_pos, self.ws, self.ws_bytes, stream)
         self.weights = topk_weights
 
     def _rows(self, x):
-        if x.dim() != 2 or x.shape[0] != self.T or x.stride(1) != 1:
+        if x.dim() != 2 or x.shape[0] != self.T or (x.shape[1] > 1 and x.stride(1) != 1):
             raise ValueError(f"expected {self.T} rows with contiguous elements, got {tuple(x.shape)}")
-        return x.shape[1], x.stride(0)
+        # (a single row's stride means nothing to torch, which may give any)
+        return x.shape[1], x.shape[1] if self.T == 1 else x.stride(0)
+
+    def _token_rows(self, name, t, H, dtype, device, stream):
+        """Token rows to write [T][H]: t (rows may be strided) after its checks, or new."""
+        t = _output(name, None, (self.T, H), dtype, device, stream) if t is None else t
+        h, ld = self._rows(t)
+        if h != H or t.dtype != dtype:
+            raise ValueError(f"{name}: expected {dtype} rows of {H}, got {t.dtype} rows of {h}")
+        return t, ld
 
     def _sorted(self, ys):
         if ys.dim() != 2 or ys.shape[0] != self.P or not ys.is_contiguous():
@@ -520,10 +567,8 @@ class TokenExchange:
 
     def permute(self, x, xs=None, zero_padding=True, stream=None):
         """x [T][H] -> sorted rows [P][H]."""
-        import torch
         H, ld = self._rows(x)
-        xs = torch.empty(self.P, H, dtype=x.dtype, device=x.device) if xs is None else xs
-        self._sorted(xs)
+        xs = _output("xs", xs, (self.P, H), x.dtype, x.device, stream)
         moe_permute(_row_type(x.dtype), x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T,
                     self.k, H, self.P, int(zero_padding), xs, stream)
         return xs
@@ -534,28 +579,30 @@ class TokenExchange:
         H, ld = self._rows(x)
         if x.dtype != torch.bfloat16:
             raise TypeError("permute_fp8 takes bf16 rows")
-        q = torch.empty(self.P, H, dtype=torch.uint8, device=x.device) if q is None else q
-        s = torch.empty(H // 128, self.P, dtype=torch.float32, device=x.device) if s is None else s
+        if q is not None:
+            _expect("q", q, (self.P, H), *_codes())
+        else:
+            q = _output("q", None, (self.P, H), torch.uint8, x.device, stream)
+        s = _output("s", s, (H // 128, self.P), torch.float32, x.device, stream)
         moe_permute_fp8(x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T, self.k, H, self.P,
                         int(zero_padding), q, s, stream)
         return q, s
 
     def unpermute(self, ys, out=None, weights=True, stream=None):
         """Sorted rows [P][H] -> [T][H], each token's rows summed with its top-k weights (or 1)."""
-        import torch
         H = self._sorted(ys)
-        out = torch.empty(self.T, H, dtype=ys.dtype, device=ys.device) if out is None else out
+        out, ld = self._token_rows("out", out, H, ys.dtype, ys.device, stream)
         moe_unpermute(_row_type(ys.dtype), ys, self.slot_pos, self.weights if weights else None, self.T, self.k, H,
-                      self.P, out, self._rows(out)[1], stream)
+                      self.P, out, ld, stream)
         return out
 
     def unpermute_backward(self, dout, ys, zero_padding=True, stream=None):
         """Gradients of unpermute: (dys [P][H], dweights [T][k] fp32)."""
         import torch
         H, ld = self._rows(dout)
-        self._sorted(ys)
-        dys = torch.empty_like(ys)
-        dw = torch.empty(self.T, self.k, dtype=torch.float32, device=ys.device)
+        _expect("ys", ys, (self.P, H), dout.dtype)
+        dys = _output("dys", None, (self.P, H), ys.dtype, ys.device, stream)
+        dw = _output("dweights", None, (self.T, self.k), torch.float32, ys.device, stream)
         moe_unpermute_backward(_row_type(ys.dtype), dout, ld, ys, self.slot_pos, self.weights, self.sorted_ids,
                                self.num_tokens_post_padded, self.T, self.k, H, self.P, int(zero_padding), dys, dw,
                                stream)
@@ -563,12 +610,11 @@ class TokenExchange:
 
     def permute_backward(self, dxs, dx=None, stream=None):
         """Gradient of permute: sorted rows [P][H] -> [T][H]."""
-        import torch
         H = self._sorted(dxs)
-        dx = torch.empty(self.T, H, dtype=dxs.dtype, device=dxs.device) if dx is None else dx
-        moe_permute_backward(_row_type(dxs.dtype), dxs, self.slot_pos, self.T, self.k, H, self.P, dx,
-                             self._rows(dx)[1], stream)
+        dx, ld = self._token_rows("dx", dx, H, dxs.dtype, dxs.device, stream)
+        moe_permute_backward(_row_type(dxs.dtype), dxs, self.slot_pos, self.T, self.k, H, self.P, dx, ld, stream)
         return dx
+
 
 class FusedMoE:
     """Owns the workspace for one layer shape and calls moe_fused_forward.
@@ -677,14 +723,19 @@ class FP8Weights:
         if a.dim() != 2 or a.shape[1] != K or not a.is_contiguous():
             raise ValueError(f"expected contiguous rows of {K} codes, got {tuple(a.shape)}")
         M = a.shape[0]
-        if (exchange is None) != (self.E == 1) or (exchange is not None and M != exchange.P):
+        if (exchange is None) != (self.E == 1) or (exchange is not None and (M, self.E) != (exchange.P, exchange.E)):
             raise ValueError("several experts take sorted rows [P] and the exchange that sorted them")
-        if out is None:
-            out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=a.device)
+        _expect("codes", a, (M, K), *_codes())
+        KB = -(-K // 128)
+        _expect("scales", a_scale, (KB, M) if by_block else (M, KB), torch.float32)
+        dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"products are bf16 or fp32, not {dtype}")
+        out = _output("out", out, (M, N), dtype, a.device, stream)
         g = (0, None, None) if exchange is None else (exchange.block_m, exchange.expert_ids,
                                                       exchange.num_tokens_post_padded)
         moe_gemm_fp8_block(a, a_scale, int(by_block), q, s, M, N, K, self.E, *g, _row_type(out.dtype), out,
-                           out.stride(0), self.ws, self.ws.numel(), stream)
+                           N, self.ws, self.ws.numel(), stream)
         return out
 
     def product(self, a, a_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
@@ -694,13 +745,27 @@ class FP8Weights:
 
     def input_gradient(self, d, d_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
         """rows [M][N] of an output gradient times W -> [M][K]."""
+        if not self.training:
+            raise ValueError("the input gradient needs FP8Weights(..., training=True)")
         return self._product(d, d_scale, by_block, self.qt, self.st, self.K, self.N, exchange, out, out_dtype, stream)
 
     def weight_gradient(self, d, d_scale, x, x_scale, exchange=None, out=None, accumulate=False, stream=None):
         """(d [N][P], x [K][P], as moe_quantize_fp8_act_t gives them) -> fp32 [E][N][K]."""
         import torch
-        if out is None:
-            out = torch.empty(self.E, self.N, self.K, dtype=torch.float32, device=d.device)
+        if (exchange is None) != (self.E == 1) or (exchange is not None and self.E != exchange.E):
+            raise ValueError("several experts take sorted rows and the exchange that sorted them")
+        if d.dim() != 2:
+            raise ValueError(f"expected codes [N][P], got {tuple(d.shape)}")
+        P = d.shape[1]
+        # each expert's blocks of 128 rows are its own: the sort's blocks have to be whole ones
+        if exchange is not None and (exchange.block_m % 128 or P < exchange.P):
+            raise ValueError("the exchange's blocks have to be multiples of 128 rows, and P no less than its rows")
+        for name, t, sc, rows in (("d", d, d_scale, self.N), ("x", x, x_scale, self.K)):
+            _expect(name, t, (rows, P), *_codes())
+            _expect(name + "_scale", sc, (P // 128, rows), torch.float32)
+        if accumulate and out is None:
+            raise ValueError("accumulate needs the gradients to add to")
+        out = _output("out", out, (self.E, self.N, self.K), torch.float32, d.device, stream)
         moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E,
                             None if exchange is None else exchange.expert_counts, out, int(accumulate), self.ws,
                             self.ws.numel(), stream)
@@ -725,17 +790,25 @@ class BlockNorm:
             raise MoEError("moe_block_norm_workspace_size", MOE_ERR_INVALID_ARG)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
 
-    def _rows(self, **tensors):
-        for name, t in tensors.items():
-            if t is not None and (tuple(t.shape) != (self.T, self.H) or not t.is_contiguous()):
-                raise ValueError(f"{name}: expected contiguous rows {(self.T, self.H)}, got {tuple(t.shape)}")
+    def _check(self, h, w_post, w_pre, gate, **rows):
+        _expect("h", h, (self.T, self.H), h.dtype)
+        for name, t in rows.items():
+            _expect(name, t, (self.T, self.H), h.dtype)
+        _expect("w_post", w_post, (self.H,), h.dtype)
+        _expect("w_pre", w_pre, (self.H,), h.dtype)
+        if self.gate_kind != MOE_GATE_NONE:
+            _expect("gate", gate, self._gate_shape(), h.dtype)
+
+    def _gate_shape(self):
+        return {MOE_GATE_NONE: None, MOE_GATE_CHANNEL: (self.H,), MOE_GATE_TOKEN: (self.T,),
+                MOE_GATE_FULL: (self.T, self.H)}[self.gate_kind]
 
     def forward(self, h, residual, w_post=None, w_pre=None, gate=None, y=None, z=None, stream=None):
         """Returns (y, z): the residual stream after the block and the next block's input (None without w_pre)."""
-        import torch
-        y = torch.empty_like(h) if y is None else y
-        z = torch.empty_like(h) if z is None and w_pre is not None else z
-        self._rows(h=h, residual=residual, y=y, z=z)
+        self._check(h, w_post, w_pre, gate, residual=residual)
+        y = _output("y", y, h.shape, h.dtype, h.device, stream)
+        if w_pre is not None:
+            z = _output("z", z, h.shape, h.dtype, h.device, stream)
         moe_block_norm(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
                        self.scale, self.weight_offset, self.eps, y, z, self.rstd_h, self.rstd_y, stream)
         return y, z
@@ -743,15 +816,14 @@ class BlockNorm:
     def backward(self, h, residual, dy, dz, w_post=None, w_pre=None, gate=None, stream=None):
         """Returns dict d_residual, dh, dgate, dw_post, dw_pre (None where there is no such input)."""
         import torch
-        self._rows(h=h, residual=residual, dy=dy, dz=dz)
-        dev, f32 = h.device, torch.float32
-        shape = {MOE_GATE_NONE: None, MOE_GATE_CHANNEL: (self.H,), MOE_GATE_TOKEN: (self.T,),
-                 MOE_GATE_FULL: (self.T, self.H)}[self.gate_kind]
-        g = {"d_residual": torch.empty_like(h), "dh": torch.empty_like(h),
-             "dgate": None if shape is None else torch.empty(
-                 shape, dtype=h.dtype if self.gate_kind == MOE_GATE_FULL else f32, device=dev),
-             "dw_post": None if w_post is None else torch.empty(self.H, dtype=f32, device=dev),
-             "dw_pre": None if w_pre is None else torch.empty(self.H, dtype=f32, device=dev)}
+        self._check(h, w_post, w_pre, gate, residual=residual, dy=dy, dz=dz)
+        f32, shape = torch.float32, self._gate_shape()
+        new = lambda name, shape, dtype: _output(name, None, shape, dtype, h.device, stream)  # noqa: E731
+        g = {"d_residual": new("d_residual", h.shape, h.dtype), "dh": new("dh", h.shape, h.dtype),
+             "dgate": None if shape is None else new("dgate", shape,
+                                                     h.dtype if self.gate_kind == MOE_GATE_FULL else f32),
+             "dw_post": None if w_post is None else new("dw_post", (self.H,), f32),
+             "dw_pre": None if w_pre is None else new("dw_pre", (self.H,), f32)}
         moe_block_norm_backward(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
                                 self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
                                 g["dh"], g["dgate"], g["dw_post"], g["dw_pre"], self.ws, self.ws_bytes, stream)

@@ -70,3 +70,28 @@ def test_classes_refuse_wrong_shapes():
     n = moe.BlockNorm(4, 64)
     with pytest.raises(ValueError):
         n.forward(torch.zeros(4, 32, device="cuda"), torch.zeros(4, 32, device="cuda"))
+
+
+def test_streams_given_to_the_classes():
+    """Outputs that the classes make for a stream are that stream's own, and a strided or single row works."""
+    from mixture_experts_grouped_moe_gb300 import moe
+    moe.load()
+    T, H, k, E = 333, 256, 2, 8
+    ids, wts = ref.route(T, E, k, seed=7)
+    x = torch.randn(T, 2 * H, device="cuda", generator=torch.Generator("cuda").manual_seed(1))[:, :H]
+    st = torch.cuda.Stream()
+    ex = moe.TokenExchange(T, k, E, 64)
+    i, w = ids.cuda(), wts.cuda()
+    st.wait_stream(torch.cuda.current_stream())
+    for stream in (st, st.cuda_stream):
+        ex.sort(i, w, stream=stream)
+        back = ex.unpermute(ex.permute(x, stream=stream), stream=stream)
+        n = moe.BlockNorm(T, H)
+        y, _ = n.forward(back, back, stream=stream)
+        st.synchronize()
+        assert (back - x).abs().max() <= 4 * 2.0 ** -24 * x.abs().max()
+        assert torch.equal(y, back + back)
+    one = moe.TokenExchange(1, 1, 2, 16)
+    one.sort(torch.ones(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 1, device="cuda"))
+    r = x[:1]
+    assert torch.equal(one.unpermute(one.permute(r)), r)

@@ -117,3 +117,58 @@ def test_block_norm(lib):
         (dict(wi=None), INVALID), (dict(wi=None, dz=None, dy=None), INVALID), (dict(g=None, gk=0), INVALID),
         (dict(r=P + 1), INVALID), (dict(r=None), INVALID), (dict(dwo=P + 2), INVALID), (dict(H=20000), UNSUPPORTED), (dict(wsb=16), WORKSPACE)])
     assert lib.moe_block_norm_workspace_size(-1, 64) == 0 and lib.moe_block_norm_workspace_size(4, 1 << 20) == 0
+
+
+def test_classes_refuse_on_the_host(lib):
+    """What the entry points cannot see (shapes, strides and types of tensors) the classes refuse before any
+    launch: nothing here needs a GPU."""
+    import torch
+    from mixture_experts_grouped_moe_gb300 import moe
+    T, k, E, H = 8, 2, 4, 128
+    ex = moe.TokenExchange(T, k, E, 16, device="cpu")
+    P, bf = ex.P, torch.bfloat16
+    x, ys = torch.zeros(T, H, dtype=bf), torch.zeros(P, H, dtype=bf)
+    refused = [
+        (TypeError, lambda: ex.sort(torch.zeros(T, k, dtype=torch.int64), torch.zeros(T, k))),
+        (ValueError, lambda: ex.sort(torch.zeros(T, k + 1, dtype=torch.int32), torch.zeros(T, k))),
+        (ValueError, lambda: ex.permute(x, xs=torch.zeros(P, H - 1, dtype=bf))),
+        (TypeError, lambda: ex.permute(x, xs=torch.zeros(P, H))),
+        (ValueError, lambda: ex.permute(torch.zeros(H, T, dtype=bf).t())),
+        (TypeError, lambda: ex.permute(torch.zeros(T, H, dtype=torch.float64))),
+        (ValueError, lambda: ex.permute_fp8(x, q=torch.zeros(P, H // 2, dtype=torch.uint8))),
+        (ValueError, lambda: ex.permute_fp8(x, s=torch.zeros(P, H // 128))),
+        (ValueError, lambda: ex.unpermute(ys, out=torch.zeros(T, H // 2, dtype=bf))),
+        (ValueError, lambda: ex.unpermute(ys, out=torch.zeros(T, H))),
+        (ValueError, lambda: ex.unpermute_backward(x, ys[:, :64].contiguous())),
+        (TypeError, lambda: ex.unpermute_backward(x, ys.float())),
+        (ValueError, lambda: ex.permute_backward(ys, dx=torch.zeros(T, H // 2, dtype=bf))),
+    ]
+    w = moe.FP8Weights.__new__(moe.FP8Weights)  # (its constructor quantises on the GPU)
+    w.E, w.N, w.K, w.training, w.ws = E, 256, H, False, torch.zeros(64, dtype=torch.uint8)
+    w.q, w.s = torch.zeros(E, 256, H, dtype=torch.uint8), torch.ones(E, 2, 1)
+    q, s = torch.zeros(P, H, dtype=torch.uint8), torch.ones(P, 1)
+    dt, xt = torch.zeros(256, 128, dtype=torch.uint8), torch.zeros(H, 128, dtype=torch.uint8)
+    refused += [
+        (ValueError, lambda: w.product(q, s)),
+        (ValueError, lambda: w.product(q, s[:1], exchange=ex)),
+        (ValueError, lambda: w.product(q, s, by_block=True, exchange=ex)),
+        (TypeError, lambda: w.product(q.int(), s, exchange=ex)),
+        (ValueError, lambda: w.product(q, s, exchange=ex, out=torch.zeros(P, 128, dtype=bf))),
+        (TypeError, lambda: w.product(q, s, exchange=ex, out_dtype=torch.float16)),
+        (ValueError, lambda: w.product(q, s, exchange=moe.TokenExchange(T, k, 2 * E, 16, device="cpu"))),
+        (ValueError, lambda: w.input_gradient(q, s, exchange=ex)),
+        (ValueError, lambda: w.weight_gradient(dt, torch.ones(1, 256), xt, torch.ones(1, H), exchange=ex)),  # blocks of 16
+    ]
+    n = moe.BlockNorm(T, H, moe.MOE_GATE_CHANNEL, device="cpu")
+    gate = torch.ones(H, dtype=bf)
+    refused += [
+        (ValueError, lambda: n.forward(x, x, gate=torch.ones(T, dtype=bf))),
+        (TypeError, lambda: n.forward(x, x, gate=gate.float())),
+        (TypeError, lambda: n.forward(x, x.float(), gate=gate)),
+        (ValueError, lambda: n.forward(x, x, gate=gate, w_post=torch.ones(H - 8, dtype=bf))),
+        (ValueError, lambda: n.forward(x, x, gate=gate, y=torch.zeros(T, 2 * H, dtype=bf)[:, :H])),
+        (TypeError, lambda: n.backward(x, x, x.half(), x, gate=gate)),
+    ]
+    for error, call in refused:
+        with pytest.raises(error):
+            call()
