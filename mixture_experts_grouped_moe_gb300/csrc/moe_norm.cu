@@ -23,7 +23,12 @@
 // A row's two sums are a chain of barriers, so a block that loads its next row only after this one
 // leaves HBM idle most of the time.  The blocks are persistent and copy the next rows ahead into
 // shared memory (cp.async; each thread copies exactly the pieces that it will read itself, so no
-// barrier guards the ring): kAhead of them @MEASURE@.
+// barrier guards the ring).  8192 rows of 4096 bf16 with a gate per column: forward 44 us (6.0 TB/s; 103 us
+// without the ring), forward and backward 153 (250), 8192 rows of 2048 86 (123), of 4096 fp32 214 (384);
+// rows of 16384 gain in the forward only (64 / 73), since one block an SM has its barriers to itself.  A third
+// row in the ring was no faster (155 and 48 us again, fp32 220).  Rows that are no whole number of 16-byte
+// pieces go by single elements and without the ring (8192 rows of 401, forward: 17.8 us); the widest of
+// those (over 4096 elements) no longer fit a thread's registers, 8192 rows of 4097 taking 300 us forward.
 #include "moe_internal.h"
 #include "rows.cuh"
 #include "sm100_ptx.cuh"
@@ -35,6 +40,7 @@ namespace {
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxH = 16384;
+constexpr int kSlots = 2;  // rows of a block's ring in shared memory
 
 struct NormArgs {
     const void *h, *residual, *gate, *w_post, *w_pre;
@@ -48,7 +54,6 @@ struct NormArgs {
     const void *dy, *dz;
     void *dres, *dh, *dgate;
     float *part;  // [blocks][2][H]: the blocks' column sums
-    int slots;    // rows of the ring in shared memory
 };
 
 // The rows that a block walks (blockIdx.x, + gridDim.x, ...), each of N arrays, a thread's pieces of
@@ -58,15 +63,15 @@ struct RowRing {
     const V *src[N];  // null: not read
     V *ring;
     int64_t T;
-    int units, slots, slot;
+    int units, slot;
 
-    __device__ __forceinline__ void init(int64_t rows, int nunits, int nslots)
+    __device__ __forceinline__ void init(int64_t rows, int nunits)
     {
         extern __shared__ __align__(16) uint8_t smem[];
         ring = reinterpret_cast<V *>(smem);
-        T = rows, units = nunits, slots = nslots, slot = 0;
+        T = rows, units = nunits, slot = 0;
         if (RING)
-            for (int i = 0; i < slots; ++i)
+            for (int i = 0; i < kSlots; ++i)
                 fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
     }
     __device__ __forceinline__ void fetch(int64_t t, int to)
@@ -86,10 +91,8 @@ struct RowRing {
     __device__ __forceinline__ void wait()
     {
         if (RING) {
-            if (slots == 2)  // every copy but the slots - 1 newer ones
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
+            static_assert(kSlots == 2, "every copy but the kSlots - 1 newer ones");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
         }
     }
     // Piece i of array a of that row (row t).
@@ -98,13 +101,12 @@ struct RowRing {
         const int u = threadIdx.x + i * blockDim.x;
         return RING ? ring[(slot * N + a) * units + u] : src[a][t * units + u];
     }
-    // Row t's pieces have been read: its place takes the row `slots` further on.
+    // Row t's pieces have been read: its place takes the row kSlots further on.
     __device__ __forceinline__ void next(int64_t t)
     {
         if (RING) {
-            fetch(t + (int64_t)slots * gridDim.x, slot);
-            if (++slot == slots)
-                slot = 0;
+            fetch(t + (int64_t)kSlots * gridDim.x, slot);
+            slot ^= 1;
         }
     }
 };
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING && NV == 1 ? 2 : 1) norm_ker
     RowRing<V, NV, 2, RING> in = {{static_cast<const V *>(a.h), static_cast<const V *>(a.residual)}};
     pdl_wait();
     pdl_trigger();
-    in.init(a.T, units, a.slots);
+    in.init(a.T, units);
     float k[NV][VEC], wi[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs a)
                                    static_cast<const V *>(a.dy), static_cast<const V *>(a.dz)}};
     pdl_wait();
     pdl_trigger();
-    in.init(a.T, units, a.slots);
+    in.init(a.T, units);
     float c_post[NV][VEC], c_pre[NV][VEC], k[NV][VEC], wi[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -459,7 +461,7 @@ cudaError_t run_ring(NormArgs a, bool bwd, int threads, int per_sm, cudaStream_t
                     : (full ? norm_kernel<T, VEC, NV, RING, true> : norm_kernel<T, VEC, NV, RING, false>);
     size_t smem = 0;
     if (RING) {
-        smem = (size_t)a.slots * (bwd ? 4 : 2) * a.H * sizeof(T);
+        smem = (size_t)kSlots * (bwd ? 4 : 2) * a.H * sizeof(T);
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess)
             return err;
@@ -475,28 +477,26 @@ cudaError_t run(NormArgs a, bool bwd, cudaStream_t st)
     const int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
     if (threads > kMaxThreads)
         return cudaErrorInvalidValue;
-    // Copied ahead where an SM's blocks have two or three rows each in its shared memory.
+    // Copied ahead wherever the rows are whole 16-byte pieces and two of them fit.
     int per_sm = (bwd || NV > 1 ? 512 : 1024) / threads;  // (by registers: up to 128 and 64 a thread)
     const int64_t slot = (int64_t)(bwd ? 4 : 2) * a.H * sizeof(T);
-    while (per_sm > 1 && per_sm * 2 * slot > kRingBytes)
+    while (per_sm > 1 && per_sm * kSlots * slot > kRingBytes)
         --per_sm;
     if (VEC * sizeof(T) == 16) {
-        a.slots = per_sm * 3 * slot <= kRingBytes ? 3 : 2;
-        if (a.slots * slot <= kRingBytes)
+        if (kSlots * slot <= kRingBytes)
             return run_ring<T, VEC, NV, VEC * sizeof(T) == 16>(a, bwd, threads, per_sm, st);
     }
     return run_ring<T, VEC, NV, false>(a, bwd, threads, 16, st);
 }
 
-// Pieces a thread holds: the fewest that cover the row with at most kMaxThreads threads.
+// Pieces a thread holds.  Up to 256 threads have one each: a row of 4096 bf16 elements is as fast in 256
+// threads as in 512 (forward 48.1 / 48.5 us for 8192 rows, backward 103 / 105), and single elements are
+// faster (8192 rows of 401: 17.8 us, 23.9 with 512 threads).
 template <typename T, int VEC>
 cudaError_t run_nv(const NormArgs &a, bool bwd, cudaStream_t st)
 {
     const int units = a.H / VEC;
-    // (single elements, and the backward: fewer, fuller threads, whose columns' factors and sums stay in
-    // registers)
-    const int most = VEC == 1 || bwd ? 256 : kMaxThreads;
-    if (units <= most)
+    if (units <= 256)
         return run<T, VEC, 1>(a, bwd, st);
     if (units <= (VEC == 1 ? 512 : 2 * kMaxThreads))
         return run<T, VEC, 2>(a, bwd, st);
