@@ -488,7 +488,7 @@ def _expect(name, t, shape, *dtypes):
     """t (None passes) is contiguous, of that shape and of one of those types."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():  # (a torch.Size is a tuple)
         raise ValueError(f"{name}: expected contiguous {tuple(shape)}, got {tuple(t.shape)} with strides {t.stride()}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
@@ -496,16 +496,13 @@ def _expect(name, t, shape, *dtypes):
 
 def _output(name, t, shape, dtype, device, stream):
     """t after its checks, or a new tensor that belongs to the stream that will write it."""
-    import contextlib
-    import torch
     if t is not None:
         _expect(name, t, shape, dtype)
         return t
+    import torch
     if stream is None:
-        scope = contextlib.nullcontext()
-    else:
-        scope = torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    with scope:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
