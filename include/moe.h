@@ -477,12 +477,27 @@ int moe_align_sort_noalloc(const int32_t *topk_ids, const float *topk_weights, i
 /*
  * moe_align_sort that also gives the inverse map: slot_pos (device) int32
  * [T*k], the sorted position of each slot, -1 for a slot left out because its
- * id is outside [0, E).  Everything else as moe_align_sort (same ws).
+ * id is outside [0, E).  Everything else as moe_align_sort (same ws): such an
+ * id is an error, num_tokens_post_padded = -1 refuses the whole routing, and
+ * the entries below that read it then zero no padding and compute no row.
  */
 int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
                        int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
                        int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos, void *ws,
                        size_t ws_bytes, void *stream);
+
+/*
+ * moe_align_sort_map for routings that leave slots out on purpose (dropped
+ * tokens, masked rows, experts held elsewhere): an id outside [0, E) is no
+ * error.  num_tokens_post_padded is the sum of the padded segments of the
+ * slots that stay (never -1), and num_left_out (device) int32 [1] the number
+ * of slots left out, for callers that expect none.  The entries below then
+ * give such a slot nothing and add nothing for it.
+ */
+int moe_align_sort_drop(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
+                        int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
+                        int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos,
+                        int32_t *num_left_out, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Rows to the experts' order: xs[slot_pos[t*k + j]] = x[t].

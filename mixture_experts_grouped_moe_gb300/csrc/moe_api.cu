@@ -396,7 +396,7 @@ static int forward_impl(int dtype, const void *x, const void *W_router, const fl
     }
     mark(o, 1, st);
 
-    SortOut so;
+    SortOut so = {};
     so.sorted_ids = static_cast<int32_t *>(at(L.sorted_ids));
     so.sorted_weights = static_cast<float *>(at(L.sorted_w));
     so.sorted_expert_ids = static_cast<int32_t *>(at(L.sorted_eids));

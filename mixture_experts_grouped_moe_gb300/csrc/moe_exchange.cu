@@ -432,12 +432,11 @@ int check_exchange(int row_type, int T, int k, int H, int64_t P, int64_t ld)
 
 using namespace moe;
 
-extern "C" {
-
-int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
-                       int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
-                       int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos, void *ws,
-                       size_t ws_bytes, void *stream)
+// left_out: where the slots left out are counted (a routing with such slots is then no error), or null.
+static int sort_with_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
+                         int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
+                         int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos,
+                         int32_t *left_out, void *ws, size_t ws_bytes, void *stream)
 {
     if (T < 0 || k <= 0 || E <= 0 || block_m <= 0)
         return MOE_ERR_INVALID_ARG;
@@ -456,10 +455,33 @@ int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T
     so.num_post_padded = num_tokens_post_padded;
     so.expert_counts = expert_counts;
     so.slot_pos = slot_pos;
+    so.left_out = left_out;
     // as moe_align_sort lays its scratch out: chunk histograms, then the E + 1 padded offsets
     so.expert_offsets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + need - (size_t)(E + 1) * 4);
     return to_status(launch_align_sort(topk_ids, topk_weights, T, k, E, block_m, so, ws, true, true,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" {
+
+int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
+                       int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
+                       int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos, void *ws,
+                       size_t ws_bytes, void *stream)
+{
+    return sort_with_map(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
+                         num_tokens_post_padded, expert_counts, slot_pos, nullptr, ws, ws_bytes, stream);
+}
+
+int moe_align_sort_drop(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
+                        int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,
+                        int32_t *num_tokens_post_padded, int32_t *expert_counts, int32_t *slot_pos,
+                        int32_t *num_left_out, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!num_left_out)
+        return MOE_ERR_INVALID_ARG;
+    return sort_with_map(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
+                         num_tokens_post_padded, expert_counts, slot_pos, num_left_out, ws, ws_bytes, stream);
 }
 
 int moe_permute(int row_type, const void *x, int64_t ld_x, const int32_t *slot_pos, const int32_t *sorted_ids,

@@ -117,10 +117,12 @@ struct SortOut {
     int32_t *active_experts;  // [E] compact list of experts with slots (may be null)
     int32_t *num_active;      // [1] (may be null)
     int32_t *slot_pos;        // [S] sorted position of each slot (may be null)
+    int32_t *left_out;        // [1] slots with an id outside [0, E) (may be null)
 };
 // pdl_first: the first launch follows another kernel of this library; pdl_inner: the
 // chunked sort's second and third launches.  An id outside [0, E) is left out of every
-// segment and sets *num_post_padded to -1.
+// segment; without left_out it also sets *num_post_padded to -1 (the routing is refused), with
+// left_out the slots are counted there and *num_post_padded stays the sum of the segments.
 cudaError_t launch_align_sort(const int32_t *ids, const float *wts, int T, int k, int E, int block_m,
                               const SortOut &o, void *scratch, bool pdl_first, bool pdl_inner, cudaStream_t st);
 

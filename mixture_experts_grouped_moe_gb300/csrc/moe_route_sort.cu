@@ -833,8 +833,8 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t *__restr
             o.slot_pos[e] = -1;
     }
     // an id outside [0, E) matches no expert below, so its slot is left out; it is reported
-    // through num_post_padded = -1
-    const bool any_bad = __syncthreads_or(bad_id);
+    // through num_post_padded = -1, or counted where the caller leaves slots out on purpose
+    const int nbad = __syncthreads_count(bad_id);
     int cnt = 0;
     if (e < E)
         for (int s = 0; s < S; ++s)
@@ -870,7 +870,9 @@ __global__ void __launch_bounds__(1024) sort_small_kernel(const int32_t *__restr
             o.sorted_expert_ids[b] = e;
     }
     if (e == 0) {
-        *o.num_post_padded = any_bad ? -1 : total;
+        *o.num_post_padded = nbad && !o.left_out ? -1 : total;
+        if (o.left_out)
+            *o.left_out = nbad;
         if (o.expert_offsets)
             o.expert_offsets[E] = total;
         if (o.num_active)
@@ -896,16 +898,14 @@ __global__ void __launch_bounds__(256) sort_few_kernel(const int32_t *__restrict
     __shared__ int s_total;
     pdl_wait();
     pdl_trigger();
-    bool bad_id = false;
     for (int i = threadIdx.x; i < S; i += blockDim.x) {
         s_ids[i] = ids[i];
         s_w[i] = wts[i];
-        const bool bad = (unsigned)s_ids[i] >= (unsigned)E;  // matches no expert below: left out, reported
-        if (bad && o.slot_pos)
+        // (a bad id matches no expert below: left out, reported)
+        if (o.slot_pos && (unsigned)s_ids[i] >= (unsigned)E)
             o.slot_pos[i] = -1;
-        bad_id |= bad;
     }
-    const bool any_bad = __syncthreads_or(bad_id);
+    __syncthreads();
     if (threadIdx.x < 32) {
         const int e = threadIdx.x;
         int cnt = 0;
@@ -927,6 +927,7 @@ __global__ void __launch_bounds__(256) sort_few_kernel(const int32_t *__restrict
         const int off = ipad - pad;
         const int total = __shfl_sync(0xffffffffu, ipad, 31);
         const int nact = __shfl_sync(0xffffffffu, iact, 31);
+        const int nbad = S - __reduce_add_sync(0xffffffffu, cnt);
         if (e < E) {
             if (o.expert_counts)
                 o.expert_counts[e] = cnt;
@@ -951,7 +952,9 @@ __global__ void __launch_bounds__(256) sort_few_kernel(const int32_t *__restrict
                 o.sorted_expert_ids[b] = e;
         }
         if (e == 0) {
-            *o.num_post_padded = any_bad ? -1 : total;
+            *o.num_post_padded = nbad && !o.left_out ? -1 : total;
+            if (o.left_out)
+                *o.left_out = nbad;
             if (o.expert_offsets)
                 o.expert_offsets[E] = total;
             if (o.num_active)
@@ -1042,7 +1045,9 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t *__restrict__ c
     }
     const int total = s_pad[1023];
     if (e == 0) {
-        *o.num_post_padded = (s_counted == S) ? total : -1;
+        *o.num_post_padded = (s_counted == S || o.left_out) ? total : -1;
+        if (o.left_out)
+            *o.left_out = S - s_counted;
         o.expert_offsets[E] = total;
         if (o.num_active)
             *o.num_active = s_act[1023];

@@ -44,7 +44,7 @@ EXPORTED = [
     "moe_quantize_fp8_act", "moe_quantize_fp8_weights", "moe_quantize_fp8_rows", "moe_fused_forward",
     "moe_host_staging_bytes", "moe_fused_forward_host", "moe_align_sort_noalloc", "moe_quantize_mxfp4",
     "moe_train_workspace_size", "moe_fused_forward_train", "moe_fused_backward", "moe_options_init",
-    "moe_fused_forward_ex", "moe_align_sort_map", "moe_permute", "moe_permute_fp8", "moe_permute_backward",
+    "moe_fused_forward_ex", "moe_align_sort_map", "moe_align_sort_drop", "moe_permute", "moe_permute_fp8", "moe_permute_backward",
     "moe_unpermute", "moe_unpermute_backward", "moe_gemm_fp8_block", "moe_wgrad_fp8_block",
     "moe_quantize_fp8_act_t", "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
 ]
@@ -125,6 +125,7 @@ def load(build_if_missing: bool = False):
             "moe_quantize_mxfp4": (I, [P, I64, I, P, P, I, P]),
             "moe_align_sort_noalloc": (I, [P, P, I, I, I, I, P, P, P, P, P, P]),
             "moe_align_sort_map": (I, [P, P, I, I, I, I, P, P, P, P, P, P, P, SZ, P]),
+            "moe_align_sort_drop": (I, [P, P, I, I, I, I, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_permute": (I, [I, P, I64, P, P, P, I, I, I, I64, I, P, P]),
             "moe_permute_fp8": (I, [P, I64, P, P, P, I, I, I, I64, I, P, P, P]),
             "moe_permute_backward": (I, [I, P, P, I, I, I, I64, P, I64, P]),
@@ -371,6 +372,15 @@ def moe_align_sort_map(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sor
         _stream(stream)))
 
 
+def moe_align_sort_drop(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
+                        num_tokens_post_padded, expert_counts, slot_pos, num_left_out, ws, ws_bytes, stream=None):
+    """moe_align_sort_map where an id outside [0, E) leaves its slot out instead of refusing the routing."""
+    return _check("moe_align_sort_drop", load().moe_align_sort_drop(
+        _p(topk_ids), _p(topk_weights), T, k, E, block_m, _p(sorted_ids), _p(sorted_weights),
+        _p(sorted_expert_ids), _p(num_tokens_post_padded), _p(expert_counts), _p(slot_pos), _p(num_left_out), _p(ws),
+        ws_bytes, _stream(stream)))
+
+
 def moe_permute(row_type, x, ld_x, slot_pos, sorted_ids, num_tokens_post_padded, T, k, H, P, zero_padding, xs,
                 stream=None):
     return _check("moe_permute", load().moe_permute(
@@ -515,8 +525,8 @@ class TokenExchange:
     """Owns the maps of one routing shape (T tokens, k of E experts, blocks of block_m rows): sort(),
     then rows to the experts' order and back, with gradients.
 
-    After sort(): sorted_ids, sorted_weights, expert_ids, num_tokens_post_padded, expert_counts and
-    slot_pos (see moe_align_sort_map in include/moe.h); P is the number of sorted rows to allocate.
+    After sort(): sorted_ids, sorted_weights, expert_ids, num_tokens_post_padded, expert_counts, slot_pos
+    and num_left_out (see moe_align_sort_drop in include/moe.h); P is the number of sorted rows to allocate.
     """
 
     def __init__(self, T, k, E, block_m=128, device="cuda"):
@@ -526,21 +536,21 @@ class TokenExchange:
         i32 = dict(dtype=torch.int32, device=device)
         self.sorted_ids, self.slot_pos = torch.empty(self.P, **i32), torch.empty(T * k, **i32)
         self.expert_ids, self.expert_counts = torch.empty(nb, **i32), torch.empty(E, **i32)
-        self.num_tokens_post_padded = torch.empty(1, **i32)
+        self.num_tokens_post_padded, self.num_left_out = torch.empty(1, **i32), torch.empty(1, **i32)
         self.sorted_weights = torch.empty(self.P, dtype=torch.float32, device=device)
         self.ws_bytes = moe_align_sort_workspace_size(T, k, E)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.weights = None
 
     def sort(self, topk_ids, topk_weights, stream=None):
-        """topk_ids int32 [T][k] (outside [0, E): the slot is left out), topk_weights fp32 [T][k]: kept, for
-        unpermute and its gradient."""
+        """topk_ids int32 [T][k] (outside [0, E): the slot is left out, and counted in num_left_out),
+        topk_weights fp32 [T][k]: kept, for unpermute and its gradient."""
         import torch
         _expect("topk_ids", topk_ids, (self.T, self.k), torch.int32)
         _expect("topk_weights", topk_weights, (self.T, self.k), torch.float32)
-        moe_align_sort_map(topk_ids, topk_weights, self.T, self.k, self.E, self.block_m, self.sorted_ids,
-                           self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
-                           self.slot_pos, self.ws, self.ws_bytes, stream)
+        moe_align_sort_drop(topk_ids, topk_weights, self.T, self.k, self.E, self.block_m, self.sorted_ids,
+                            self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
+                            self.slot_pos, self.num_left_out, self.ws, self.ws_bytes, stream)
         self.weights = topk_weights
 
     def _rows(self, x):
