@@ -589,7 +589,9 @@ int moe_gemm_fp8_block(const uint8_t *A, const float *a_scale, int a_scale_by_bl
  *   A (device) e4m3 [M][P], a_scale (device) fp32 [P/128][M];
  *   B (device) e4m3 [N][P], b_scale (device) fp32 [P/128][N] (both as
  *   moe_quantize_fp8_act_t gives them: padding rows are zero codes);
- *   expert_counts (device) int32 [E], or NULL with E = 1: all P rows;
+ *   expert_counts (device) int32 [E], or NULL with E = 1: all P rows.  For
+ *   rows sorted with a block_m above 128, pass the counts rounded up to
+ *   multiples of block_m (the sort's segments);
  *   D (device) fp32 [E][M][N]; accumulate = 1 adds to D, 0 overwrites it (an
  *   expert without rows gets zeros).
  * P % 128 == 0, N % 4 == 0, E <= 1024, b_scale on a 16-byte boundary.

@@ -8,6 +8,7 @@ call raises (build it with `mixture_experts_grouped_moe_gb300.build`).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -504,6 +505,14 @@ def _expect(name, t, shape, *dtypes):
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
 
 
+def _on(stream):
+    """Context in which torch allocates and launches on `stream` (None: the current stream)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _output(name, t, shape, dtype, device, stream):
     """t after its checks, or a new tensor that belongs to the stream that will write it."""
     if t is not None:
@@ -512,7 +521,7 @@ def _output(name, t, shape, dtype, device, stream):
     import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+    with _on(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -552,6 +561,15 @@ class TokenExchange:
                             self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
                             self.slot_pos, self.num_left_out, self.ws, self.ws_bytes, stream)
         self.weights = topk_weights
+
+    def segment_counts(self, stream=None):
+        """Rows of each expert's segment, for moe_wgrad_fp8_block, which starts an expert after ceil(count / 128)
+        blocks of 128 of each one before it: with larger sort blocks a segment's padding may hold whole blocks of
+        128 (zero codes, which add nothing), so the counts are rounded up to the sort's blocks."""
+        if self.block_m <= 128:
+            return self.expert_counts
+        with _on(stream):
+            return (self.expert_counts + (self.block_m - 1)) // self.block_m * self.block_m
 
     def _rows(self, x):
         if x.dim() != 2 or x.shape[0] != self.T or (x.shape[1] > 1 and x.stride(1) != 1):
@@ -764,7 +782,7 @@ class FP8Weights:
         if d.dim() != 2:
             raise ValueError(f"expected codes [N][P], got {tuple(d.shape)}")
         P = d.shape[1]
-        # each expert's blocks of 128 rows are its own: the sort's blocks have to be whole ones
+        # each expert's blocks of 128 rows are its own: the sort's blocks have to be whole numbers of them
         if exchange is not None and (exchange.block_m % 128 or P < exchange.P):
             raise ValueError("the exchange's blocks have to be multiples of 128 rows, and P no less than its rows")
         for name, t, sc, rows in (("d", d, d_scale, self.N), ("x", x, x_scale, self.K)):
@@ -773,9 +791,9 @@ class FP8Weights:
         if accumulate and out is None:
             raise ValueError("accumulate needs the gradients to add to")
         out = _output("out", out, (self.E, self.N, self.K), torch.float32, d.device, stream)
-        moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E,
-                            None if exchange is None else exchange.expert_counts, out, int(accumulate), self.ws,
-                            self.ws.numel(), stream)
+        counts = None if exchange is None else exchange.segment_counts(stream)
+        moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E, counts, out, int(accumulate),
+                            self.ws, self.ws.numel(), stream)
         return out
 
     def status(self, stream=None) -> int:
