@@ -716,32 +716,36 @@ class FP8Weights:
     """Block-quantised weights of one product, [E][N][K] (E = 1: a dense layer): the e4m3 codes and the
     128 x 128 scales, and with `training` the transposed ones that the input gradient multiplies by.
 
-    N and K are multiples of 128 (moe_quantize_fp8_weights).  Owns the products' workspace."""
+    N and K are multiples of 128 (moe_quantize_fp8_weights).  Owns the products' workspace.  The constructor
+    and update() write on `stream` as the products read on theirs: calls on different streams are the
+    caller's to order."""
 
-    def __init__(self, W, training=False):
+    def __init__(self, W, training=False, stream=None):
         import torch
         if W.dtype != torch.bfloat16 or W.dim() != 3 or not W.is_contiguous():
             raise ValueError("expected contiguous bf16 weights [E][N][K]")
-        self.E, self.N, self.K = W.shape
-        self.ws = torch.zeros(MOE_GEMM_BLOCK_WS_BYTES, dtype=torch.uint8, device=W.device)
+        E, N, K = self.E, self.N, self.K = W.shape
         self.training = training
-        self.update(W)
+        dev = W.device
+        with _on(stream):
+            self.ws = torch.zeros(MOE_GEMM_BLOCK_WS_BYTES, dtype=torch.uint8, device=dev)
+            self.q = torch.empty(E, N, K, dtype=torch.uint8, device=dev)
+            self.s = torch.empty(E, N // 128, K // 128, dtype=torch.float32, device=dev)
+            if training:
+                self.qt = torch.empty(E, K, N, dtype=torch.uint8, device=dev)
+                self.st = torch.empty(E, K // 128, N // 128, dtype=torch.float32, device=dev)
+        self.update(W, stream)
 
-    @staticmethod
-    def _quantise(W):
+    def update(self, W, stream=None):
+        """Quantise the weights anew (after an optimiser step), in place: products enqueued before on the same
+        stream still read the old ones."""
         import torch
-        E, N, K = W.shape
-        q = torch.empty(E, N, K, dtype=torch.uint8, device=W.device)
-        s = torch.empty(E, N // 128, K // 128, dtype=torch.float32, device=W.device)
-        moe_quantize_fp8_weights(W, E * N, K, q, s)
-        return q, s
-
-    def update(self, W):
-        """Quantise the weights anew (after an optimiser step)."""
-        self.q, self.s = self._quantise(W)
+        _expect("W", W, (self.E, self.N, self.K), torch.bfloat16)
+        moe_quantize_fp8_weights(W, self.E * self.N, self.K, self.q, self.s, stream)
         if self.training:  # the same blocks, transposed: the same codes and scales
-            self.qt = self.q.transpose(1, 2).contiguous()
-            self.st = self.s.transpose(1, 2).contiguous()
+            with _on(stream):
+                self.qt.copy_(self.q.transpose(1, 2))
+                self.st.copy_(self.s.transpose(1, 2))
 
     def _product(self, a, a_scale, by_block, q, s, N, K, exchange, out, out_dtype, stream):
         import torch
