@@ -505,6 +505,16 @@ def _expect(name, t, shape, *dtypes):
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
 
 
+def _on_gpu(owner, **tensors):
+    """The tensors (None passes) are on the GPU of `owner`, a tensor of the object whose method is called: a
+    kernel is given their addresses.  Checked last, right before a launch."""
+    gpu = owner.get_device()  # (-1: not on a GPU)
+    for name, t in tensors.items():
+        if t is not None and (gpu < 0 or t.get_device() != gpu):
+            raise ValueError(f"{name} is on {t.device}, what belongs to the operator on {owner.device}: "
+                             "both have to be on one GPU")
+
+
 def _on(stream):
     """Context in which torch allocates and launches on `stream` (None: the current stream)."""
     import torch
@@ -557,6 +567,7 @@ class TokenExchange:
         import torch
         _expect("topk_ids", topk_ids, (self.T, self.k), torch.int32)
         _expect("topk_weights", topk_weights, (self.T, self.k), torch.float32)
+        _on_gpu(self.slot_pos, topk_ids=topk_ids, topk_weights=topk_weights)
         moe_align_sort_drop(topk_ids, topk_weights, self.T, self.k, self.E, self.block_m, self.sorted_ids,
                             self.sorted_weights, self.expert_ids, self.num_tokens_post_padded, self.expert_counts,
                             self.slot_pos, self.num_left_out, self.ws, self.ws_bytes, stream)
@@ -594,7 +605,9 @@ class TokenExchange:
         """x [T][H] -> sorted rows [P][H]."""
         H, ld = self._rows(x)
         xs = _output("xs", xs, (self.P, H), x.dtype, x.device, stream)
-        moe_permute(_row_type(x.dtype), x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T,
+        row_type = _row_type(x.dtype)
+        _on_gpu(self.slot_pos, x=x, xs=xs)
+        moe_permute(row_type, x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T,
                     self.k, H, self.P, int(zero_padding), xs, stream)
         return xs
 
@@ -609,6 +622,7 @@ class TokenExchange:
         else:
             q = _output("q", None, (self.P, H), torch.uint8, x.device, stream)
         s = _output("s", s, (H // 128, self.P), torch.float32, x.device, stream)
+        _on_gpu(self.slot_pos, x=x, q=q, s=s)
         moe_permute_fp8(x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T, self.k, H, self.P,
                         int(zero_padding), q, s, stream)
         return q, s
@@ -617,7 +631,9 @@ class TokenExchange:
         """Sorted rows [P][H] -> [T][H], each token's rows summed with its top-k weights (or 1)."""
         H = self._sorted(ys)
         out, ld = self._token_rows("out", out, H, ys.dtype, ys.device, stream)
-        moe_unpermute(_row_type(ys.dtype), ys, self.slot_pos, self.weights if weights else None, self.T, self.k, H,
+        row_type = _row_type(ys.dtype)
+        _on_gpu(self.slot_pos, ys=ys, out=out)
+        moe_unpermute(row_type, ys, self.slot_pos, self.weights if weights else None, self.T, self.k, H,
                       self.P, out, ld, stream)
         return out
 
@@ -628,7 +644,9 @@ class TokenExchange:
         _expect("ys", ys, (self.P, H), dout.dtype)
         dys = _output("dys", None, (self.P, H), ys.dtype, ys.device, stream)
         dw = _output("dweights", None, (self.T, self.k), torch.float32, ys.device, stream)
-        moe_unpermute_backward(_row_type(ys.dtype), dout, ld, ys, self.slot_pos, self.weights, self.sorted_ids,
+        row_type = _row_type(ys.dtype)
+        _on_gpu(self.slot_pos, dout=dout, ys=ys)
+        moe_unpermute_backward(row_type, dout, ld, ys, self.slot_pos, self.weights, self.sorted_ids,
                                self.num_tokens_post_padded, self.T, self.k, H, self.P, int(zero_padding), dys, dw,
                                stream)
         return dys, dw
@@ -637,7 +655,9 @@ class TokenExchange:
         """Gradient of permute: sorted rows [P][H] -> [T][H]."""
         H = self._sorted(dxs)
         dx, ld = self._token_rows("dx", dx, H, dxs.dtype, dxs.device, stream)
-        moe_permute_backward(_row_type(dxs.dtype), dxs, self.slot_pos, self.T, self.k, H, self.P, dx, ld, stream)
+        row_type = _row_type(dxs.dtype)
+        _on_gpu(self.slot_pos, dxs=dxs, dx=dx)
+        moe_permute_backward(row_type, dxs, self.slot_pos, self.T, self.k, H, self.P, dx, ld, stream)
         return dx
 
 
@@ -724,6 +744,7 @@ class FP8Weights:
         import torch
         if W.dtype != torch.bfloat16 or W.dim() != 3 or not W.is_contiguous():
             raise ValueError("expected contiguous bf16 weights [E][N][K]")
+        _on_gpu(W, W=W)
         E, N, K = self.E, self.N, self.K = W.shape
         self.training = training
         dev = W.device
@@ -741,6 +762,7 @@ class FP8Weights:
         stream still read the old ones."""
         import torch
         _expect("W", W, (self.E, self.N, self.K), torch.bfloat16)
+        _on_gpu(self.ws, W=W)
         moe_quantize_fp8_weights(W, self.E * self.N, self.K, self.q, self.s, stream)
         if self.training:  # the same blocks, transposed: the same codes and scales
             with _on(stream):
@@ -761,6 +783,8 @@ class FP8Weights:
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"products are bf16 or fp32, not {dtype}")
         out = _output("out", out, (M, N), dtype, a.device, stream)
+        _on_gpu(self.ws, codes=a, scales=a_scale, out=out,
+                exchange=None if exchange is None else exchange.slot_pos)
         g = (0, None, None) if exchange is None else (exchange.block_m, exchange.expert_ids,
                                                       exchange.num_tokens_post_padded)
         moe_gemm_fp8_block(a, a_scale, int(by_block), q, s, M, N, K, self.E, *g, _row_type(out.dtype), out,
@@ -795,6 +819,8 @@ class FP8Weights:
         if accumulate and out is None:
             raise ValueError("accumulate needs the gradients to add to")
         out = _output("out", out, (self.E, self.N, self.K), torch.float32, d.device, stream)
+        _on_gpu(self.ws, d=d, d_scale=d_scale, x=x, x_scale=x_scale, out=out,
+                exchange=None if exchange is None else exchange.slot_pos)
         counts = None if exchange is None else exchange.segment_counts(stream)
         moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E, counts, out, int(accumulate),
                             self.ws, self.ws.numel(), stream)
@@ -838,7 +864,9 @@ class BlockNorm:
         y = _output("y", y, h.shape, h.dtype, h.device, stream)
         if w_pre is not None:
             z = _output("z", z, h.shape, h.dtype, h.device, stream)
-        moe_block_norm(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
+        row_type = _row_type(h.dtype)
+        _on_gpu(self.ws, h=h, residual=residual, gate=gate, w_post=w_post, w_pre=w_pre, y=y, z=z)
+        moe_block_norm(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
                        self.scale, self.weight_offset, self.eps, y, z, self.rstd_h, self.rstd_y, stream)
         return y, z
 
@@ -853,7 +881,9 @@ class BlockNorm:
                                                      h.dtype if self.gate_kind == MOE_GATE_FULL else f32),
              "dw_post": None if w_post is None else new("dw_post", (self.H,), f32),
              "dw_pre": None if w_pre is None else new("dw_pre", (self.H,), f32)}
-        moe_block_norm_backward(_row_type(h.dtype), h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
+        row_type = _row_type(h.dtype)
+        _on_gpu(self.ws, h=h, residual=residual, dy=dy, dz=dz, w_post=w_post, w_pre=w_pre, gate=gate)
+        moe_block_norm_backward(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
                                 self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
                                 g["dh"], g["dgate"], g["dw_post"], g["dw_pre"], self.ws, self.ws_bytes, stream)
         return g

@@ -1,0 +1,71 @@
+"""What the operator classes refuse on the host beyond shapes, strides and types: nothing here needs a GPU."""
+import pytest
+import torch
+
+from mixture_experts_grouped_moe_gb300 import build as moe_build
+
+
+@pytest.fixture(scope="module")
+def moe():
+    moe_build.build()
+    from mixture_experts_grouped_moe_gb300 import moe as m
+    m.load()
+    return m
+
+
+T, K_, E, H = 8, 2, 4, 128
+BF = torch.bfloat16
+
+
+def test_tensors_off_the_gpu(moe):
+    """Right shapes and types, but addresses that a kernel must not be given."""
+    ex = moe.TokenExchange(T, K_, E, 128, device="cpu")
+    P = ex.P
+    x, ys = torch.zeros(T, H, dtype=BF), torch.zeros(P, H, dtype=BF)
+    w = moe.FP8Weights.__new__(moe.FP8Weights)  # (its constructor quantises on the GPU)
+    w.E, w.N, w.K, w.training, w.ws = E, 256, H, True, torch.zeros(64, dtype=torch.uint8)
+    w.q, w.s = torch.zeros(E, 256, H, dtype=torch.uint8), torch.ones(E, 2, 1)
+    w.qt, w.st = torch.zeros(E, H, 256, dtype=torch.uint8), torch.ones(E, 1, 2)
+    R = 128 * (-(-P // 128))
+    q, s = torch.zeros(P, H, dtype=torch.uint8), torch.ones(P, 1)
+    d, ds = torch.zeros(P, 256, dtype=torch.uint8), torch.ones(P, 2)
+    dt, xt = torch.zeros(256, R, dtype=torch.uint8), torch.zeros(H, R, dtype=torch.uint8)
+    dts, xts = torch.ones(R // 128, 256), torch.ones(R // 128, H)
+    n = moe.BlockNorm(T, H, moe.MOE_GATE_CHANNEL, device="cpu")
+    gate = torch.ones(H, dtype=BF)
+    for call in (
+        lambda: ex.sort(torch.zeros(T, K_, dtype=torch.int32), torch.zeros(T, K_), stream=0),
+        lambda: ex.permute(x),
+        lambda: ex.permute_fp8(x),
+        lambda: ex.unpermute(ys),
+        lambda: ex.unpermute_backward(x, ys),
+        lambda: ex.permute_backward(ys),
+        lambda: moe.FP8Weights(torch.zeros(1, 128, 128, dtype=BF)),
+        lambda: w.update(torch.zeros(E, 256, H, dtype=BF)),
+        lambda: w.product(q, s, exchange=ex),
+        lambda: w.input_gradient(d, ds, exchange=ex),
+        lambda: w.weight_gradient(dt, dts, xt, xts, exchange=ex),
+        lambda: n.forward(x, x, gate=gate),
+        lambda: n.backward(x, x, x, None, gate=gate),
+    ):
+        with pytest.raises(ValueError, match="on one GPU"):
+            call()
+
+
+def test_device_check_names_the_tensor(moe):
+    a = torch.zeros(2)
+    with pytest.raises(ValueError, match="x is on cpu"):
+        moe._on_gpu(a, none=None, x=a)
+    moe._on_gpu(a, none=None)
+
+    class OnGpu:  # a stand-in for CUDA tensors of two devices
+        def __init__(self, index):
+            self.index, self.device = index, f"cuda:{index}"
+
+        def get_device(self):
+            return self.index
+
+    moe._on_gpu(OnGpu(0), x=OnGpu(0))
+    for owner, t in ((OnGpu(0), OnGpu(1)), (OnGpu(0), a), (a, OnGpu(0))):
+        with pytest.raises(ValueError):
+            moe._on_gpu(owner, x=t)
