@@ -573,6 +573,11 @@ class TokenExchange:
                             self.slot_pos, self.num_left_out, self.ws, self.ws_bytes, stream)
         self.weights = topk_weights
 
+    def check_sorted(self):
+        """Raises before the first sort(): the maps are unwritten memory until then."""
+        if self.weights is None:
+            raise ValueError("the exchange has no routing yet: sort() comes first")
+
     def segment_counts(self, stream=None):
         """Rows of each expert's segment, for moe_wgrad_fp8_block, which starts an expert after ceil(count / 128)
         blocks of 128 of each one before it: with larger sort blocks a segment's padding may hold whole blocks of
@@ -607,6 +612,7 @@ class TokenExchange:
         xs = _output("xs", xs, (self.P, H), x.dtype, x.device, stream)
         row_type = _row_type(x.dtype)
         _on_gpu(self.slot_pos, x=x, xs=xs)
+        self.check_sorted()
         moe_permute(row_type, x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T,
                     self.k, H, self.P, int(zero_padding), xs, stream)
         return xs
@@ -623,6 +629,7 @@ class TokenExchange:
             q = _output("q", None, (self.P, H), torch.uint8, x.device, stream)
         s = _output("s", s, (H // 128, self.P), torch.float32, x.device, stream)
         _on_gpu(self.slot_pos, x=x, q=q, s=s)
+        self.check_sorted()
         moe_permute_fp8(x, ld, self.slot_pos, self.sorted_ids, self.num_tokens_post_padded, self.T, self.k, H, self.P,
                         int(zero_padding), q, s, stream)
         return q, s
@@ -633,6 +640,7 @@ class TokenExchange:
         out, ld = self._token_rows("out", out, H, ys.dtype, ys.device, stream)
         row_type = _row_type(ys.dtype)
         _on_gpu(self.slot_pos, ys=ys, out=out)
+        self.check_sorted()
         moe_unpermute(row_type, ys, self.slot_pos, self.weights if weights else None, self.T, self.k, H,
                       self.P, out, ld, stream)
         return out
@@ -646,6 +654,7 @@ class TokenExchange:
         dw = _output("dweights", None, (self.T, self.k), torch.float32, ys.device, stream)
         row_type = _row_type(ys.dtype)
         _on_gpu(self.slot_pos, dout=dout, ys=ys)
+        self.check_sorted()
         moe_unpermute_backward(row_type, dout, ld, ys, self.slot_pos, self.weights, self.sorted_ids,
                                self.num_tokens_post_padded, self.T, self.k, H, self.P, int(zero_padding), dys, dw,
                                stream)
@@ -657,6 +666,7 @@ class TokenExchange:
         dx, ld = self._token_rows("dx", dx, H, dxs.dtype, dxs.device, stream)
         row_type = _row_type(dxs.dtype)
         _on_gpu(self.slot_pos, dxs=dxs, dx=dx)
+        self.check_sorted()
         moe_permute_backward(row_type, dxs, self.slot_pos, self.T, self.k, H, self.P, dx, ld, stream)
         return dx
 
@@ -785,6 +795,8 @@ class FP8Weights:
         out = _output("out", out, (M, N), dtype, a.device, stream)
         _on_gpu(self.ws, codes=a, scales=a_scale, out=out,
                 exchange=None if exchange is None else exchange.slot_pos)
+        if exchange is not None:
+            exchange.check_sorted()
         g = (0, None, None) if exchange is None else (exchange.block_m, exchange.expert_ids,
                                                       exchange.num_tokens_post_padded)
         moe_gemm_fp8_block(a, a_scale, int(by_block), q, s, M, N, K, self.E, *g, _row_type(out.dtype), out,
@@ -821,6 +833,8 @@ class FP8Weights:
         out = _output("out", out, (self.E, self.N, self.K), torch.float32, d.device, stream)
         _on_gpu(self.ws, d=d, d_scale=d_scale, x=x, x_scale=x_scale, out=out,
                 exchange=None if exchange is None else exchange.slot_pos)
+        if exchange is not None:
+            exchange.check_sorted()
         counts = None if exchange is None else exchange.segment_counts(stream)
         moe_wgrad_fp8_block(d, d_scale, x, x_scale, d.shape[1], self.N, self.K, self.E, counts, out, int(accumulate),
                             self.ws, self.ws.numel(), stream)

@@ -69,3 +69,38 @@ def test_device_check_names_the_tensor(moe):
     for owner, t in ((OnGpu(0), OnGpu(1)), (OnGpu(0), a), (a, OnGpu(0))):
         with pytest.raises(ValueError):
             moe._on_gpu(owner, x=t)
+
+
+def test_exchange_before_its_sort(moe, monkeypatch):
+    """The maps are unwritten until sort(): every use of them is refused, and allowed after it."""
+    monkeypatch.setattr(moe, "_on_gpu", lambda *a, **k: None)
+    launched = []
+    for name in ("moe_align_sort_drop", "moe_permute", "moe_permute_fp8", "moe_unpermute", "moe_unpermute_backward",
+                 "moe_permute_backward", "moe_gemm_fp8_block", "moe_wgrad_fp8_block"):
+        monkeypatch.setattr(moe, name, lambda *a, name=name: launched.append(name))
+    ex = moe.TokenExchange(T, K_, E, 128, device="cpu")
+    P = ex.P
+    R = 128 * (-(-P // 128))
+    x, ys = torch.zeros(T, H, dtype=BF), torch.zeros(P, H, dtype=BF)
+    w = moe.FP8Weights.__new__(moe.FP8Weights)
+    w.E, w.N, w.K, w.training, w.ws = E, 256, H, True, torch.zeros(64, dtype=torch.uint8)
+    w.q = w.s = w.qt = w.st = None
+    uses = (
+        lambda: ex.permute(x),
+        lambda: ex.permute_fp8(x),
+        lambda: ex.unpermute(ys),
+        lambda: ex.unpermute_backward(x, ys),
+        lambda: ex.permute_backward(ys),
+        lambda: w.product(torch.zeros(P, H, dtype=torch.uint8), torch.ones(P, 1), exchange=ex),
+        lambda: w.input_gradient(torch.zeros(P, 256, dtype=torch.uint8), torch.ones(P, 2), exchange=ex),
+        lambda: w.weight_gradient(torch.zeros(256, R, dtype=torch.uint8), torch.ones(R // 128, 256),
+                                  torch.zeros(H, R, dtype=torch.uint8), torch.ones(R // 128, H), exchange=ex),
+    )
+    for use in uses:
+        with pytest.raises(ValueError, match="sort"):
+            use()
+    assert not launched
+    ex.sort(torch.zeros(T, K_, dtype=torch.int32), torch.zeros(T, K_))
+    for use in uses:
+        use()
+    assert len(launched) == 1 + len(uses)
