@@ -854,6 +854,7 @@ class BlockNorm:
         self.T, self.H, self.gate_kind = T, H, gate_kind
         self.scale, self.weight_offset, self.eps = scale, weight_offset, eps
         self.rstd_h, self.rstd_y = (torch.empty(T, dtype=torch.float32, device=device) for _ in range(2))
+        self.kept = ()  # the norms whose statistics the last forward() has left
         self.ws_bytes = moe_block_norm_workspace_size(T, H)
         if self.ws_bytes == 0:
             raise MoEError("moe_block_norm_workspace_size", MOE_ERR_INVALID_ARG)
@@ -882,10 +883,12 @@ class BlockNorm:
         _on_gpu(self.ws, h=h, residual=residual, gate=gate, w_post=w_post, w_pre=w_pre, y=y, z=z)
         moe_block_norm(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
                        self.scale, self.weight_offset, self.eps, y, z, self.rstd_h, self.rstd_y, stream)
+        self.kept = tuple(n for n, w in (("w_post", w_post), ("w_pre", w_pre)) if w is not None)
         return y, z
 
     def backward(self, h, residual, dy, dz, w_post=None, w_pre=None, gate=None, stream=None):
-        """Returns dict d_residual, dh, dgate, dw_post, dw_pre (None where there is no such input)."""
+        """Gradients of the last forward(), from its statistics: dict d_residual, dh, dgate, dw_post, dw_pre (None
+        where there is no such input)."""
         import torch
         self._check(h, w_post, w_pre, gate, residual=residual, dy=dy, dz=dz)
         f32, shape = torch.float32, self._gate_shape()
@@ -897,6 +900,9 @@ class BlockNorm:
              "dw_pre": None if w_pre is None else new("dw_pre", (self.H,), f32)}
         row_type = _row_type(h.dtype)
         _on_gpu(self.ws, h=h, residual=residual, dy=dy, dz=dz, w_post=w_post, w_pre=w_pre, gate=gate)
+        for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+            if w is not None and name not in self.kept:
+                raise ValueError(f"{name}: no forward() with this norm has left its statistics")
         moe_block_norm_backward(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
                                 self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
                                 g["dh"], g["dgate"], g["dw_post"], g["dw_pre"], self.ws, self.ws_bytes, stream)

@@ -104,3 +104,27 @@ def test_exchange_before_its_sort(moe, monkeypatch):
     for use in uses:
         use()
     assert len(launched) == 1 + len(uses)
+
+
+def test_norm_backward_before_its_forward(moe, monkeypatch):
+    """The statistics are unwritten until a forward() with that norm: a backward that reads them is refused."""
+    monkeypatch.setattr(moe, "_on_gpu", lambda *a, **k: None)
+    launched = []
+    for name in ("moe_block_norm", "moe_block_norm_backward"):
+        monkeypatch.setattr(moe, name, lambda *a, name=name: launched.append(name))
+    n = moe.BlockNorm(T, H, device="cpu")
+    x, w = torch.zeros(T, H, dtype=BF), torch.ones(H, dtype=BF)
+    both = lambda: n.backward(x, x, x, x, w_post=w, w_pre=w)  # noqa: E731
+    post = lambda: n.backward(x, x, x, None, w_post=w)  # noqa: E731
+    for call in (both, post):
+        with pytest.raises(ValueError, match="statistics"):
+            call()
+    n.backward(x, x, x, None)  # (no norm: no statistics)
+    n.forward(x, x, w_post=w)
+    post()
+    with pytest.raises(ValueError, match="w_pre"):
+        both()
+    n.forward(x, x, w_post=w, w_pre=w)
+    both()
+    post()
+    assert launched.count("moe_block_norm_backward") == 4
