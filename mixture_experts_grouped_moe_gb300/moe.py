@@ -779,13 +779,18 @@ class FP8Weights:
                 self.qt.copy_(self.q.transpose(1, 2))
                 self.st.copy_(self.s.transpose(1, 2))
 
+    def _check_exchange(self, exchange):
+        if (exchange is None and self.E != 1) or (exchange is not None and exchange.E != self.E):
+            raise ValueError(f"{self.E} experts take sorted rows and the exchange of {self.E} experts that sorted them")
+
     def _product(self, a, a_scale, by_block, q, s, N, K, exchange, out, out_dtype, stream):
         import torch
         if a.dim() != 2 or a.shape[1] != K or not a.is_contiguous():
             raise ValueError(f"expected contiguous rows of {K} codes, got {tuple(a.shape)}")
         M = a.shape[0]
-        if (exchange is None) != (self.E == 1) or (exchange is not None and (M, self.E) != (exchange.P, exchange.E)):
-            raise ValueError("several experts take sorted rows [P] and the exchange that sorted them")
+        self._check_exchange(exchange)
+        if exchange is not None and M != exchange.P:
+            raise ValueError(f"expected the exchange's {exchange.P} sorted rows, got {M}")
         _expect("codes", a, (M, K), *_codes())
         KB = -(-K // 128)
         _expect("scales", a_scale, (KB, M) if by_block else (M, KB), torch.float32)
@@ -804,8 +809,8 @@ class FP8Weights:
         return out
 
     def product(self, a, a_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
-        """rows [M][K] (codes, scales) times W^T -> [M][N]; with several experts, each sorted row times its
-        expert's."""
+        """rows [M][K] (codes, scales) times W^T -> [M][N]; with an exchange (several experts need one), each
+        sorted row times its expert's."""
         return self._product(a, a_scale, by_block, self.q, self.s, self.N, self.K, exchange, out, out_dtype, stream)
 
     def input_gradient(self, d, d_scale, by_block=False, exchange=None, out=None, out_dtype=None, stream=None):
@@ -817,8 +822,7 @@ class FP8Weights:
     def weight_gradient(self, d, d_scale, x, x_scale, exchange=None, out=None, accumulate=False, stream=None):
         """(d [N][P], x [K][P], as moe_quantize_fp8_act_t gives them) -> fp32 [E][N][K]."""
         import torch
-        if (exchange is None) != (self.E == 1) or (exchange is not None and self.E != exchange.E):
-            raise ValueError("several experts take sorted rows and the exchange that sorted them")
+        self._check_exchange(exchange)
         if d.dim() != 2:
             raise ValueError(f"expected codes [N][P], got {tuple(d.shape)}")
         P = d.shape[1]
