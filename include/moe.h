@@ -469,6 +469,8 @@ int moe_align_sort_noalloc(const int32_t *topk_ids, const float *topk_weights, i
  * result rounded once.  None of these entries uses floating-point atomics:
  * results are bitwise reproducible.  Rows that start and end on 16-byte
  * boundaries are moved 16 bytes at a time, others element by element.
+ * Counts of zero (tokens, rows) are valid; pointers that are not said to be
+ * optional are non-null in such a call too, and nothing behind them is read.
  */
 #define MOE_ROW_BF16 0
 #define MOE_ROW_FP16 1

@@ -45,7 +45,8 @@ EXPORTED = [
     "moe_quantize_fp8_act", "moe_quantize_fp8_weights", "moe_quantize_fp8_rows", "moe_fused_forward",
     "moe_host_staging_bytes", "moe_fused_forward_host", "moe_align_sort_noalloc", "moe_quantize_mxfp4",
     "moe_train_workspace_size", "moe_fused_forward_train", "moe_fused_backward", "moe_options_init",
-    "moe_fused_forward_ex", "moe_align_sort_map", "moe_align_sort_drop", "moe_permute", "moe_permute_fp8", "moe_permute_backward",
+    "moe_fused_forward_ex", "moe_align_sort_map", "moe_align_sort_drop", "moe_permute",
+    "moe_permute_fp8", "moe_permute_backward",
     "moe_unpermute", "moe_unpermute_backward", "moe_gemm_fp8_block", "moe_wgrad_fp8_block",
     "moe_quantize_fp8_act_t", "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
 ]
@@ -154,6 +155,12 @@ def _p(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _pn(t, n, instead=256):
+    """Raw pointer of a tensor of n rows.  An empty tensor's is null, which the entry points turn down where
+    they need a pointer; with n = 0 they touch nothing behind it, so any aligned address (`instead`) will do."""
+    return _p(t) or (_p(instead) if t is not None and n == 0 else None)
 
 
 _raw_stream = None  # () -> cudaStream_t of the current device's current stream
@@ -367,75 +374,80 @@ def moe_fused_backward(x, W_router, router_bias, W_gate_up, W_down, dout, T, H, 
 def moe_align_sort_map(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
                        num_tokens_post_padded, expert_counts, slot_pos, ws, ws_bytes, stream=None):
     """moe_align_sort that also writes slot_pos, the sorted position of each slot."""
+    P = T * k + E * block_m - k
     return _check("moe_align_sort_map", load().moe_align_sort_map(
-        _p(topk_ids), _p(topk_weights), T, k, E, block_m, _p(sorted_ids), _p(sorted_weights),
-        _p(sorted_expert_ids), _p(num_tokens_post_padded), _p(expert_counts), _p(slot_pos), _p(ws), ws_bytes,
+        _pn(topk_ids, T), _pn(topk_weights, T), T, k, E, block_m, _pn(sorted_ids, P), _pn(sorted_weights, P),
+        _pn(sorted_expert_ids, P), _p(num_tokens_post_padded), _p(expert_counts), _pn(slot_pos, T), _p(ws), ws_bytes,
         _stream(stream)))
 
 
 def moe_align_sort_drop(topk_ids, topk_weights, T, k, E, block_m, sorted_ids, sorted_weights, sorted_expert_ids,
                         num_tokens_post_padded, expert_counts, slot_pos, num_left_out, ws, ws_bytes, stream=None):
     """moe_align_sort_map where an id outside [0, E) leaves its slot out instead of refusing the routing."""
+    P = T * k + E * block_m - k
     return _check("moe_align_sort_drop", load().moe_align_sort_drop(
-        _p(topk_ids), _p(topk_weights), T, k, E, block_m, _p(sorted_ids), _p(sorted_weights),
-        _p(sorted_expert_ids), _p(num_tokens_post_padded), _p(expert_counts), _p(slot_pos), _p(num_left_out), _p(ws),
-        ws_bytes, _stream(stream)))
+        _pn(topk_ids, T), _pn(topk_weights, T), T, k, E, block_m, _pn(sorted_ids, P), _pn(sorted_weights, P),
+        _pn(sorted_expert_ids, P), _p(num_tokens_post_padded), _p(expert_counts), _pn(slot_pos, T), _p(num_left_out),
+        _p(ws), ws_bytes, _stream(stream)))
 
 
 def moe_permute(row_type, x, ld_x, slot_pos, sorted_ids, num_tokens_post_padded, T, k, H, P, zero_padding, xs,
                 stream=None):
     return _check("moe_permute", load().moe_permute(
-        row_type, _p(x), ld_x, _p(slot_pos), _p(sorted_ids), _p(num_tokens_post_padded), T, k, H, P, zero_padding,
-        _p(xs), _stream(stream)))
+        row_type, _pn(x, T), ld_x, _pn(slot_pos, T), _pn(sorted_ids, T and P), _p(num_tokens_post_padded), T, k, H, P,
+        zero_padding, _pn(xs, T and P), _stream(stream)))
 
 
 def moe_permute_fp8(x, ld_x, slot_pos, sorted_ids, num_tokens_post_padded, T, k, H, P, zero_padding, q, s,
                     stream=None):
     return _check("moe_permute_fp8", load().moe_permute_fp8(
-        _p(x), ld_x, _p(slot_pos), _p(sorted_ids), _p(num_tokens_post_padded), T, k, H, P, zero_padding, _p(q), _p(s),
-        _stream(stream)))
+        _pn(x, T), ld_x, _pn(slot_pos, T), _pn(sorted_ids, T and P), _p(num_tokens_post_padded), T, k, H, P,
+        zero_padding, _pn(q, T and P), _pn(s, T and P), _stream(stream)))
 
 
 def moe_permute_backward(row_type, dxs, slot_pos, T, k, H, P, dx, ld_dx, stream=None):
     return _check("moe_permute_backward", load().moe_permute_backward(
-        row_type, _p(dxs), _p(slot_pos), T, k, H, P, _p(dx), ld_dx, _stream(stream)))
+        row_type, _pn(dxs, T and P), _pn(slot_pos, T), T, k, H, P, _pn(dx, T), ld_dx, _stream(stream)))
 
 
 def moe_unpermute(row_type, ys, slot_pos, topk_weights, T, k, H, P, out, ld_out, stream=None):
     return _check("moe_unpermute", load().moe_unpermute(
-        row_type, _p(ys), _p(slot_pos), _p(topk_weights), T, k, H, P, _p(out), ld_out, _stream(stream)))
+        row_type, _pn(ys, T and P), _pn(slot_pos, T), _p(topk_weights), T, k, H, P, _pn(out, T), ld_out,
+        _stream(stream)))
 
 
 def moe_unpermute_backward(row_type, dout, ld_dout, ys, slot_pos, topk_weights, sorted_ids, num_tokens_post_padded,
                            T, k, H, P, zero_padding, dys, dweights, stream=None):
     return _check("moe_unpermute_backward", load().moe_unpermute_backward(
-        row_type, _p(dout), ld_dout, _p(ys), _p(slot_pos), _p(topk_weights), _p(sorted_ids),
-        _p(num_tokens_post_padded), T, k, H, P, zero_padding, _p(dys), _p(dweights), _stream(stream)))
+        row_type, _pn(dout, T), ld_dout, _pn(ys, T and P), _pn(slot_pos, T), _p(topk_weights),
+        _pn(sorted_ids, T and P), _p(num_tokens_post_padded), T, k, H, P, zero_padding, _pn(dys, T and P),
+        _pn(dweights, T), _stream(stream)))
 
 
 def moe_gemm_fp8_block(A, a_scale, a_scale_by_block, B, b_scale, M, N, K, E, block_m, sorted_expert_ids,
                        num_tokens_post_padded, out_type, D, ld_d, ws, ws_bytes, stream=None):
     return _check("moe_gemm_fp8_block", load().moe_gemm_fp8_block(
-        _p(A), _p(a_scale), a_scale_by_block, _p(B), _p(b_scale), M, N, K, E, block_m, _p(sorted_expert_ids),
-        _p(num_tokens_post_padded), out_type, _p(D), ld_d, _p(ws), ws_bytes, _stream(stream)))
+        _pn(A, M), _pn(a_scale, M), a_scale_by_block, _p(B), _p(b_scale), M, N, K, E, block_m,
+        _pn(sorted_expert_ids, M), _p(num_tokens_post_padded), out_type, _pn(D, M), ld_d, _p(ws), ws_bytes,
+        _stream(stream)))
 
 
 def moe_wgrad_fp8_block(A, a_scale, B, b_scale, P, M, N, E, expert_counts, D, accumulate, ws, ws_bytes, stream=None):
     return _check("moe_wgrad_fp8_block", load().moe_wgrad_fp8_block(
-        _p(A), _p(a_scale), _p(B), _p(b_scale), P, M, N, E, _p(expert_counts), _p(D), accumulate, _p(ws), ws_bytes,
-        _stream(stream)))
+        _pn(A, P, ws), _pn(a_scale, P, ws), _pn(B, P, ws), _pn(b_scale, P, ws), P, M, N, E, _p(expert_counts), _p(D),
+        accumulate, _p(ws), ws_bytes, _stream(stream)))
 
 
 def moe_quantize_fp8_act_t(X, ld_x, R, C, sorted_ids, S, k, num_rows, q, ld_q, s, stream=None):
     return _check("moe_quantize_fp8_act_t", load().moe_quantize_fp8_act_t(
-        _p(X), ld_x, R, C, _p(sorted_ids), S, k, _p(num_rows), _p(q), ld_q, _p(s), _stream(stream)))
+        _pn(X, R), ld_x, R, C, _p(sorted_ids), S, k, _p(num_rows), _pn(q, R), ld_q, _pn(s, R), _stream(stream)))
 
 
 def moe_block_norm(row_type, h, residual, gate, gate_kind, w_post, w_pre, T, H, scale, weight_offset, eps, y, z,
                    rstd_h, rstd_y, stream=None):
     return _check("moe_block_norm", load().moe_block_norm(
-        row_type, _p(h), _p(residual), _p(gate), gate_kind, _p(w_post), _p(w_pre), T, H, scale, weight_offset, eps,
-        _p(y), _p(z), _p(rstd_h), _p(rstd_y), _stream(stream)))
+        row_type, _pn(h, T), _pn(residual, T), _pn(gate, T), gate_kind, _p(w_post), _p(w_pre), T, H, scale,
+        weight_offset, eps, _pn(y, T), _pn(z, T), _p(rstd_h), _p(rstd_y), _stream(stream)))
 
 
 def moe_block_norm_workspace_size(T, H) -> int:
@@ -444,10 +456,11 @@ def moe_block_norm_workspace_size(T, H) -> int:
 
 def moe_block_norm_backward(row_type, h, residual, gate, gate_kind, w_post, w_pre, rstd_h, rstd_y, dy, dz, T, H, scale,
                             weight_offset, d_residual, dh, dgate, dw_post, dw_pre, ws, ws_bytes, stream=None):
+    gates = H if gate_kind == MOE_GATE_CHANNEL else T  # (without rows, a column's gate and its gradient are still used)
     return _check("moe_block_norm_backward", load().moe_block_norm_backward(
-        row_type, _p(h), _p(residual), _p(gate), gate_kind, _p(w_post), _p(w_pre), _p(rstd_h), _p(rstd_y), _p(dy), _p(dz),
-        T, H, scale, weight_offset, _p(d_residual), _p(dh), _p(dgate), _p(dw_post), _p(dw_pre), _p(ws), ws_bytes,
-        _stream(stream)))
+        row_type, _pn(h, T), _pn(residual, T), _pn(gate, gates), gate_kind, _p(w_post), _p(w_pre), _pn(rstd_h, T),
+        _pn(rstd_y, T), _pn(dy, T), _pn(dz, T), T, H, scale, weight_offset, _pn(d_residual, T), _pn(dh, T),
+        _pn(dgate, gates), _p(dw_post), _p(dw_pre), _p(ws), ws_bytes, _stream(stream)))
 
 
 class MoETrain:

@@ -128,3 +128,42 @@ def test_norm_backward_before_its_forward(moe, monkeypatch):
     both()
     post()
     assert launched.count("moe_block_norm_backward") == 4
+
+
+def test_empty_tensors(moe):
+    """A batch without rows has null addresses: the calls that then launch nothing accept it."""
+    none = lambda *s, dt=BF: torch.empty(*s, dtype=dt)  # noqa: E731
+    i32, one = torch.int32, torch.zeros(1, dtype=torch.int32)
+    assert none(0, H).data_ptr() == 0
+    pos, wts, sid = none(0, dt=i32), none(0, K_, dt=torch.float32), torch.zeros(64, dtype=i32)
+    xs, q, s = none(64, H), none(64, H, dt=torch.uint8), none(1, 64, dt=torch.float32)
+    bf, f32 = moe.MOE_ROW_BF16, torch.float32
+    moe.moe_permute(bf, none(0, H), H, pos, sid, one, 0, K_, H, 64, 1, xs, stream=0)
+    moe.moe_permute(bf, none(0, H), H, pos, pos, one, 0, K_, H, 0, 1, none(0, H), stream=0)
+    moe.moe_permute_fp8(none(0, H), H, pos, sid, one, 0, K_, H, 64, 1, q, s, stream=0)
+    moe.moe_unpermute(bf, xs, pos, wts, 0, K_, H, 64, none(0, H), H, stream=0)
+    moe.moe_unpermute_backward(bf, none(0, H), H, xs, pos, wts, sid, one, 0, K_, H, 64, 1, xs, wts, stream=0)
+    moe.moe_permute_backward(bf, xs, pos, 0, K_, H, 64, none(0, H), H, stream=0)
+    b, sb, ws = none(64, H, dt=torch.uint8), none(1, 1, dt=f32), torch.zeros(64, dtype=torch.uint8)
+    codes, scales = none(0, H, dt=torch.uint8), none(0, 1, dt=f32)
+    moe.moe_gemm_fp8_block(codes, scales, 0, b, sb, 0, 64, H, 1, 0, None, None, bf, none(0, 64), 64, ws, 64, stream=0)
+    moe.moe_gemm_fp8_block(codes, scales, 0, b, sb, 0, 64, H, 1, 16, pos, one, bf, none(0, 64), 64, ws, 64, stream=0)
+    moe.moe_quantize_fp8_act_t(none(0, H), H, 0, H, pos, 0, 1, one, none(H, 0, dt=torch.uint8), 0,
+                               none(0, H, dt=f32), stream=0)
+    for kind, gate in ((moe.MOE_GATE_NONE, None), (moe.MOE_GATE_TOKEN, none(0)), (moe.MOE_GATE_FULL, none(0, H))):
+        moe.moe_block_norm(bf, none(0, H), none(0, H), gate, kind, one, one, 0, H, 1.0, 0.0, 1e-6, none(0, H),
+                           none(0, H), none(0, dt=f32), none(0, dt=f32), stream=0)
+
+
+def test_empty_tensors_where_rows_are_expected(moe):
+    """With rows to move, a null address stays an error."""
+    x, pos, xs = torch.zeros(T, H, dtype=BF), torch.zeros(T * K_, dtype=torch.int32), torch.zeros(64, H, dtype=BF)
+    none, bf = torch.empty(0, dtype=BF), moe.MOE_ROW_BF16
+    for args in ((none, pos, xs), (x, none, xs), (x, pos, none)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_permute(bf, args[0], H, args[1], None, None, T, K_, H, 64, 0, args[2], stream=0)
+    with pytest.raises(moe.MoEError):
+        moe.moe_block_norm(bf, none, x, None, 0, None, None, T, H, 1.0, 0.0, 1e-6, x, None, None, None, stream=0)
+    with pytest.raises(moe.MoEError):  # no tokens, but padding rows to write
+        i32, n = torch.zeros(64, dtype=torch.int32), torch.empty(0, dtype=torch.int32)
+        moe.moe_align_sort_drop(n, torch.empty(0), 0, 2, 4, 16, n, xs, i32, i32, i32, n, i32, i32, 1 << 20, stream=0)
