@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<TN, WG>::kThreads, Cfg<TN, WG>::kCtas) gem
             float4(*ep)[4] = sm.ep_out[warp - kFirstPromo];
             const int rr = lane >> 2, cq = lane & 3;
             const int n0 = tl.col0 + sub * kCols;
-            const int64_t left = a.M - tl.row0 - q * 32;  // rows of D from lane 0's
+            const int64_t left = rows - tl.row0 - q * 32;  // rows of D from lane 0's
             const int es = a.out_f32 ? 4 : 2, per = 16 / es;
             uint8_t *dst[4];
 #pragma unroll
