@@ -160,7 +160,9 @@ def _p(t):
 def _pn(t, n, instead=256):
     """Raw pointer of a tensor of n rows.  An empty tensor's is null, which the entry points turn down where
     they need a pointer; with n = 0 they touch nothing behind it, so any aligned address (`instead`) will do."""
-    return _p(t) or (_p(instead) if t is not None and n == 0 else None)
+    if n:
+        return t if t is None or isinstance(t, int) else t.data_ptr()
+    return _p(t) or (_p(instead) if t is not None else None)
 
 
 _raw_stream = None  # () -> cudaStream_t of the current device's current stream
@@ -500,12 +502,17 @@ class MoETrain:
 
 # ------------------------------------------------------------- conveniences
 
+_row_types = {}  # of torch's types, filled at the first use
+
+
 def _row_type(dtype):
-    import torch
-    types = {torch.bfloat16: MOE_ROW_BF16, torch.float16: MOE_ROW_FP16, torch.float32: MOE_ROW_FP32}
-    if dtype not in types:
+    if not _row_types:
+        import torch
+        _row_types.update({torch.bfloat16: MOE_ROW_BF16, torch.float16: MOE_ROW_FP16, torch.float32: MOE_ROW_FP32})
+    row_type = _row_types.get(dtype)
+    if row_type is None:
         raise TypeError(f"rows are bf16, fp16 or fp32, not {dtype}")
-    return types[dtype]
+    return row_type
 
 
 def _expect(name, t, shape, *dtypes):
@@ -522,6 +529,12 @@ def _on_gpu(owner, **tensors):
     """The tensors (None passes) are on the GPU of `owner`, a tensor of the object whose method is called: a
     kernel is given their addresses.  Checked last, right before a launch."""
     gpu = owner.get_device()  # (-1: not on a GPU)
+    for t in tensors.values():
+        if t is not None and t.get_device() != gpu:
+            break
+    else:
+        if gpu >= 0:
+            return
     for name, t in tensors.items():
         if t is not None and (gpu < 0 or t.get_device() != gpu):
             raise ValueError(f"{name} is on {t.device}, what belongs to the operator on {owner.device}: "
@@ -601,10 +614,11 @@ class TokenExchange:
             return (self.expert_counts + (self.block_m - 1)) // self.block_m * self.block_m
 
     def _rows(self, x):
-        if x.dim() != 2 or x.shape[0] != self.T or (x.shape[1] > 1 and x.stride(1) != 1):
-            raise ValueError(f"expected {self.T} rows with contiguous elements, got {tuple(x.shape)}")
+        shape = x.shape
+        if len(shape) != 2 or shape[0] != self.T or (shape[1] > 1 and x.stride(1) != 1):
+            raise ValueError(f"expected {self.T} rows with contiguous elements, got {tuple(shape)}")
         # (a single row's stride means nothing to torch, which may give any)
-        return x.shape[1], x.shape[1] if self.T == 1 else x.stride(0)
+        return shape[1], shape[1] if self.T == 1 else x.stride(0)
 
     def _token_rows(self, name, t, H, dtype, device, stream):
         """Token rows to write [T][H]: t (rows may be strided) after its checks, or new."""
@@ -615,9 +629,10 @@ class TokenExchange:
         return t, ld
 
     def _sorted(self, ys):
-        if ys.dim() != 2 or ys.shape[0] != self.P or not ys.is_contiguous():
-            raise ValueError(f"expected {self.P} contiguous sorted rows, got {tuple(ys.shape)}")
-        return ys.shape[1]
+        shape = ys.shape
+        if len(shape) != 2 or shape[0] != self.P or not ys.is_contiguous():
+            raise ValueError(f"expected {self.P} contiguous sorted rows, got {tuple(shape)}")
+        return shape[1]
 
     def permute(self, x, xs=None, zero_padding=True, stream=None):
         """x [T][H] -> sorted rows [P][H]."""
@@ -798,9 +813,10 @@ class FP8Weights:
 
     def _product(self, a, a_scale, by_block, q, s, N, K, exchange, out, out_dtype, stream):
         import torch
-        if a.dim() != 2 or a.shape[1] != K or not a.is_contiguous():
-            raise ValueError(f"expected contiguous rows of {K} codes, got {tuple(a.shape)}")
-        M = a.shape[0]
+        shape = a.shape
+        if len(shape) != 2 or shape[1] != K or not a.is_contiguous():
+            raise ValueError(f"expected contiguous rows of {K} codes, got {tuple(shape)}")
+        M = shape[0]
         self._check_exchange(exchange)
         if exchange is not None and M != exchange.P:
             raise ValueError(f"expected the exchange's {exchange.P} sorted rows, got {M}")
@@ -871,24 +887,27 @@ class BlockNorm:
         self.T, self.H, self.gate_kind = T, H, gate_kind
         self.scale, self.weight_offset, self.eps = scale, weight_offset, eps
         self.rstd_h, self.rstd_y = (torch.empty(T, dtype=torch.float32, device=device) for _ in range(2))
-        self.kept = ()  # the norms whose statistics the last forward() has left
+        self.kept = False, False  # the norms (after, before) whose statistics the last forward() has left
         self.ws_bytes = moe_block_norm_workspace_size(T, H)
         if self.ws_bytes == 0:
             raise MoEError("moe_block_norm_workspace_size", MOE_ERR_INVALID_ARG)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
 
     def _check(self, h, w_post, w_pre, gate, **rows):
-        _expect("h", h, (self.T, self.H), h.dtype)
+        shape, columns, dtype = (self.T, self.H), (self.H,), h.dtype
+        _expect("h", h, shape, dtype)
         for name, t in rows.items():
-            _expect(name, t, (self.T, self.H), h.dtype)
-        _expect("w_post", w_post, (self.H,), h.dtype)
-        _expect("w_pre", w_pre, (self.H,), h.dtype)
+            _expect(name, t, shape, dtype)
+        _expect("w_post", w_post, columns, dtype)
+        _expect("w_pre", w_pre, columns, dtype)
         if self.gate_kind != MOE_GATE_NONE:
-            _expect("gate", gate, self._gate_shape(), h.dtype)
+            _expect("gate", gate, self._gate_shape(), dtype)
 
     def _gate_shape(self):
-        return {MOE_GATE_NONE: None, MOE_GATE_CHANNEL: (self.H,), MOE_GATE_TOKEN: (self.T,),
-                MOE_GATE_FULL: (self.T, self.H)}[self.gate_kind]
+        kind = self.gate_kind
+        if kind == MOE_GATE_CHANNEL:
+            return self.H,
+        return None if kind == MOE_GATE_NONE else (self.T,) if kind == MOE_GATE_TOKEN else (self.T, self.H)
 
     def forward(self, h, residual, w_post=None, w_pre=None, gate=None, y=None, z=None, stream=None):
         """Returns (y, z): the residual stream after the block and the next block's input (None without w_pre)."""
@@ -900,7 +919,7 @@ class BlockNorm:
         _on_gpu(self.ws, h=h, residual=residual, gate=gate, w_post=w_post, w_pre=w_pre, y=y, z=z)
         moe_block_norm(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.T, self.H,
                        self.scale, self.weight_offset, self.eps, y, z, self.rstd_h, self.rstd_y, stream)
-        self.kept = tuple(n for n, w in (("w_post", w_post), ("w_pre", w_pre)) if w is not None)
+        self.kept = w_post is not None, w_pre is not None
         return y, z
 
     def backward(self, h, residual, dy, dz, w_post=None, w_pre=None, gate=None, stream=None):
@@ -917,8 +936,8 @@ class BlockNorm:
              "dw_pre": None if w_pre is None else new("dw_pre", (self.H,), f32)}
         row_type = _row_type(h.dtype)
         _on_gpu(self.ws, h=h, residual=residual, dy=dy, dz=dz, w_post=w_post, w_pre=w_pre, gate=gate)
-        for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-            if w is not None and name not in self.kept:
+        for name, w, kept in (("w_post", w_post, self.kept[0]), ("w_pre", w_pre, self.kept[1])):
+            if w is not None and not kept:
                 raise ValueError(f"{name}: no forward() with this norm has left its statistics")
         moe_block_norm_backward(row_type, h, residual, gate, self.gate_kind, w_post, w_pre, self.rstd_h,
                                 self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
