@@ -517,9 +517,9 @@ int moe_permute(int row_type, const void *x, int64_t ld_x, const int32_t *slot_p
 
 /*
  * The same for bf16 rows, quantised per 1x128 group as moe_quantize_fp8_act
- * does: q (device) e4m3 [P][H], s (device) fp32 [H/128][P] (by block: the
- * a_scale_by_block = 1 form of moe_gemm_fp8_block).  A padding row that is
- * zeroed has scale 1.  H % 128 == 0, ld_x % 8 == 0, x and q on 16-byte
+ * does (a negative zero's code is that of zero): q (device) e4m3 [P][H], s
+ * (device) fp32 [H/128][P] (by block: the a_scale_by_block = 1 form of
+ * moe_gemm_fp8_block).  A padding row that is zeroed has scale 1.  H % 128 == 0, ld_x % 8 == 0, x and q on 16-byte
  * boundaries.
  */
 int moe_permute_fp8(const void *x, int64_t ld_x, const int32_t *slot_pos, const int32_t *sorted_ids,
@@ -604,7 +604,8 @@ int moe_wgrad_fp8_block(const uint8_t *A, const float *a_scale, const uint8_t *B
 
 /*
  * Transposing quantiser for moe_wgrad_fp8_block: per column c and 128 rows,
- * scale = amax / 448 (1 if zero) and codes as moe_quantize_fp8_act.
+ * scale = amax / 448 (1 if zero) and codes as moe_quantize_fp8_act (a
+ * negative zero's code is that of zero).
  *   X (device) bf16 rows of C at a pitch of ld_x; with sorted_ids (device,
  *   int32 [R]) row p is X's row sorted_ids[p] / k, zero where sorted_ids[p] is
  *   outside [0, S) (padding); NULL: row p of X;

@@ -416,7 +416,7 @@ cudaError_t run_bwd(RowArgs &a, bool zero, cudaStream_t st)
     return run_bwd_w<T, VEC, 8>(a, zero, st);
 }
 
-// Shape checks shared by the entries: MOE_OK, a negative status, or 1 for T = 0 (nothing to do).
+// Shape checks shared by the entries: MOE_OK or a negative status.
 int check_exchange(int row_type, int T, int k, int H, int64_t P, int64_t ld)
 {
     if (row_size(row_type) == 0 || T < 0 || k <= 0 || H <= 0 || P < 0 || ld < H)

@@ -11,10 +11,14 @@
 // while the tensor core fills the next buffer.  K need not be a multiple of 128: the copies zero-fill
 // past the end, and a zero code adds nothing.
 //
-// Bounds and figures (one GB300): large products by the board's power -- 4096 tokens top-2, N 14336, K 4096
-// of eight experts take 476 us (2.02 PFLOP/s) with the SM clock held at 1725-1770 of 2070 MHz; few rows by HBM
-// -- 32 tokens, N 28672, K 4096 of eight experts in 147 us, 6.4 TB/s; one row, N 4096, K 14336 in 17.8 us; the
-// weight gradient by its promotion (4096 x 14336 of eight experts, 841 us).
+// Bounds and figures (one GB300): large products by the hand-off of every block of K between the tensor core
+// and the promotion warps (a single launch has the tensor pipe active half of the time and 36 % of the issue
+// slots in use) and, back to back, by the board's power as well -- 4096 tokens top-2, N 14336, K 4096 of eight
+// experts take 450 us (2.14 PFLOP/s) in launches apart at 2070 MHz and 476-492 us in a row, where the power
+// limit holds the SM clock at 1680-1800 MHz; few rows by HBM -- 32 tokens, N 28672, K 4096 of eight experts in
+// 147 us, 6.4 TB/s; one row, N 4096, K 14336 in 17.8 us.  The weight gradient (4096 x 14336 of eight experts,
+// 841 us) fills neither the tensor pipe (24 %) nor the issue slots (40 %): its promotion waits for every load
+// from TMEM before the arithmetic on it.
 #include <cuda_bf16.h>
 
 #include "gemm_common.cuh"

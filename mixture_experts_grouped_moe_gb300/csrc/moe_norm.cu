@@ -10,25 +10,27 @@
 //   v = dn (w_post + offset)         dh = r_h (v - hh mean(v hh))
 //   dw_post = sum_rows dn hh         dgate = scale * n * D, summed over what it was broadcast over
 //
-// Bound by HBM: the forward reads h and the residual and writes y and z once each, the backward
-// reads h, the residual, dy and dz and writes d residual and dh once each.  A row stays in one block's
-// registers between its passes (a row needs its own two sums before its results), so nothing is
-// read twice.  All sums are fp32.  z is computed from y before y's rounding, and the backward forms
-// the same unrounded y again from h and the residual: reading the rounded y instead would cost the
-// same bytes and leave the sums over the rows off by bf16's 2^-9.  The column sums (dw, per-column
-// dgate) are
-// kept in registers over the rows that a block walks and written as one partial row per block;
+// From HBM the forward reads h and the residual and writes y and z once each, the backward reads h, the
+// residual, dy and dz and writes d residual and dh once each.  A row needs its own two sums before its
+// results.  The forward keeps the row in registers between its passes.  The backward reads it again, h in
+// three passes, the residual and dz in two: from shared memory where rows are copied ahead (below), else
+// from global memory.  A gate per element is read in every pass that uses it.  All sums are fp32.  z is
+// computed from y before y's rounding, and the backward forms the same unrounded y again from h and the
+// residual: reading the rounded y instead would cost the same bytes and leave the sums over the rows off
+// by bf16's 2^-9.  The column sums (dw, per-column dgate) are kept in registers over the rows that a block walks and written as one partial row per block;
 // a second launch adds the partial rows in order, so the gradients are bitwise reproducible.
 //
 // A row's two sums are a chain of barriers, so a block that loads its next row only after this one
 // leaves HBM idle most of the time.  The blocks are persistent and copy the next rows ahead into
 // shared memory (cp.async; each thread copies exactly the pieces that it will read itself, so no
 // barrier guards the ring).  8192 rows of 4096 bf16 with a gate per column: forward 44 us (6.0 TB/s; 103 us
-// without the ring), forward and backward 153 (250), 8192 rows of 2048 86 (123), of 4096 fp32 214 (384);
-// rows of 16384 gain in the forward only (64 / 73), since one block an SM has its barriers to itself.  A third
-// row in the ring was no faster (155 and 48 us again, fp32 220).  Rows that are no whole number of 16-byte
-// pieces go by single elements and without the ring (8192 rows of 401, forward: 17.8 us); the widest of
-// those (over 4096 elements) no longer fit a thread's registers, 8192 rows of 4097 taking 300 us forward.
+// without the ring), forward and backward 153 (250), 8192 rows of 2048 86 (123), of 4096 fp32 214 (384).
+// 2048 rows of 16384 have the ring in the forward only (64-68 us, 73 without): two rows of the backward's four
+// arrays are more than an SM's shared memory, and forward and backward take 303 us.  A third row in the
+// ring was no faster (155 and 48 us again, fp32 220).  Rows that are no whole number of 16-byte pieces go by
+// single elements and without the ring (8192 rows of 401, forward: 17.8 us; of 1001 46.5, with the backward
+// 170); the widest of those (over 4096 elements) no longer fit a thread's registers, 8192 rows of 4097 taking
+// 300 us forward and 1760 with the backward.
 #include "moe_internal.h"
 #include "rows.cuh"
 #include "sm100_ptx.cuh"
