@@ -482,6 +482,7 @@ int moe_align_sort_noalloc(const int32_t *topk_ids, const float *topk_weights, i
  * id is outside [0, E).  Everything else as moe_align_sort (same ws): such an
  * id is an error, num_tokens_post_padded = -1 refuses the whole routing, and
  * the entries below that read it then zero no padding and compute no row.
+ * Limit: T*k + E*block_m - k < 2^31.
  */
 int moe_align_sort_map(const int32_t *topk_ids, const float *topk_weights, int T, int k, int E, int block_m,
                        int32_t *sorted_ids, float *sorted_weights, int32_t *sorted_expert_ids,

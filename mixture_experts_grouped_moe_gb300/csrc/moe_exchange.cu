@@ -440,7 +440,8 @@ static int sort_with_map(const int32_t *topk_ids, const float *topk_weights, int
 {
     if (T < 0 || k <= 0 || E <= 0 || block_m <= 0)
         return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || k > E || (int64_t)T * k > (int64_t)1 << 30)
+    if (E > 1024 || k > E || (int64_t)T * k > (int64_t)1 << 30 ||
+        (int64_t)T * k + (int64_t)E * block_m - k > INT32_MAX)  // (positions are int32)
         return MOE_ERR_UNSUPPORTED;
     if (!topk_ids || !topk_weights || !sorted_ids || !sorted_weights || !sorted_expert_ids ||
         !num_tokens_post_padded || !slot_pos || !ws)

@@ -167,3 +167,15 @@ def test_empty_tensors_where_rows_are_expected(moe):
     with pytest.raises(moe.MoEError):  # no tokens, but padding rows to write
         i32, n = torch.zeros(64, dtype=torch.int32), torch.empty(0, dtype=torch.int32)
         moe.moe_align_sort_drop(n, torch.empty(0), 0, 2, 4, 16, n, xs, i32, i32, i32, n, i32, i32, 1 << 20, stream=0)
+
+
+@pytest.mark.parametrize("entry", ["map", "drop"])
+def test_sorts_past_32_bits(moe, entry):
+    """Sorted positions are int32: blocks so large that they could pass it are refused before a launch."""
+    fn = getattr(moe, "moe_align_sort_" + entry)
+    P = 1024  # a non-null, aligned stand-in for a device pointer
+    args = (P,) * 6 + ((P,) if entry == "drop" else ())
+    for T, k, E, block_m in ((1 << 20, 2, 1024, 1 << 21), (4, 1, 2, 1 << 30), (1 << 20, 4, 512, (1 << 22) - 1)):
+        with pytest.raises(moe.MoEError) as err:
+            fn(P, P, T, k, E, block_m, *args, P, 1 << 40, stream=0)
+        assert err.value.status == moe.MOE_ERR_UNSUPPORTED
