@@ -153,7 +153,7 @@ def prepare(case, seed):
         wts = 0.5 + torch.rand(T, generator=g, device=DEV)
         s["dloss"] = wts / max(1, T)
         s["dx"], s["dw"] = torch.empty(T, H, dtype=dt, device=DEV), torch.empty_like(s["w"])
-        bytes_ += T * H * 4 + T * s["piece"] * 2
+        bytes_ += T * H * 6 + T * s["piece"] * 2
     s["ws"] = torch.zeros(bytes_, dtype=torch.uint8, device=DEV)
     return s
 
