@@ -664,6 +664,119 @@ int moe_block_norm_backward(int row_type, const void *h, const void *residual, c
                             void *d_residual, void *dh, void *dgate, float *dw_post, float *dw_pre, void *ws,
                             size_t ws_bytes, void *stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The rest of a training step: the gated feed-forward block that every token
+ * passes, the cross entropy at the end, and the clipping of all gradients.
+ *
+ * Matrices of the first two are bf16 or fp16 (row_type; MOE_ROW_FP32 is
+ * MOE_ERR_UNSUPPORTED) with fp32 sums; they start on 16-byte boundaries, H and
+ * I are multiples of 8, and so are the pitches of rows.  T is any number, also
+ * 0.  Each workspace starts with a status word that the caller zeroes once
+ * before the first call; a call whose wait runs out leaves MOE_ERR_TIMEOUT in
+ * it (read with moe_workspace_status).  Results are bitwise reproducible.
+ */
+#define MOE_ACT_SILU 0       /* g sigmoid(g) */
+#define MOE_ACT_GELU_TANH 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+#define MOE_ACT_RELU 2       /* max(g, 0) */
+
+/* Workspace bytes of moe_ffn (training = 0) and of moe_ffn_backward and a
+ * moe_ffn that is given h (training = 1); 0 on invalid or unsupported sizes. */
+size_t moe_ffn_workspace_size(int64_t T, int H, int I, int training);
+
+/*
+ * The gated feed-forward block (a shared expert next to the routed ones, or a
+ * dense layer):
+ *   g = x W_gate^T, u = x W_up^T, h = act(g) * u, out = add + h W_down^T
+ *   x (device) [T] rows of H at a pitch of ld_x;
+ *   W_gate_up (device) [2I][H], gate rows first; W_down (device) [H][I];
+ *   add (device) [T] rows of H at a pitch of ld_add, or NULL (nothing is
+ *   added; ld_add is ignored);
+ *   out (device) [T] rows of H at a pitch of ld_out; it may be add, with its
+ *   pitch;
+ *   gu (device) [T][2I] (g | u of a row, rounded) and h (device) [T][I]: kept
+ *   for the backward; both may be NULL, and gu with h given.
+ * h is rounded to row_type before its product.  ws (device)
+ * moe_ffn_workspace_size bytes.
+ */
+int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
+            const void *add, int64_t ld_add, int64_t T, int H, int I, void *gu, void *h, void *out, int64_t ld_out,
+            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of moe_ffn for loss = sum(dout * out) (that of add is dout):
+ *   gu, h as the forward kept them; dout (device) [T] rows at a pitch of
+ *   ld_dout;
+ *   dx (device) [T] rows at a pitch of ld_dx; dW_gate_up (device) [2I][H] and
+ *   dW_down (device) [H][I], of grad_type (row_type or MOE_ROW_FP32); each of
+ *   the three may be NULL and is then not computed;
+ *   accumulate = 1 adds the weight gradients to what is there (one rounding of
+ *   the sum), 0 overwrites it;
+ *   ws (device) moe_ffn_workspace_size(..., 1) bytes.
+ */
+int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
+                     const void *gu, const void *h, const void *dout, int64_t ld_dout, int64_t T, int H, int I,
+                     void *dx, int64_t ld_dx, int grad_type, int accumulate, void *dW_gate_up, void *dW_down, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* Workspace bytes of moe_vocab_loss (piece = 0), or of it and
+ * moe_vocab_loss_backward with that piece; 0 on invalid or unsupported sizes. */
+size_t moe_vocab_loss_workspace_size(int64_t T, int H, int V, int piece);
+
+/*
+ * Softmax cross entropy over a vocabulary, from the hidden states:
+ *   l = x W^T, lse[t] = log(sum over v of exp(l[t][v])),
+ *   loss[t] = lse[t] - l[t][targets[t]]
+ * and loss[t] = 0 for a row whose target is outside [0, V) (it is left out;
+ * lse is computed for it all the same).  The logits are not kept.
+ *   x (device) [T] rows of H at a pitch of ld_x; W (device) [V][H];
+ *   targets (device) int32 [T]; loss, lse (device) fp32 [T];
+ *   ws (device) moe_vocab_loss_workspace_size bytes.
+ * Any V up to 2^24.
+ */
+int moe_vocab_loss(int row_type, const void *x, int64_t ld_x, const void *W, const int32_t *targets, int64_t T, int H,
+                   int V, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of sum over t of dloss[t] * loss[t]:
+ *   lse as the forward gave it; dloss (device) fp32 [T] (not read into
+ *   anything for a row left out, whose x may be anything too);
+ *   piece: columns of the vocabulary at a time, a multiple of 64 (the
+ *   workspace grows with T * piece, the time with the number of pieces);
+ *   dx (device) [T] rows at a pitch of ld_dx (zeros for a row left out); dW
+ *   (device) [V][H] of grad_type (row_type or MOE_ROW_FP32); each may be NULL;
+ *   accumulate = 1 adds dW to what is there.
+ * The logits' gradients are rounded to row_type (scaled by a power of two so
+ * that fp16 holds them) before their products.
+ */
+int moe_vocab_loss_backward(int row_type, const void *x, int64_t ld_x, const void *W, const int32_t *targets,
+                            const float *lse, const float *dloss, int64_t T, int H, int V, int piece, void *dx,
+                            int64_t ld_dx, int grad_type, int accumulate, void *dW, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* Workspace bytes of moe_grad_norm and moe_clip_gradients for n tensors. */
+#define MOE_CLIP_WS_BYTES(n) ((((size_t)(n) + 511) / 512 + 1) * 9728)
+
+/*
+ * The 2-norm of all elements of n tensors: *norm (device fp32) = sqrt(sum of
+ * squares), summed so that no square overflows or underflows.
+ *   types, grads, numel (host) [n]: MOE_ROW_ type, device address (on a
+ *   boundary of its elements) and number of elements of each tensor; they are
+ *   read during the call.
+ * n <= 65536; n = 0 gives 0.
+ */
+int moe_grad_norm(int n, const int *types, const void *const *grads, const int64_t *numel, float *norm, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/*
+ * The same, then out[i] = grads[i] * min(1, max_norm / (norm + eps)), each
+ * element rounded once to its tensor's type.  out (host) [n]: device addresses; out[i]
+ * may be grads[i], and overlaps no other tensor.  max_norm, eps >= 0.  A norm
+ * that is infinite or a NaN scales as the formula says.
+ */
+int moe_clip_gradients(int n, const int *types, const void *const *grads, void *const *out, const int64_t *numel,
+                       float max_norm, float eps, float *norm, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,11 +47,17 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool encode_tmap_2d(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner, uint64_t rows,
                     uint32_t box_inner, uint32_t box_rows)
 {
+    return encode_tmap_2d_pitched(map, base, elem_bytes, inner, rows, inner, box_inner, box_rows);
+}
+
+bool encode_tmap_2d_pitched(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner, uint64_t rows,
+                            uint64_t pitch, uint32_t box_inner, uint32_t box_rows)
+{
     auto fn = get_encode_fn();
     if (!fn)
         return false;
     cuuint64_t dims[2] = {inner, rows};
-    cuuint64_t strides[1] = {inner * (uint64_t)elem_bytes};
+    cuuint64_t strides[1] = {pitch * (uint64_t)elem_bytes};
     cuuint32_t box[2] = {box_inner, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,

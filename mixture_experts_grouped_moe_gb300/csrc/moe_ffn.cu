@@ -1,0 +1,178 @@
+// The gated feed-forward block that every token passes (a shared expert, a dense layer), 16-bit rows:
+//   h = act(x Wg^T) * (x Wu^T),   out = add + h Wd^T
+// and its gradients
+//   dh = dout Wd,  dg = dh u act'(g),  du = dh act(g),
+//   dx = [dg | du] Wgu,  dWgu = [dg | du]^T x,  dWd = dout^T h.
+// Six products of dense_gemm.cuh; the activation and its gradient are epilogues, and every matrix is read as it
+// lies.  h, and in the backward [dg | du], are rounded to the rows' type between the products (they are operands
+// of 16-bit MMAs): errors of half a step an element, independent ones, that a sum over I or T averages.
+#include "dense_gemm.cuh"
+
+namespace moe {
+namespace {
+
+using namespace dense;
+
+constexpr int64_t kHead = 1024;  // the status word, and what keeps the rest aligned
+
+int64_t up1k(int64_t v) { return (v + 1023) / 1024 * 1024; }
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// A matrix of 16-bit elements in boxes of 64 x box_rows.
+bool map16(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t pitch, int box_rows)
+{
+    return encode_tmap_2d_pitched(m, p, 2, inner, rows, pitch, 64, box_rows);
+}
+
+bool bad_sizes(int64_t T, int H, int I)
+{
+    return H % 8 != 0 || I % 8 != 0 || H > 1 << 20 || I > 1 << 20 || T > 1 << 30;
+}
+
+int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+template <class TE>
+cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *Wgu, const void *Wd, const void *add,
+                    int64_t ld_add, int64_t T, int H, int I, int act, void *gu, void *h, void *out, int64_t ld_out,
+                    float *part, cudaStream_t st)
+{
+    Args a = base;
+    a.M = T, a.N = I, a.K = H;
+    a.act = act, a.h = h, a.gu = gu;
+    if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, Wgu, H, 2 * (int64_t)I, H, 128))
+        return cudaErrorInvalidValue;
+    cudaError_t err = launch<kGated, 0, TE, 256>(a, part, st);
+    if (err != cudaSuccess)
+        return err;
+    a = base;
+    a.M = T, a.N = H, a.K = I;
+    a.d = out, a.ld_d = ld_out, a.add = add, a.ld_add = ld_add;
+    if (!map16(&a.tm_a, h, I, T, I, 128) || !map16(&a.tm_b, Wd, I, H, I, 128))
+        return cudaErrorInvalidValue;
+    return launch<kStore, 0, TE, 256>(a, part, st);
+}
+
+template <class TE>
+cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *Wgu, const void *Wd, const void *gu,
+                     const void *h, const void *dout, int64_t ld_dout, int64_t T, int H, int I, int act, void *dx,
+                     int64_t ld_dx, bool f32, bool accumulate, void *dWgu, void *dWd, void *dgu, float *part,
+                     cudaStream_t st)
+{
+    cudaError_t err = cudaSuccess;
+    Args a = base;
+    if (dx || dWgu) {
+        a.M = T, a.N = I, a.K = H;
+        a.act = act, a.gu = const_cast<void *>(gu), a.dgu = dgu;
+        if (!map16(&a.tm_a, dout, H, T, ld_dout, 128) || !map16(&a.tm_b, Wd, I, H, I, 64))
+            return cudaErrorInvalidValue;
+        if ((err = launch<kGatedBwd, 1, TE, 256>(a, part, st)) != cudaSuccess)
+            return err;
+    }
+    if (dx) {
+        a = base;
+        a.M = T, a.N = H, a.K = 2 * I;
+        a.d = dx, a.ld_d = ld_dx;
+        if (!map16(&a.tm_a, dgu, 2 * (int64_t)I, T, 2 * (int64_t)I, 128) ||
+            !map16(&a.tm_b, Wgu, H, 2 * (int64_t)I, H, 64))
+            return cudaErrorInvalidValue;
+        if ((err = launch<kStore, 1, TE, 256>(a, part, st)) != cudaSuccess)
+            return err;
+    }
+    const auto wgrad = [&](const void *d, int64_t rows, int64_t ld, const void *v, int cols, int64_t ld_v, void *dW) {
+        a = base;
+        a.M = rows, a.N = cols, a.K = (int)T;
+        a.d = dW, a.ld_d = cols, a.d_f32 = f32;
+        if (accumulate)
+            a.add = dW, a.ld_add = cols;
+        if (!map16(&a.tm_a, d, rows, T, ld, 64) || !map16(&a.tm_b, v, cols, T, ld_v, 64))
+            return cudaErrorInvalidValue;
+        return launch<kStore, 2, TE, 256>(a, part, st);
+    };
+    if (dWgu && (err = wgrad(dgu, 2 * (int64_t)I, 2 * (int64_t)I, x, H, ld_x, dWgu)) != cudaSuccess)
+        return err;
+    if (dWd)
+        err = wgrad(dout, H, ld_dout, h, I, I, dWd);
+    return err;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_ffn_workspace_size(int64_t T, int H, int I, int training)
+{
+    if (T < 0 || H <= 0 || I <= 0 || training < 0 || training > 1 || bad_sizes(T, H, I))
+        return 0;
+    return (size_t)(kHead + (int64_t)kPartBytes + up1k(T * I * 2 * (training ? 2 : 1)));
+}
+
+int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
+            const void *add, int64_t ld_add, int64_t T, int H, int I, void *gu, void *h, void *out, int64_t ld_out,
+            void *ws, size_t ws_bytes, void *stream)
+{
+    if (T < 0 || H <= 0 || I <= 0 || act < 0 || act > MOE_ACT_RELU || !x || !W_gate_up || !W_down || !out || !ws ||
+        ld_x < H || ld_out < H || (add && ld_add < H) || row_type < 0 || row_type > MOE_ROW_FP32 || (gu && !h))
+        return MOE_ERR_INVALID_ARG;
+    if (off16(x) || off16(W_gate_up) || off16(W_down) || off16(add) || off16(gu) || off16(h) || off16(out) ||
+        off16(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (row_type == MOE_ROW_FP32 || bad_sizes(T, H, I) || ld_x % 8 != 0 || ld_out % 8 != 0 ||
+        (add && ld_add % 8 != 0) || ld_x > 1ll << 36 || ld_out > 1ll << 36 || ld_add > 1ll << 36)
+        return MOE_ERR_UNSUPPORTED;
+    if (ws_bytes < kHead + kPartBytes + (h ? 0 : (size_t)up1k(T * I * 2)))
+        return MOE_ERR_WORKSPACE;
+    if (T == 0)
+        return MOE_OK;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    Args base = {};
+    base.status = reinterpret_cast<int *>(at);
+    float *part = reinterpret_cast<float *>(at + kHead);
+    if (!h)
+        h = at + kHead + kPartBytes;
+    const auto st = static_cast<cudaStream_t>(stream);
+    const auto go = row_type == MOE_ROW_BF16 ? forward<__nv_bfloat16> : forward<__half>;
+    return to_status(go(base, x, ld_x, W_gate_up, W_down, add, ld_add, T, H, I, act, gu, h, out, ld_out, part, st));
+}
+
+int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
+                     const void *gu, const void *h, const void *dout, int64_t ld_dout, int64_t T, int H, int I,
+                     void *dx, int64_t ld_dx, int grad_type, int accumulate, void *dW_gate_up, void *dW_down, void *ws,
+                     size_t ws_bytes, void *stream)
+{
+    if (T < 0 || H <= 0 || I <= 0 || act < 0 || act > MOE_ACT_RELU || !x || !W_gate_up || !W_down || !gu || !h ||
+        !dout || !ws || ld_x < H || ld_dout < H || (dx && ld_dx < H) || row_type < 0 || row_type > MOE_ROW_FP32 ||
+        accumulate < 0 || accumulate > 1 || (grad_type != row_type && grad_type != MOE_ROW_FP32))
+        return MOE_ERR_INVALID_ARG;
+    if (off16(x) || off16(W_gate_up) || off16(W_down) || off16(gu) || off16(h) || off16(dout) || off16(dx) ||
+        off16(dW_gate_up) || off16(dW_down) || off16(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (row_type == MOE_ROW_FP32 || bad_sizes(T, H, I) || ld_x % 8 != 0 || ld_dout % 8 != 0 ||
+        (dx && ld_dx % 8 != 0) || ld_x > 1ll << 36 || ld_dout > 1ll << 36 || ld_dx > 1ll << 36)
+        return MOE_ERR_UNSUPPORTED;
+    if (ws_bytes < moe_ffn_workspace_size(T, H, I, 1))
+        return MOE_ERR_WORKSPACE;
+    const auto st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // no tokens: gradients of zero
+        const size_t es = grad_type == MOE_ROW_FP32 ? 4 : 2, n = (size_t)H * I * es;
+        cudaError_t err = cudaSuccess;
+        if (!accumulate && dW_gate_up)
+            err = cudaMemsetAsync(dW_gate_up, 0, 2 * n, st);
+        if (!accumulate && dW_down && err == cudaSuccess)
+            err = cudaMemsetAsync(dW_down, 0, n, st);
+        return to_status(err);
+    }
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    Args base = {};
+    base.status = reinterpret_cast<int *>(at);
+    float *part = reinterpret_cast<float *>(at + kHead);
+    void *dgu = at + kHead + kPartBytes;
+    const auto go = row_type == MOE_ROW_BF16 ? backward<__nv_bfloat16> : backward<__half>;
+    return to_status(go(base, x, ld_x, W_gate_up, W_down, gu, h, dout, ld_dout, T, H, I, act, dx, ld_dx,
+                        grad_type == MOE_ROW_FP32, accumulate != 0, dW_gate_up, dW_down, dgu, part, st));
+}
+
+}  // extern "C"

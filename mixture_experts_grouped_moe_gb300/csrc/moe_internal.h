@@ -209,6 +209,9 @@ struct GemmArgs {
 
 bool encode_tmap_2d(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner, uint64_t rows,
                     uint32_t box_inner, uint32_t box_rows);
+// The same with rows `pitch` elements apart.
+bool encode_tmap_2d_pitched(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner, uint64_t rows,
+                            uint64_t pitch, uint32_t box_inner, uint32_t box_rows);
 // A byte buffer of nbytes (a multiple of 16) as rows of 16 bytes, unswizzled, box_rows rows per box.
 bool encode_tmap_rows16(CUtensorMap *map, const void *base, uint64_t nbytes, uint32_t box_rows);
 

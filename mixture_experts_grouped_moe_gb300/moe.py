@@ -37,6 +37,9 @@ MOE_GATE_CHANNEL = 1
 MOE_GATE_TOKEN = 2
 MOE_GATE_FULL = 3
 MOE_GEMM_BLOCK_WS_BYTES = 64
+MOE_ACT_SILU = 0
+MOE_ACT_GELU_TANH = 1
+MOE_ACT_RELU = 2
 
 EXPORTED = [
     "moe_status_string", "moe_version", "moe_align_sort_sizes", "moe_block_size_m_heuristic",
@@ -49,6 +52,8 @@ EXPORTED = [
     "moe_permute_fp8", "moe_permute_backward",
     "moe_unpermute", "moe_unpermute_backward", "moe_gemm_fp8_block", "moe_wgrad_fp8_block",
     "moe_quantize_fp8_act_t", "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
+    "moe_ffn_workspace_size", "moe_ffn", "moe_ffn_backward", "moe_vocab_loss_workspace_size", "moe_vocab_loss",
+    "moe_vocab_loss_backward", "moe_grad_norm", "moe_clip_gradients",
 ]
 
 
@@ -139,6 +144,14 @@ def load(build_if_missing: bool = False):
             "moe_block_norm": (I, [I, P, P, P, I, P, P, I64, I, F, F, F, P, P, P, P, P]),
             "moe_block_norm_workspace_size": (SZ, [I64, I]),
             "moe_block_norm_backward": (I, [I, P, P, P, I, P, P, P, P, P, P, I64, I, F, F, P, P, P, P, P, P, SZ, P]),
+            "moe_ffn_workspace_size": (SZ, [I64, I, I, I]),
+            "moe_ffn": (I, [I, I, P, I64, P, P, P, I64, I64, I, I, P, P, P, I64, P, SZ, P]),
+            "moe_ffn_backward": (I, [I, I, P, I64, P, P, P, P, P, I64, I64, I, I, P, I64, I, I, P, P, P, SZ, P]),
+            "moe_vocab_loss_workspace_size": (SZ, [I64, I, I, I]),
+            "moe_vocab_loss": (I, [I, P, I64, P, P, I64, I, I, P, P, P, SZ, P]),
+            "moe_vocab_loss_backward": (I, [I, P, I64, P, P, P, P, I64, I, I, I, P, I64, I, I, P, P, SZ, P]),
+            "moe_grad_norm": (I, [I, P, P, P, P, P, SZ, P]),
+            "moe_clip_gradients": (I, [I, P, P, P, P, F, F, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -463,6 +476,71 @@ def moe_block_norm_backward(row_type, h, residual, gate, gate_kind, w_post, w_pr
         row_type, _pn(h, T), _pn(residual, T), _pn(gate, gates), gate_kind, _p(w_post), _p(w_pre), _pn(rstd_h, T),
         _pn(rstd_y, T), _pn(dy, T), _pn(dz, T), T, H, scale, weight_offset, _pn(d_residual, T), _pn(dh, T),
         _pn(dgate, gates), _p(dw_post), _p(dw_pre), _p(ws), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------- the rest of a training step
+
+def moe_ffn_workspace_size(T, H, I, training=False) -> int:
+    return load().moe_ffn_workspace_size(T, H, I, int(training))
+
+
+def moe_ffn(row_type, act, x, ld_x, W_gate_up, W_down, add, ld_add, T, H, I, gu, h, out, ld_out, ws, ws_bytes,
+            stream=None):
+    return _check("moe_ffn", load().moe_ffn(
+        row_type, act, _pn(x, T), ld_x, _p(W_gate_up), _p(W_down), _pn(add, T), ld_add, T, H, I, _pn(gu, T), _pn(h, T),
+        _pn(out, T), ld_out, _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_ffn_backward(row_type, act, x, ld_x, W_gate_up, W_down, gu, h, dout, ld_dout, T, H, I, dx, ld_dx, grad_type,
+                     accumulate, dW_gate_up, dW_down, ws, ws_bytes, stream=None):
+    return _check("moe_ffn_backward", load().moe_ffn_backward(
+        row_type, act, _pn(x, T), ld_x, _p(W_gate_up), _p(W_down), _pn(gu, T), _pn(h, T), _pn(dout, T), ld_dout, T, H,
+        I, _pn(dx, T), ld_dx, grad_type, accumulate, _p(dW_gate_up), _p(dW_down), _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_vocab_loss_workspace_size(T, H, V, piece=0) -> int:
+    return load().moe_vocab_loss_workspace_size(T, H, V, piece)
+
+
+def moe_vocab_loss(row_type, x, ld_x, W, targets, T, H, V, loss, lse, ws, ws_bytes, stream=None):
+    return _check("moe_vocab_loss", load().moe_vocab_loss(
+        row_type, _pn(x, T), ld_x, _p(W), _pn(targets, T), T, H, V, _pn(loss, T), _pn(lse, T), _p(ws), ws_bytes,
+        _stream(stream)))
+
+
+def moe_vocab_loss_backward(row_type, x, ld_x, W, targets, lse, dloss, T, H, V, piece, dx, ld_dx, grad_type,
+                            accumulate, dW, ws, ws_bytes, stream=None):
+    return _check("moe_vocab_loss_backward", load().moe_vocab_loss_backward(
+        row_type, _pn(x, T), ld_x, _p(W), _pn(targets, T), _pn(lse, T), _pn(dloss, T), T, H, V, piece, _pn(dx, T),
+        ld_dx, grad_type, accumulate, _p(dW), _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_clip_workspace_size(n) -> int:
+    """MOE_CLIP_WS_BYTES(n)."""
+    return ((n + 511) // 512 + 1) * 9728
+
+
+def _tensor_table(tensors):
+    """The C arrays (types, numbers of elements, addresses) of contiguous tensors."""
+    n = len(tensors)
+    return ((ctypes.c_int * n)(*[_row_type(t.dtype) for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]))
+
+
+def moe_grad_norm(grads, norm, ws, ws_bytes, stream=None):
+    """grads: contiguous bf16, fp16 or fp32 tensors; norm: fp32 [1]."""
+    types, numel, addresses = _tensor_table(grads)
+    return _check("moe_grad_norm", load().moe_grad_norm(len(grads), types, addresses, numel, _p(norm), _p(ws),
+                                                        ws_bytes, _stream(stream)))
+
+
+def moe_clip_gradients(grads, out, max_norm, eps, norm, ws, ws_bytes, stream=None):
+    """grads as in moe_grad_norm; out: tensors of the same types and sizes (the same ones: in place)."""
+    types, numel, addresses = _tensor_table(grads)
+    to = addresses if out is grads else (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out])
+    return _check("moe_clip_gradients", load().moe_clip_gradients(
+        len(grads), types, addresses, to, numel, max_norm, eps, _p(norm), _p(ws), ws_bytes, _stream(stream)))
 
 
 class MoETrain:
@@ -943,3 +1021,211 @@ class BlockNorm:
                                 self.rstd_y, dy, dz, self.T, self.H, self.scale, self.weight_offset, g["d_residual"],
                                 g["dh"], g["dgate"], g["dw_post"], g["dw_pre"], self.ws, self.ws_bytes, stream)
         return g
+
+
+def _token_rows(name, t, shape, dtype):
+    """The pitch of rows [T][H] (their elements contiguous, the rows may be strided)."""
+    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected {tuple(shape)} with contiguous rows, got {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    # (a single row's stride means nothing to torch, which may give any)
+    return shape[1] if shape[0] <= 1 else t.stride(0)
+
+
+def _half_type(dtype):
+    import torch
+    dtype = dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"rows are bf16 or fp16, not {dtype}")
+    return dtype
+
+
+def _weight_gradient(name, t, shape, dtype, grad_dtype, accumulate, device, stream):
+    """A weight gradient to write: t after its checks (it says the type), or new, fp32 unless grad_dtype says else."""
+    import torch
+    if t is None:
+        if accumulate:
+            raise ValueError(f"accumulate needs the gradients to add to: {name}")
+        t = _output(name, None, shape, grad_dtype or torch.float32, device, stream)
+    _expect(name, t, shape, dtype, torch.float32)
+    return t
+
+
+class GatedFFN:
+    """The gated feed-forward block that every token passes (a shared expert next to the routed ones, a dense
+    layer), for T tokens: forward(), and with `training` then backward() (see moe_ffn in include/moe.h).  Owns the
+    workspace and what the backward needs (gate | up and h of the last forward)."""
+
+    def __init__(self, T, H, I, act=MOE_ACT_SILU, dtype=None, training=False, device="cuda"):
+        import torch
+        self.T, self.H, self.I, self.act, self.training = T, H, I, act, training
+        self.dtype = _half_type(dtype)
+        self.row_type = _row_type(self.dtype)
+        self.ws_bytes = moe_ffn_workspace_size(T, H, I, training)
+        if self.ws_bytes == 0:
+            raise MoEError("moe_ffn_workspace_size", MOE_ERR_INVALID_ARG)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.gu = self.h = None
+        if training:
+            self.gu = torch.empty(T, 2 * I, dtype=self.dtype, device=device)
+            self.h = torch.empty(T, I, dtype=self.dtype, device=device)
+        self.kept = False  # whether a forward() has left gu and h
+
+    def _check(self, x, W_gate_up, W_down):
+        _expect("W_gate_up", W_gate_up, (2 * self.I, self.H), self.dtype)
+        _expect("W_down", W_down, (self.H, self.I), self.dtype)
+        return _token_rows("x", x, (self.T, self.H), self.dtype)
+
+    def forward(self, x, W_gate_up, W_down, add=None, out=None, stream=None):
+        """x [T][H] -> add + ffn(x) [T][H]; x, add and out may be strided rows, and out may be add."""
+        shape = (self.T, self.H)
+        ld_x = self._check(x, W_gate_up, W_down)
+        ld_add = 0 if add is None else _token_rows("add", add, shape, self.dtype)
+        if out is None:
+            out = _output("out", None, shape, self.dtype, x.device, stream)
+        ld_out = _token_rows("out", out, shape, self.dtype)
+        _on_gpu(self.ws, x=x, W_gate_up=W_gate_up, W_down=W_down, add=add, out=out)
+        moe_ffn(self.row_type, self.act, x, ld_x, W_gate_up, W_down, add, ld_add, self.T, self.H, self.I, self.gu,
+                self.h, out, ld_out, self.ws, self.ws_bytes, stream)
+        self.kept = self.training
+        return out
+
+    def backward(self, x, W_gate_up, W_down, dout, dW_gate_up=None, dW_down=None, accumulate=False, grad_dtype=None,
+                 stream=None):
+        """Gradients of the last forward(): dict dx, dW_gate_up, dW_down (fp32, or of the rows' type).  Given weight
+        gradients are written, or with `accumulate` added to."""
+        if not self.training:
+            raise ValueError("the backward needs GatedFFN(..., training=True)")
+        shape, dev = (self.T, self.H), x.device
+        ld_x = self._check(x, W_gate_up, W_down)
+        ld_dout = _token_rows("dout", dout, shape, self.dtype)
+        g = {"dx": _output("dx", None, shape, self.dtype, dev, stream),
+             "dW_gate_up": _weight_gradient("dW_gate_up", dW_gate_up, W_gate_up.shape, self.dtype, grad_dtype,
+                                            accumulate, dev, stream),
+             "dW_down": _weight_gradient("dW_down", dW_down, W_down.shape, self.dtype, grad_dtype, accumulate, dev,
+                                         stream)}
+        if g["dW_gate_up"].dtype != g["dW_down"].dtype:
+            raise TypeError("both weight gradients are of one type")
+        _on_gpu(self.ws, x=x, W_gate_up=W_gate_up, W_down=W_down, dout=dout, **g)
+        if not self.kept:
+            raise ValueError("no forward() has left what the backward needs")
+        moe_ffn_backward(self.row_type, self.act, x, ld_x, W_gate_up, W_down, self.gu, self.h, dout, ld_dout, self.T,
+                         self.H, self.I, g["dx"], self.H, _row_type(g["dW_down"].dtype), int(accumulate),
+                         g["dW_gate_up"], g["dW_down"], self.ws, self.ws_bytes, stream)
+        return g
+
+    def status(self, stream=None) -> int:
+        return moe_workspace_status(self.ws, stream)
+
+
+class VocabularyLoss:
+    """Softmax cross entropy of T rows over V words straight from the hidden states, `piece` words at a time in the
+    backward: forward(), and with `training` then backward() (see moe_vocab_loss in include/moe.h).  Owns the
+    workspace and the last forward's lse."""
+
+    def __init__(self, T, H, V, dtype=None, training=False, piece=8192, device="cuda"):
+        import torch
+        self.T, self.H, self.V, self.training, self.piece = T, H, V, training, piece
+        self.dtype = _half_type(dtype)
+        self.row_type = _row_type(self.dtype)
+        self.ws_bytes = 0 if piece <= 0 else moe_vocab_loss_workspace_size(T, H, V, piece if training else 0)
+        if self.ws_bytes == 0:
+            raise MoEError("moe_vocab_loss_workspace_size", MOE_ERR_INVALID_ARG)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.lse = torch.empty(T, dtype=torch.float32, device=device)
+        self.kept = False  # whether a forward() has left lse
+
+    def _check(self, x, W, targets):
+        import torch
+        _expect("W", W, (self.V, self.H), self.dtype)
+        _expect("targets", targets, (self.T,), torch.int32)
+        return _token_rows("x", x, (self.T, self.H), self.dtype)
+
+    def forward(self, x, W, targets, loss=None, stream=None):
+        """x [T][H] (rows may be strided), W [V][H], targets int32 [T] (outside [0, V): the row is left out) ->
+        losses fp32 [T]."""
+        import torch
+        ld_x = self._check(x, W, targets)
+        loss = _output("loss", loss, (self.T,), torch.float32, x.device, stream)
+        _on_gpu(self.ws, x=x, W=W, targets=targets, loss=loss)
+        moe_vocab_loss(self.row_type, x, ld_x, W, targets, self.T, self.H, self.V, loss, self.lse, self.ws,
+                       self.ws_bytes, stream)
+        self.kept = True
+        return loss
+
+    def backward(self, x, W, targets, dloss, dW=None, accumulate=False, grad_dtype=None, stream=None):
+        """Gradients of sum(dloss * loss) of the last forward(), dloss fp32 [T]: dict dx, dW (fp32, or of the rows'
+        type).  A given dW is written, or with `accumulate` added to."""
+        import torch
+        if not self.training:
+            raise ValueError("the backward needs VocabularyLoss(..., training=True)")
+        ld_x = self._check(x, W, targets)
+        _expect("dloss", dloss, (self.T,), torch.float32)
+        g = {"dx": _output("dx", None, (self.T, self.H), self.dtype, x.device, stream),
+             "dW": _weight_gradient("dW", dW, W.shape, self.dtype, grad_dtype, accumulate, x.device, stream)}
+        _on_gpu(self.ws, x=x, W=W, targets=targets, dloss=dloss, **g)
+        if not self.kept:
+            raise ValueError("no forward() has left its lse")
+        moe_vocab_loss_backward(self.row_type, x, ld_x, W, targets, self.lse, dloss, self.T, self.H, self.V,
+                                self.piece, g["dx"], self.H, _row_type(g["dW"].dtype), int(accumulate), g["dW"],
+                                self.ws, self.ws_bytes, stream)
+        return g
+
+    def status(self, stream=None) -> int:
+        return moe_workspace_status(self.ws, stream)
+
+
+class GradientClip:
+    """The norm of all elements of up to n gradients, and their clipping to max_norm (see moe_clip_gradients in
+    include/moe.h).  Owns the workspace."""
+
+    def __init__(self, max_norm, eps=1e-6, n=512, device="cuda"):
+        import torch
+        if not (max_norm >= 0 and eps >= 0 and 0 <= n <= 65536):
+            raise ValueError("expected max_norm and eps of at least 0, and up to 65536 gradients")
+        self.max_norm, self.eps, self.n = max_norm, eps, n
+        self.ws_bytes = moe_clip_workspace_size(n)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    def _tensors(self, name, tensors):
+        tensors = list(tensors)
+        if len(tensors) > self.n:
+            raise ValueError(f"{len(tensors)} {name}, more than this object's {self.n}")
+        for i, t in enumerate(tensors):
+            _row_type(t.dtype)
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: expected a contiguous tensor, got strides {t.stride()}")
+        return tensors
+
+    def norm(self, grads, norm=None, stream=None):
+        """grads: contiguous bf16, fp16 and fp32 tensors of any shapes -> their norm, fp32 [1]."""
+        import torch
+        grads = self._tensors("gradients", grads)
+        norm = _output("norm", norm, (1,), torch.float32, self.ws.device, stream)
+        _on_gpu(self.ws, norm=norm, **{f"grads[{i}]": t for i, t in enumerate(grads)})
+        moe_grad_norm(grads, norm, self.ws, self.ws_bytes, stream)
+        return norm
+
+    def clip(self, grads, out=None, norm=None, stream=None):
+        """Scales the gradients by min(1, max_norm / (norm + eps)), in place or into `out`, and returns their norm
+        from before, fp32 [1].  No two of the tensors written overlap."""
+        import torch
+        grads = self._tensors("gradients", grads)
+        norm = _output("norm", norm, (1,), torch.float32, self.ws.device, stream)
+        to = grads if out is None else self._tensors("outputs", out)
+        if len(to) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, but {len(to)} outputs")
+        for i, (g, t) in enumerate(zip(grads, to)):
+            if t is not g:
+                _expect(f"out[{i}]", t, g.shape, g.dtype)
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in to if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("tensors to write overlap: each would be scaled more than once")
+        tensors = {f"grads[{i}]": t for i, t in enumerate(grads)}
+        if to is not grads:
+            tensors.update({f"out[{i}]": t for i, t in enumerate(to)})
+        _on_gpu(self.ws, norm=norm, **tensors)
+        moe_clip_gradients(grads, to, self.max_norm, self.eps, norm, self.ws, self.ws_bytes, stream)
+        return norm
