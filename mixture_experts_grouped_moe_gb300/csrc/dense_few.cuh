@@ -1,0 +1,310 @@
+// Dense products of few rows (T <= 128 tokens): streaming the weights.  The operands are swapped: 128 weight rows
+// are the MMA's M side and the tokens, rounded up to NP = 16, 32, 64 or 128, its N side, so that nothing is padded
+// to 256 rows and a stage of the pipeline is nearly all weights.  A gated tile holds 64 gate rows and the matching
+// 64 up rows, so that both products of a column end in one CTA.
+//
+// A CTA does one tile, or, with few tiles, 1/S of a tile's K: the S <= 8 CTAs of a cluster add their fp32 parts
+// through distributed shared memory (each gets the parts of 128/S rows, adds them in ascending order and applies
+// the epilogue).  Two CTAs fit an SM (about 100 KB each, up to 64 tokens), so that up to 304 tiles or parts stream
+// at once, and a kernel that follows in the same call starts while this one still runs: it brings its first
+// stages of weights before it waits for the tokens (griddepcontrol.wait).
+#pragma once
+
+#include "dense_gemm.cuh"
+
+namespace moe {
+namespace dense {
+
+constexpr int kFewMost = 128;  // tokens
+
+template <int NP>
+constexpr int kFewStageBytes = 16384 + NP * 128;
+template <int NP>
+constexpr int kFewStages = NP == 16 ? 5 : NP == 32 ? 4 : NP == 64 ? 3 : 4;
+
+template <int NP>
+struct __align__(1024) FewSmem {
+    uint8_t stage[kFewStages<NP>][kFewStageBytes<NP>];
+    float red[128 * NP];  // [S][NP][128 / S]: every CTA's part of the rows that this one finishes
+    uint64_t full[kFewStages<NP>];
+    uint64_t empty[kFewStages<NP>];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort;
+};
+template <int NP>
+constexpr size_t kFewSmemBytes = sizeof(FewSmem<NP>) + 1024;
+static_assert(2 * (kFewSmemBytes<16> + 1024) <= 228 * 1024 && 2 * (kFewSmemBytes<32> + 1024) <= 228 * 1024 &&
+                  2 * (kFewSmemBytes<64> + 1024) <= 228 * 1024 && kFewSmemBytes<128> <= 227 * 1024,
+              "two CTAs an SM up to 64 tokens");
+
+// a.tm_a: tokens in boxes of 64 x NP; a.tm_b: weights in boxes of 64 x (gated 64, else 128); a.M tokens, a.N
+// features, a.S CTAs a tile.  early: the weights may be read before what precedes the kernel has ended.
+template <int MODE, class TE, int NP>
+__global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ Args a, int early)
+{
+    using SmemT = FewSmem<NP>;
+    constexpr int kS = kFewStages<NP>;
+    constexpr int kTile = MODE == kGated ? 64 : 128;  // features of a tile
+    extern __shared__ uint8_t smem_raw[];
+    SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.S;
+    const int rank = blockIdx.x % S, tile = blockIdx.x / S;
+    volatile int *abort_flag = &sm.abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kS; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&a.tm_a);
+        tma_prefetch_desc(&a.tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, NP < 32 ? 32 : NP);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // every CTA of the cluster has started before any of them writes to another's shared memory
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const uint32_t tmem_base = sm.tmem_base;
+    const int nkb = (a.K + 63) / 64;
+    const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+            const auto weights = [&](int s, int kb) {
+                mbar_arrive_expect_tx(&sm.full[s], kFewStageBytes<NP>);
+                tma_load_2d(sm.stage[s], &a.tm_b, kb * 64, tile * kTile, &sm.full[s], once);
+                if (MODE == kGated)
+                    tma_load_2d(sm.stage[s] + 8192, &a.tm_b, kb * 64, a.N + tile * kTile, &sm.full[s], once);
+            };
+            const auto tokens = [&](int s, int kb) {
+                tma_load_2d(sm.stage[s] + 16384, &a.tm_a, kb * 64, 0, &sm.full[s], keep);
+            };
+            const int pre = early ? min(kS, kb1 - kb0) : 0;
+            for (int i = 0; i < pre; ++i)
+                weights(i, kb0 + i);
+            pdl_wait();
+            for (int i = 0; i < pre; ++i)
+                tokens(i, kb0 + i);
+            int s = pre % kS;
+            uint32_t ph = pre / kS;
+            for (int kb = kb0 + pre; kb < kb1; ++kb) {
+                if (!mbar_wait(&sm.empty[s], ph ^ 1, a.status, abort_flag)) {
+                    // copies in flight: a bounded moment for them to land
+                    const unsigned long long t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 20000000ull) {
+                    }
+                    break;
+                }
+                weights(s, kb);
+                tokens(s, kb);
+                if (++s == kS) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t type = std::is_same<TE, __nv_bfloat16>::value ? 1u : 0u;
+            const uint32_t idesc = make_idesc(type, type, 128, NP);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag))
+                    break;
+                tc_fence_after();
+                const uint8_t *w = sm.stage[s], *x = sm.stage[s] + 16384;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16(tmem_base, smem_desc_sw128(w + kk * 32), smem_desc_sw128(x + kk * 32), idesc,
+                             (kb > kb0 || kk > 0) ? 1u : 0u);
+                mma_commit(&sm.empty[s]);
+                if (++s == kS) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            mma_commit(&sm.done);
+        }
+    } else {
+        pdl_wait();
+        pdl_trigger();
+        const int q = warp & 3;
+        const int r = q * 32 + lane;  // weight row
+        ok = mbar_wait(&sm.done, 0, a.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        // rows that a CTA of the cluster finishes: 128 / S consecutive ones, gated as many gate rows and up rows
+        const int own = 128 / S;
+        int owner, local;
+        if (MODE == kGated) {
+            const int half = own / 2;
+            owner = r % 64 / half;
+            local = r / 64 * half + r % half;
+        } else {
+            owner = r / own;
+            local = r % own;
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const uint32_t dst = cluster_map(sm.red, owner) + (uint32_t)((rank * NP * own + local) * 4);
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
+        constexpr int kC = NP < 32 ? 16 : 32;
+#pragma unroll 1
+        for (int c = 0; c < NP; c += kC) {
+            float v[kC];
+            if constexpr (kC == 16)
+                tmem_ld16(tacc + c, v);
+            else
+                tmem_ld32(tacc + c, v);
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+                if (c + i < a.M)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)((c + i) * own * 4)),
+                                 "f"(v[i])
+                                 : "memory");
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (warp < 2)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_sync();  // every part has arrived; (S = 1: the block's own barrier)
+    if (warp >= 2 && ok) {
+        const int t = threadIdx.x - 64;
+        const int own = 128 / S;
+        const auto sum = [&](int col, int local) {
+            float v = 0.0f;
+            for (int s = 0; s < S; ++s)
+                v += sm.red[(s * NP + col) * own + local];
+            return v;
+        };
+        if (MODE == kGated) {
+            const int half = own / 2, f0 = tile * 64 + rank * half;
+            for (int e = t; e < half * (int)a.M; e += 128) {
+                const int i = e % half, col = e / half, f = f0 + i;
+                if (f >= a.N)
+                    continue;
+                const float g = sum(col, i), u = sum(col, half + i);
+                static_cast<TE *>(a.h)[(int64_t)col * a.N + f] = row_from_f<TE>(act_of(g, a.act) * u);
+                if (a.gu) {
+                    TE *kept = static_cast<TE *>(a.gu) + (int64_t)col * 2 * a.N + f;
+                    kept[0] = row_from_f<TE>(g);
+                    kept[a.N] = row_from_f<TE>(u);
+                }
+            }
+        } else if (MODE == kStore) {
+            const int f0 = tile * 128 + rank * own;
+            for (int e = t; e < own * (int)a.M; e += 128) {
+                const int i = e % own, col = e / own, f = f0 + i;
+                if (f >= a.N)
+                    continue;
+                float v = sum(col, i);
+                if (a.add)
+                    v += row_to_f(static_cast<const TE *>(a.add)[col * a.ld_add + f]);
+                static_cast<TE *>(a.d)[col * a.ld_d + f] = row_from_f<TE>(v);
+            }
+        } else {
+            // logits: a warp a token, its maximum and sum of exponentials over the rows finished here
+            const int f0 = tile * 128 + rank * own;
+            for (int col = warp - 2; col < (int)a.M; col += 4) {
+                float v[4], m = -INFINITY;
+                const int target = a.targets[col];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = lane + 32 * j;
+                    v[j] = i < own && f0 + i < a.N ? sum(col, i) : -INFINITY;
+                    if (i < own && f0 + i == target && target < a.N)
+                        a.target_logit[col] = v[j];
+                    m = fmaxf(m, v[j]);
+                }
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                const float base = m == -INFINITY ? 0.0f : m * kLog2e;
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s += exp2_fast(fmaf(v[j], kLog2e, -base));
+                s = warp_sum(s);
+                if (lane == 0)
+                    a.stats[(int64_t)col * a.tiles_n * S + tile * S + rank] = make_float2(m, s);
+            }
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, NP < 32 ? 32 : NP);
+}
+
+// ------------------------------------------------------------------- host
+
+// CTAs that share a tile: doubled while all parts run at once (`slots`) and each keeps at least four blocks of K.
+inline int few_split(int64_t tiles, int K, int slots)
+{
+    int S = 1;
+    while (S < 8 && tiles * 2 * S <= slots && (K + 63) / 64 / (2 * S) >= 4)
+        S *= 2;
+    return S;
+}
+
+template <int MODE, class TE, int NP>
+cudaError_t launch_few_np(Args &a, const void *x, int64_t ld_x, const void *W, int64_t w_rows, bool early,
+                          cudaStream_t st)
+{
+    constexpr int kTile = MODE == kGated ? 64 : 128;
+    auto kern = few_kernel<MODE, TE, NP>;
+    const int sms = num_sms_current_device();
+    if (sms <= 0)
+        return cudaErrorInvalidConfiguration;
+    a.tiles_n = (a.N + kTile - 1) / kTile;
+    a.tiles_m = 1;
+    a.S = few_split(a.tiles_n, a.K, sms * (NP <= 64 ? 2 : 1));
+    if (!encode_tmap_2d_pitched(&a.tm_a, x, 2, a.K, a.M, ld_x, 64, NP) ||
+        !encode_tmap_2d_pitched(&a.tm_b, W, 2, a.K, w_rows, a.K, 64, kTile))
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmemBytes<NP>);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.tiles_n * a.S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kFewSmemBytes<NP>;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, early ? 1 : 0);
+}
+
+// The product of a.M <= kFewMost tokens (rows of a.K at pitch ld_x) with w_rows weight rows of a.K.
+template <int MODE, class TE>
+cudaError_t launch_few(Args &a, const void *x, int64_t ld_x, const void *W, int64_t w_rows, bool early,
+                       cudaStream_t st)
+{
+    return a.M <= 16   ? launch_few_np<MODE, TE, 16>(a, x, ld_x, W, w_rows, early, st)
+           : a.M <= 32 ? launch_few_np<MODE, TE, 32>(a, x, ld_x, W, w_rows, early, st)
+           : a.M <= 64 ? launch_few_np<MODE, TE, 64>(a, x, ld_x, W, w_rows, early, st)
+                       : launch_few_np<MODE, TE, 128>(a, x, ld_x, W, w_rows, early, st);
+}
+
+}  // namespace dense
+}  // namespace moe

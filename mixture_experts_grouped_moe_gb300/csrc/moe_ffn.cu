@@ -6,7 +6,7 @@
 // Six products of dense_gemm.cuh; the activation and its gradient are epilogues, and every matrix is read as it
 // lies.  h, and in the backward [dg | du], are rounded to the rows' type between the products (they are operands
 // of 16-bit MMAs): errors of half a step an element, independent ones, that a sum over I or T averages.
-#include "dense_gemm.cuh"
+#include "dense_few.cuh"
 
 namespace moe {
 namespace {
@@ -40,6 +40,16 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     Args a = base;
     a.M = T, a.N = I, a.K = H;
     a.act = act, a.h = h, a.gu = gu;
+    if (T <= kFewMost) {
+        const cudaError_t err = launch_few<kGated, TE>(a, x, ld_x, Wgu, 2 * (int64_t)I, false, st);
+        if (err != cudaSuccess)
+            return err;
+        a = base;
+        a.M = T, a.N = H, a.K = I;
+        a.d = out, a.ld_d = ld_out, a.add = add, a.ld_add = ld_add;
+        // (the kernel before it waits for whatever wrote W_down, and lets this one start only then)
+        return launch_few<kStore, TE>(a, h, I, Wd, H, true, st);
+    }
     if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, Wgu, H, 2 * (int64_t)I, H, 128))
         return cudaErrorInvalidValue;
     cudaError_t err = launch<kGated, 0, TE, 256>(a, part, st);

@@ -13,7 +13,7 @@
 // dl is scaled by a power of two to at most 2^15 (the largest finite |dloss| to [2^14, 2^15)) and the gradients
 // by its inverse: a mean over many rows makes dl too small for fp16 otherwise (its smallest step, 2^-24, is then
 // at most 2^-38 of the largest row's factor).
-#include "dense_gemm.cuh"
+#include "dense_few.cuh"
 
 namespace moe {
 namespace {
@@ -116,7 +116,8 @@ bool map16(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t p
 
 bool bad_sizes(int64_t T, int H, int V) { return H % 8 != 0 || H > 1 << 20 || V > 1 << 24 || T > 1 << 30; }
 
-int64_t tiles_of(int V) { return (V + 255) / 256; }
+// (maximum, sum) pairs that the forward may keep of a row: one for each tile, or each part of one
+int64_t pairs_of(int64_t T, int V) { return T <= kFewMost ? ((int64_t)V + 127) / 128 * 8 : ((int64_t)V + 255) / 256; }
 
 // Byte offsets of the workspace (forward: stats and target logits; backward: dl of a piece, kept rows, dx's sum).
 struct Forward {
@@ -124,7 +125,7 @@ struct Forward {
     Forward(int64_t T, int V)
     {
         stats = kHead;
-        own = stats + up1k(T * tiles_of(V) * 8);
+        own = stats + up1k(T * pairs_of(T, V) * 8);
         total = own + up1k(T * 4);
     }
 };
@@ -148,13 +149,18 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     Args a = base;
     a.M = T, a.N = V, a.K = H, a.V = V;
     a.targets = targets, a.stats = stats, a.target_logit = own;
-    if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, W, H, V, H, 128))
-        return cudaErrorInvalidValue;
-    const cudaError_t err = launch<kLse, 0, TE, 256>(a, nullptr, st);
+    cudaError_t err;
+    if (T <= kFewMost) {
+        err = launch_few<kLse, TE>(a, x, ld_x, W, V, false, st);
+    } else {
+        if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, W, H, V, H, 128))
+            return cudaErrorInvalidValue;
+        err = launch<kLse, 0, TE, 256>(a, nullptr, st);
+    }
     if (err != cudaSuccess)
         return err;
     return launch_kernel(true, finish_kernel, dim3((unsigned)((T + 7) / 8)), dim3(256), 0, st, (const float2 *)stats,
-                         (const float *)own, targets, T, a.tiles_n, V, loss, lse);
+                         (const float *)own, targets, T, a.tiles_n * a.S, V, loss, lse);
 }
 
 template <class TE>
