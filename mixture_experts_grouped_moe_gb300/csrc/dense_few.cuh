@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
     const int nkb = (a.K + 63) / 64;
     const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
     bool ok = true;
+    int targets = -1;  // logits: those of this warp's tokens, one a lane
 
     if (warp == 0) {
         if (lane == 0) {
@@ -142,6 +143,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
         pdl_trigger();
         const int q = warp & 3;
         const int r = q * 32 + lane;  // weight row
+        if (MODE == kLse && warp - 2 + 4 * lane < (int)a.M)
+            targets = a.targets[warp - 2 + 4 * lane];
         ok = mbar_wait(&sm.done, 0, a.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -182,51 +185,71 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     cluster_sync();  // every part has arrived; (S = 1: the block's own barrier)
     if (warp >= 2 && ok) {
-        const int t = threadIdx.x - 64;
+        // An item is 8 consecutive features of a token: 16-byte loads and stores (element by element, with the
+        // loads of `add` one after the other, this took 3 to 14 us).
         const int own = 128 / S;
-        const auto sum = [&](int col, int local) {
-            float v = 0.0f;
-            for (int s = 0; s < S; ++s)
-                v += sm.red[(s * NP + col) * own + local];
-            return v;
+        const auto sum8 = [&](int col, int local, float(&v)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 0.0f;
+            for (int s = 0; s < S; ++s) {
+                const float4 *p = reinterpret_cast<const float4 *>(sm.red + (s * NP + col) * own + local);
+                const float4 f = p[0], g = p[1];
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
+            }
         };
         if (MODE == kGated) {
-            const int half = own / 2, f0 = tile * 64 + rank * half;
-            for (int e = t; e < half * (int)a.M; e += 128) {
-                const int i = e % half, col = e / half, f = f0 + i;
+            const int half = own / 2, groups = half / 8, f0 = tile * 64 + rank * half;
+            for (int e = threadIdx.x - 64; e < groups * (int)a.M; e += 128) {
+                const int i = e % groups * 8, col = e / groups, f = f0 + i;
                 if (f >= a.N)
                     continue;
-                const float g = sum(col, i), u = sum(col, half + i);
-                static_cast<TE *>(a.h)[(int64_t)col * a.N + f] = row_from_f<TE>(act_of(g, a.act) * u);
+                float g[8], u[8], h[8];
+                sum8(col, i, g);
+                sum8(col, half + i, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[j] = act_of(g[j], a.act) * u[j];
+                store8(static_cast<TE *>(a.h) + (int64_t)col * a.N + f, h);
                 if (a.gu) {
                     TE *kept = static_cast<TE *>(a.gu) + (int64_t)col * 2 * a.N + f;
-                    kept[0] = row_from_f<TE>(g);
-                    kept[a.N] = row_from_f<TE>(u);
+                    store8(kept, g);
+                    store8(kept + a.N, u);
                 }
             }
         } else if (MODE == kStore) {
-            const int f0 = tile * 128 + rank * own;
-            for (int e = t; e < own * (int)a.M; e += 128) {
-                const int i = e % own, col = e / own, f = f0 + i;
+            const int groups = own / 8, f0 = tile * 128 + rank * own;
+            for (int e = threadIdx.x - 64; e < groups * (int)a.M; e += 128) {
+                const int i = e % groups * 8, col = e / groups, f = f0 + i;
                 if (f >= a.N)
                     continue;
-                float v = sum(col, i);
+                float v[8], add[8] = {};
                 if (a.add)
-                    v += row_to_f(static_cast<const TE *>(a.add)[col * a.ld_add + f]);
-                static_cast<TE *>(a.d)[col * a.ld_d + f] = row_from_f<TE>(v);
+                    load8(static_cast<const TE *>(a.add) + col * a.ld_add + f, add);
+                sum8(col, i, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += add[j];
+                store8(static_cast<TE *>(a.d) + col * a.ld_d + f, v);
             }
         } else {
             // logits: a warp a token, its maximum and sum of exponentials over the rows finished here
             const int f0 = tile * 128 + rank * own;
             for (int col = warp - 2; col < (int)a.M; col += 4) {
+                const int target = __shfl_sync(0xffffffffu, targets, col / 4);
                 float v[4], m = -INFINITY;
-                const int target = a.targets[col];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int i = lane + 32 * j;
-                    v[j] = i < own && f0 + i < a.N ? sum(col, i) : -INFINITY;
-                    if (i < own && f0 + i == target && target < a.N)
-                        a.target_logit[col] = v[j];
+                    v[j] = -INFINITY;
+                    if (i < own && f0 + i < a.N) {
+                        v[j] = 0.0f;
+                        for (int s = 0; s < S; ++s)
+                            v[j] += sm.red[(s * NP + col) * own + i];
+                        if (f0 + i == target)
+                            a.target_logit[col] = v[j];
+                    }
                     m = fmaxf(m, v[j]);
                 }
 #pragma unroll
