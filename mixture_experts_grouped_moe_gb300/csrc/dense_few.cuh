@@ -16,6 +16,7 @@ namespace moe {
 namespace dense {
 
 constexpr int kFewMost = 128;  // tokens
+constexpr int kFewThreads = 192;
 
 template <int NP>
 constexpr int kFewStageBytes = 16384 + NP * 128;
@@ -38,10 +39,10 @@ static_assert(2 * (kFewSmemBytes<16> + 1024) <= 228 * 1024 && 2 * (kFewSmemBytes
                   2 * (kFewSmemBytes<64> + 1024) <= 228 * 1024 && kFewSmemBytes<128> <= 227 * 1024,
               "two CTAs an SM up to 64 tokens");
 
-// a.tm_a: tokens in boxes of 64 x NP; a.tm_b: weights in boxes of 64 x (gated 64, else 128); a.M tokens, a.N
-// features, a.S CTAs a tile.  early: the weights may be read before what precedes the kernel has ended.
+// p[0].tm_a: tokens in boxes of 64 x NP; tm_b: weights in boxes of 64 x (gated 64, else 128); M tokens, N
+// features, S CTAs a tile.  early: the weights may be read before what precedes the kernel has ended.
 template <int MODE, class TE, int NP>
-__global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ Args a, int early)
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ Args a, int early)
 {
     using SmemT = FewSmem<NP>;
     constexpr int kS = kFewStages<NP>;
@@ -49,7 +50,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
     extern __shared__ uint8_t smem_raw[];
     SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = a.S;
+    const Product &p = a.p[0];
+    const int S = p.S;
     const int rank = blockIdx.x % S, tile = blockIdx.x / S;
     volatile int *abort_flag = &sm.abort;
 
@@ -61,8 +63,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
         mbar_init(&sm.done, 1);
         sm.abort = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&a.tm_a);
-        tma_prefetch_desc(&a.tm_b);
+        tma_prefetch_desc(&p.tm_a);
+        tma_prefetch_desc(&p.tm_b);
     }
     if (warp == 1) {
         tmem_alloc(&sm.tmem_base, NP < 32 ? 32 : NP);
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
     // every CTA of the cluster has started before any of them writes to another's shared memory
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const uint32_t tmem_base = sm.tmem_base;
-    const int nkb = (a.K + 63) / 64;
+    const int nkb = (p.K + 63) / 64;
     const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
     bool ok = true;
     int targets = -1;  // logits: those of this warp's tokens, one a lane
@@ -84,12 +86,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
             const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
             const auto weights = [&](int s, int kb) {
                 mbar_arrive_expect_tx(&sm.full[s], kFewStageBytes<NP>);
-                tma_load_2d(sm.stage[s], &a.tm_b, kb * 64, tile * kTile, &sm.full[s], once);
+                tma_load_2d(sm.stage[s], &p.tm_b, kb * 64, tile * kTile, &sm.full[s], once);
                 if (MODE == kGated)
-                    tma_load_2d(sm.stage[s] + 8192, &a.tm_b, kb * 64, a.N + tile * kTile, &sm.full[s], once);
+                    tma_load_2d(sm.stage[s] + 8192, &p.tm_b, kb * 64, p.N + tile * kTile, &sm.full[s], once);
             };
             const auto tokens = [&](int s, int kb) {
-                tma_load_2d(sm.stage[s] + 16384, &a.tm_a, kb * 64, 0, &sm.full[s], keep);
+                tma_load_2d(sm.stage[s] + 16384, &p.tm_a, kb * 64, 0, &sm.full[s], keep);
             };
             const int pre = early ? min(kS, kb1 - kb0) : 0;
             for (int i = 0; i < pre; ++i)
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
         pdl_trigger();
         const int q = warp & 3;
         const int r = q * 32 + lane;  // weight row
-        if (MODE == kLse && warp - 2 + 4 * lane < (int)a.M)
+        if (MODE == kLse && warp - 2 + 4 * lane < (int)p.M)
             targets = a.targets[warp - 2 + 4 * lane];
         ok = mbar_wait(&sm.done, 0, a.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
                 tmem_ld32(tacc + c, v);
 #pragma unroll
             for (int i = 0; i < kC; ++i)
-                if (c + i < a.M)
+                if (c + i < p.M)
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)((c + i) * own * 4)),
                                  "f"(v[i])
                                  : "memory");
@@ -193,17 +195,17 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
             for (int i = 0; i < 8; ++i)
                 v[i] = 0.0f;
             for (int s = 0; s < S; ++s) {
-                const float4 *p = reinterpret_cast<const float4 *>(sm.red + (s * NP + col) * own + local);
-                const float4 f = p[0], g = p[1];
+                const float4 *part = reinterpret_cast<const float4 *>(sm.red + (s * NP + col) * own + local);
+                const float4 f = part[0], g = part[1];
                 v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
                 v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
             }
         };
         if (MODE == kGated) {
             const int half = own / 2, groups = half / 8, f0 = tile * 64 + rank * half;
-            for (int e = threadIdx.x - 64; e < groups * (int)a.M; e += 128) {
+            for (int e = threadIdx.x - 64; e < groups * (int)p.M; e += 128) {
                 const int i = e % groups * 8, col = e / groups, f = f0 + i;
-                if (f >= a.N)
+                if (f >= p.N)
                     continue;
                 float g[8], u[8], h[8];
                 sum8(col, i, g);
@@ -211,39 +213,39 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     h[j] = act_of(g[j], a.act) * u[j];
-                store8(static_cast<TE *>(a.h) + (int64_t)col * a.N + f, h);
+                store8(static_cast<TE *>(a.h) + (int64_t)col * p.N + f, h);
                 if (a.gu) {
-                    TE *kept = static_cast<TE *>(a.gu) + (int64_t)col * 2 * a.N + f;
+                    TE *kept = static_cast<TE *>(a.gu) + (int64_t)col * 2 * p.N + f;
                     store8(kept, g);
-                    store8(kept + a.N, u);
+                    store8(kept + p.N, u);
                 }
             }
         } else if (MODE == kStore) {
             const int groups = own / 8, f0 = tile * 128 + rank * own;
-            for (int e = threadIdx.x - 64; e < groups * (int)a.M; e += 128) {
+            for (int e = threadIdx.x - 64; e < groups * (int)p.M; e += 128) {
                 const int i = e % groups * 8, col = e / groups, f = f0 + i;
-                if (f >= a.N)
+                if (f >= p.N)
                     continue;
                 float v[8], add[8] = {};
-                if (a.add)
-                    load8(static_cast<const TE *>(a.add) + col * a.ld_add + f, add);
+                if (p.add)
+                    load8(static_cast<const TE *>(p.add) + col * p.ld_add + f, add);
                 sum8(col, i, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v[j] += add[j];
-                store8(static_cast<TE *>(a.d) + col * a.ld_d + f, v);
+                store8(static_cast<TE *>(p.d) + col * p.ld_d + f, v);
             }
         } else {
             // logits: a warp a token, its maximum and sum of exponentials over the rows finished here
             const int f0 = tile * 128 + rank * own;
-            for (int col = warp - 2; col < (int)a.M; col += 4) {
+            for (int col = warp - 2; col < (int)p.M; col += 4) {
                 const int target = __shfl_sync(0xffffffffu, targets, col / 4);
                 float v[4], m = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int i = lane + 32 * j;
                     v[j] = -INFINITY;
-                    if (i < own && f0 + i < a.N) {
+                    if (i < own && f0 + i < p.N) {
                         v[j] = 0.0f;
                         for (int s = 0; s < S; ++s)
                             v[j] += sm.red[(s * NP + col) * own + i];
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const __grid_constant__ A
                     s += exp2_fast(fmaf(v[j], kLog2e, -base));
                 s = warp_sum(s);
                 if (lane == 0)
-                    a.stats[(int64_t)col * a.tiles_n * S + tile * S + rank] = make_float2(m, s);
+                    a.stats[(int64_t)col * a.pairs + tile * S + rank] = make_float2(m, s);
             }
         }
     }
@@ -284,33 +286,35 @@ inline int few_split(int64_t tiles, int K, int slots)
 }
 
 template <int MODE, class TE, int NP>
-cudaError_t launch_few_np(Args &a, const void *x, int64_t ld_x, const void *W, int64_t w_rows, bool early,
-                          cudaStream_t st)
+cudaError_t launch_few_np(Args &a, bool early, cudaStream_t st)
 {
     constexpr int kTile = MODE == kGated ? 64 : 128;
     auto kern = few_kernel<MODE, TE, NP>;
     const int sms = num_sms_current_device();
     if (sms <= 0)
         return cudaErrorInvalidConfiguration;
-    a.tiles_n = (a.N + kTile - 1) / kTile;
-    a.tiles_m = 1;
-    a.S = few_split(a.tiles_n, a.K, sms * (NP <= 64 ? 2 : 1));
-    if (!encode_tmap_2d_pitched(&a.tm_a, x, 2, a.K, a.M, ld_x, 64, NP) ||
-        !encode_tmap_2d_pitched(&a.tm_b, W, 2, a.K, w_rows, a.K, 64, kTile))
+    Product &p = a.p[0];
+    p.tiles_n = (p.N + kTile - 1) / kTile;
+    p.tiles_m = 1;
+    p.S = few_split(p.tiles_n, p.K, sms * (NP <= 64 ? 2 : 1));
+    a.pairs = p.tiles_n * p.S;
+    const int64_t w_rows = MODE == kGated ? 2 * (int64_t)p.N : p.N;
+    if (!encode_tmap_2d_pitched(&p.tm_a, p.A, 2, p.K, p.M, p.ld_a, 64, NP) ||
+        !encode_tmap_2d_pitched(&p.tm_b, p.B, 2, p.K, w_rows, p.ld_b, 64, kTile))
         return cudaErrorInvalidValue;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmemBytes<NP>);
     if (err != cudaSuccess)
         return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.tiles_n * a.S));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(p.tiles_n * p.S));
+    cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = kFewSmemBytes<NP>;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.S;
+    attr[1].val.clusterDim.x = p.S;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -318,15 +322,15 @@ cudaError_t launch_few_np(Args &a, const void *x, int64_t ld_x, const void *W, i
     return cudaLaunchKernelEx(&cfg, kern, a, early ? 1 : 0);
 }
 
-// The product of a.M <= kFewMost tokens (rows of a.K at pitch ld_x) with w_rows weight rows of a.K.
+// The product p[0] of M <= kFewMost tokens (A) with weights (B).
 template <int MODE, class TE>
-cudaError_t launch_few(Args &a, const void *x, int64_t ld_x, const void *W, int64_t w_rows, bool early,
-                       cudaStream_t st)
+cudaError_t launch_few(Args &a, bool early, cudaStream_t st)
 {
-    return a.M <= 16   ? launch_few_np<MODE, TE, 16>(a, x, ld_x, W, w_rows, early, st)
-           : a.M <= 32 ? launch_few_np<MODE, TE, 32>(a, x, ld_x, W, w_rows, early, st)
-           : a.M <= 64 ? launch_few_np<MODE, TE, 64>(a, x, ld_x, W, w_rows, early, st)
-                       : launch_few_np<MODE, TE, 128>(a, x, ld_x, W, w_rows, early, st);
+    const int64_t T = a.p[0].M;
+    return T <= 16   ? launch_few_np<MODE, TE, 16>(a, early, st)
+           : T <= 32 ? launch_few_np<MODE, TE, 32>(a, early, st)
+           : T <= 64 ? launch_few_np<MODE, TE, 64>(a, early, st)
+                     : launch_few_np<MODE, TE, 128>(a, early, st);
 }
 
 }  // namespace dense

@@ -9,14 +9,16 @@
 //   MAJ 0: A and B [rows][K]  (x W^T);   MAJ 1: B is [K][N]  (d W);   MAJ 2: both are  (d^T x).
 // Rows and K may end anywhere: TMA fills zeros past the edges of both operands.
 //
-// Roles (192 threads a CTA, one CTA an SM): warp 0 TMA producer, warp 1 issues the pair's MMAs (in the
-// leader), warps 2..5 the epilogue of the CTA's 128 rows, which overlaps the next tile's MMAs through a
-// second accumulator.  Tiles are dealt round-robin (all cost the same); groups of eight row tiles walk the
-// columns together, so that 76 pairs in flight share about 8 x 10 tiles' rows through L2.
+// Roles (320 threads a CTA, one CTA an SM): warp 0 TMA producer, warp 1 issues the pair's MMAs (in the
+// leader), warps 2..9 the epilogue of the CTA's 128 rows (two warps a row, each half of the columns), which
+// overlaps the next tile's MMAs through a second accumulator.  Tiles are dealt round-robin (those of a product
+// cost the same); groups of eight row tiles walk the columns together, so that 76 pairs in flight share about
+// 8 x 10 tiles' rows through L2.  Products that do not depend on one another (the gradients of x and of the
+// weights) go into one launch, longest K first: one start, one tail and one rounding up to whole waves.
 //
-// Few tiles (a short batch, a narrow matrix) leave pairs idle: K is then split over S pairs a tile, which
-// store fp32 partial sums, and a second kernel adds them in ascending order and applies the epilogue.
-// Every sum has a fixed order: results are bitwise reproducible.
+// Few tiles (a short batch, a narrow matrix) leave pairs idle: tiles are then half as wide, or K is split over S
+// pairs a tile, which store fp32 partial sums, and a second kernel adds them in ascending order and applies the
+// epilogue.  Every sum has a fixed order: results are bitwise reproducible.
 #pragma once
 
 #include <atomic>
@@ -40,15 +42,19 @@ enum Mode {
     kDlogits,   // v = logits: (softmax - one at the target) times the row's factor
 };
 
-struct Args {
+constexpr int kProducts = 3;  // of one launch
+
+struct Product {
     CUtensorMap tm_a, tm_b;
+    const void *A, *B;    // from which the launch makes the maps, whose boxes go by the tile
+    int64_t ld_a, ld_b;
     int64_t M;
-    int N;                // columns (gated: of h)
+    int N;                // columns (gated: of h; B then has 2N rows)
     int K;
+    int maj;              // 0, 1 or 2, as above
     int tiles_m, tiles_n;
     int S;                // pairs that share a tile's K
-    float *part;          // S > 1: partial sums
-    int *status;
+    int first;            // its first item; an item is a tile, or a part of K of one
     // kStore: d [M] rows of N at pitch ld_d, of the rows' type or fp32; add of d's type
     void *d;
     int64_t ld_d;
@@ -57,6 +63,13 @@ struct Args {
     const float *acc_in;  // [M][N]
     const float *scale;
     int d_f32;
+};
+
+struct Args {
+    Product p[kProducts];
+    int n, items;
+    float *part;          // partial sums, one accumulator an item
+    int *status;
     // gated
     int act;
     void *h;              // [M][N]
@@ -64,14 +77,16 @@ struct Args {
     void *dgu;            // [M][2N]
     // cross entropy
     const int32_t *targets;
-    float2 *stats;        // [M][tiles_n]
+    float2 *stats;        // [M][pairs]
+    int pairs;            // (maximum, sum) pairs of a row
     float *target_logit;  // [M]
     const float *lse, *dloss;
     const float *dscale;  // {factor of dloss, its inverse}
     int v0, V;            // the piece's first column, the vocabulary
 };
 
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kGroup = 8;
 constexpr int kABytes = 128 * 128;  // 128 rows x 64 elements of K
 template <int NT>
@@ -152,15 +167,15 @@ __device__ __forceinline__ void load8(const TE *src, float *v)
     unpack_word(w.w, v[6], v[7], TE{});
 }
 
-// 32 columns from `col` of row `row` (N % 8 == 0; row < M).
-template <class TE>
-__device__ __forceinline__ void epi_store(const Args &a, int64_t row, int col, float (&v)[32])
+// W columns from `col` of row `row` (N % 8 == 0; row < M).
+template <class TE, int W>
+__device__ __forceinline__ void epi_store(const Product &a, int64_t row, int col, float (&v)[W])
 {
     const float sc = a.scale ? *a.scale : 1.0f;
     if (a.acc_in) {
         const float *src = a.acc_in + row * a.N + col;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
+        for (int i = 0; i < W; i += 4)
             if (col + i < a.N) {
                 const float4 f = *reinterpret_cast<const float4 *>(src + i);
                 v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
@@ -168,14 +183,14 @@ __device__ __forceinline__ void epi_store(const Args &a, int64_t row, int col, f
     }
     if (a.scale) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < W; ++i)
             v[i] *= sc;
     }
     if (a.d_f32) {
         float *dst = static_cast<float *>(a.d) + row * a.ld_d + col;
         const float *add = static_cast<const float *>(a.add) + row * a.ld_add + col;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
+        for (int i = 0; i < W; i += 4)
             if (col + i < a.N) {
                 float4 f = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 if (a.add) {
@@ -189,7 +204,7 @@ __device__ __forceinline__ void epi_store(const Args &a, int64_t row, int col, f
     TE *dst = static_cast<TE *>(a.d) + row * a.ld_d + col;
     const TE *add = static_cast<const TE *>(a.add) + row * a.ld_add + col;
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
+    for (int i = 0; i < W; i += 8)
         if (col + i < a.N) {
             if (a.add) {
                 float f[8];
@@ -203,40 +218,42 @@ __device__ __forceinline__ void epi_store(const Args &a, int64_t row, int col, f
 }
 
 // h = act(g) u, from the unrounded products; g and u are rounded only where they are kept.
-template <class TE>
-__device__ __forceinline__ void epi_gated(const Args &a, int64_t row, int col, float (&g)[32], float (&u)[32])
+template <class TE, int W>
+__device__ __forceinline__ void epi_gated(const Args &a, int64_t row, int col, float (&g)[W], float (&u)[W])
 {
-    TE *hd = static_cast<TE *>(a.h) + row * a.N + col;
+    const int N = a.p[0].N;
+    TE *hd = static_cast<TE *>(a.h) + row * N + col;
     if (a.gu) {
-        TE *kept = static_cast<TE *>(a.gu) + row * 2 * a.N + col;
+        TE *kept = static_cast<TE *>(a.gu) + row * 2 * N + col;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            if (col + i < a.N) {
+        for (int i = 0; i < W; i += 8)
+            if (col + i < N) {
                 store8(kept + i, g + i);
-                store8(kept + a.N + i, u + i);
+                store8(kept + N + i, u + i);
             }
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < W; ++i)
         g[i] = act_of(g[i], a.act) * u[i];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (col + i < a.N)
+    for (int i = 0; i < W; i += 8)
+        if (col + i < N)
             store8(hd + i, g + i);
 }
 
 // d gate = dh u act'(g), d up = dh act(g): rounded to 16 bits as the operands of the products that follow.
-template <class TE>
-__device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int col, const float (&dh)[32])
+template <class TE, int W>
+__device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int col, const float (&dh)[W])
 {
-    const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * a.N + col;
-    TE *out = static_cast<TE *>(a.dgu) + row * 2 * a.N + col;
+    const int N = a.p[0].N;
+    const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * N + col;
+    TE *out = static_cast<TE *>(a.dgu) + row * 2 * N + col;
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (col + i < a.N) {
+    for (int i = 0; i < W; i += 8)
+        if (col + i < N) {
             float g[8], u[8];
             load8(kept + i, g);
-            load8(kept + a.N + i, u);
+            load8(kept + N + i, u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float act, slope;
@@ -245,7 +262,7 @@ __device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int co
                 u[j] = dh[i + j] * act;
             }
             store8(out + i, g);
-            store8(out + a.N + i, u);
+            store8(out + N + i, u);
         }
 }
 
@@ -259,13 +276,13 @@ __device__ __forceinline__ float exp2_fast(float v)
 }
 
 // One more 32 columns of a row's running maximum m and sum s of exp(v - m).  Columns past N count as -inf.
-__device__ __forceinline__ void epi_lse(const Args &a, int col, int target, float (&v)[32], float &m, float &s,
-                                        float &own, bool &has)
+__device__ __forceinline__ void epi_lse(int N, int col, int target, float (&v)[32], float &m, float &s, float &own,
+                                        bool &has)
 {
-    if (col + 32 > a.N) {
+    if (col + 32 > N) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (col + i >= a.N)
+            if (col + i >= N)
                 v[i] = -INFINITY;
     }
     const int at = target - col;
@@ -290,7 +307,7 @@ __device__ __forceinline__ void epi_lse(const Args &a, int col, int target, floa
     s = fmaf(s, exp2_fast(fmaf(was, kLog2e, -base)), (part[0] + part[1]) + (part[2] + part[3]));
 }
 
-// factor (softmax - one at the target), 32 columns; the pitch of the rows (a.ld_d) is a multiple of 8.
+// factor (softmax - one at the target), 32 columns; the pitch of the rows (ld_d) is a multiple of 8.
 template <class TE>
 __device__ __forceinline__ void epi_dlogits(const Args &a, int64_t row, int col, int target, float lse, float factor,
                                             float (&v)[32])
@@ -304,58 +321,63 @@ __device__ __forceinline__ void epi_dlogits(const Args &a, int64_t row, int col,
             p -= 1.0f;
         v[i] = factor == 0.0f ? 0.0f : factor * p;  // (a row left out adds nothing, whatever its logits)
     }
-    TE *dst = static_cast<TE *>(a.d) + row * a.ld_d + col;
+    TE *dst = static_cast<TE *>(a.p[0].d) + row * a.p[0].ld_d + col;
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
-        if (col + i < a.N)
+        if (col + i < a.p[0].N)
             store8(dst + i, v + i);
 }
 
 // -------------------------------------------------------------- the tiles
 
 struct Tile {
+    int prod;      // which product
     int m0, nt;    // first row, column tile
     int kb0, kb1;  // blocks of 64 of K
-    int s;
 };
 
+template <int MODE>
 __device__ __forceinline__ Tile tile_of(const Args &a, int t)
 {
-    Tile p;
-    const int per = a.tiles_m * a.tiles_n;
-    const int nkb = (a.K + 63) / 64;
-    p.s = t / per;
-    t -= p.s * per;
-    p.kb0 = (int)((int64_t)nkb * p.s / a.S);
-    p.kb1 = (int)((int64_t)nkb * (p.s + 1) / a.S);
-    const int g = t / (kGroup * a.tiles_n);
-    const int size = min(kGroup, a.tiles_m - g * kGroup);
-    t -= g * kGroup * a.tiles_n;
-    p.nt = t / size;
-    p.m0 = (g * kGroup + t % size) * 256;
-    return p;
+    Tile r;
+    r.prod = 0;
+    if (MODE == kStore)
+        while (r.prod + 1 < a.n && t >= a.p[r.prod + 1].first)
+            ++r.prod;
+    const Product &p = a.p[r.prod];
+    t -= p.first;
+    const int per = p.tiles_m * p.tiles_n;
+    const int nkb = (p.K + 63) / 64;
+    const int s = t / per;
+    t -= s * per;
+    r.kb0 = (int)((int64_t)nkb * s / p.S);
+    r.kb1 = (int)((int64_t)nkb * (s + 1) / p.S);
+    const int g = t / (kGroup * p.tiles_n);
+    const int size = min(kGroup, p.tiles_m - g * kGroup);
+    t -= g * kGroup * p.tiles_n;
+    r.nt = t / size;
+    r.m0 = (g * kGroup + t % size) * 256;
+    return r;
 }
 
 // Columns of D that a tile covers.
 template <int MODE, int NT>
 constexpr int kCols = MODE == kGated ? NT / 2 : NT;
 
-// Partial sums of CTA `rank` of a tile: [NT / 4][128 rows] of four columns, so that neighbouring threads (rows)
+// Partial sums of CTA `rank` of an item: [NT / 4][128 rows] of four columns, so that neighbouring threads (rows)
 // touch neighbouring 16 bytes.
 template <int NT>
-__device__ __forceinline__ float4 *part_of(const Args &a, const Tile &p, int rank, int s)
+__device__ __forceinline__ float4 *part_of(const Args &a, int item, int rank)
 {
-    const int64_t tile = (int64_t)(p.m0 / 256) * a.tiles_n + p.nt;
-    return reinterpret_cast<float4 *>(a.part) +
-           (((int64_t)s * a.tiles_m * a.tiles_n + tile) * 2 + rank) * (NT / 4 * 128);
+    return reinterpret_cast<float4 *>(a.part) + ((int64_t)item * 2 + rank) * (NT / 4 * 128);
 }
 
-template <int MODE, int MAJ, class TE, int NT>
+template <int MODE, class TE, int NT>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Args a)
 {
     using SmemT = Smem<NT>;
     constexpr int kS = kStages<NT>;
-    constexpr int kHalf = NT / 2;  // B rows (accumulator columns) of one CTA
+    constexpr int kHalf = NT / 2;  // B rows of one CTA
     extern __shared__ uint8_t smem_raw[];
     SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -370,13 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.tfull[i], 1);
-            mbar_init(&sm.tempty[i], 2 * 4);
+            mbar_init(&sm.tempty[i], 2 * kEpiWarps);
         }
         mbar_init(&sm.drain, 1);
         sm.abort = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&a.tm_a);
-        tma_prefetch_desc(&a.tm_b);
+        for (int i = 0; i < a.n; ++i) {
+            tma_prefetch_desc(&a.p[i].tm_a);
+            tma_prefetch_desc(&a.p[i].tm_b);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(&sm.tmem_base, 512);
@@ -390,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
 
-    const int items = a.tiles_m * a.tiles_n * a.S;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -399,12 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int s = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < items; t += step) {
-                const Tile p = tile_of(a, t);
-                const int arow = p.m0 + rank * 128;
+            for (int t = first; ok && t < a.items; t += step) {
+                const Tile tile = tile_of<MODE>(a, t);
+                const Product &p = a.p[tile.prod];
+                const int maj = MODE == kStore ? p.maj : MODE == kGatedBwd ? 1 : 0;
+                const int arow = tile.m0 + rank * 128;
                 // gated: CTA 0 holds gate rows, CTA 1 the matching up rows
-                const int brow = MODE == kGated ? rank * a.N + p.nt * kHalf : p.nt * NT + rank * kHalf;
-                for (int kb = p.kb0; kb < p.kb1; ++kb) {
+                const int brow = MODE == kGated ? rank * p.N + tile.nt * kHalf : tile.nt * NT + rank * kHalf;
+                for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
                     if (!mbar_wait(&sm.empty[s], ph ^ 1, a.status, abort_flag)) {
                         ok = false;
                         break;
@@ -413,18 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     const uint32_t bar = cluster_map(&sm.full[s], 0);
                     if (leader)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * kStageBytes<NT>);
-                    if (MAJ == 2) {
-                        tma_load_2d_pair(sa, &a.tm_a, arow, kb * 64, bar, keep);
-                        tma_load_2d_pair(sa + kABytes / 2, &a.tm_a, arow + 64, kb * 64, bar, keep);
+                    if (maj == 2) {
+                        tma_load_2d_pair(sa, &p.tm_a, arow, kb * 64, bar, keep);
+                        tma_load_2d_pair(sa + kABytes / 2, &p.tm_a, arow + 64, kb * 64, bar, keep);
                     } else {
-                        tma_load_2d_pair(sa, &a.tm_a, kb * 64, arow, bar, keep);
+                        tma_load_2d_pair(sa, &p.tm_a, kb * 64, arow, bar, keep);
                     }
-                    if (MAJ >= 1) {
+                    if (maj >= 1) {
 #pragma unroll
                         for (int c = 0; c < kHalf; c += 64)
-                            tma_load_2d_pair(sb + c * 128, &a.tm_b, brow + c, kb * 64, bar, keep);
+                            tma_load_2d_pair(sb + c * 128, &p.tm_b, brow + c, kb * 64, bar, keep);
                     } else {
-                        tma_load_2d_pair(sb, &a.tm_b, kb * 64, brow, bar, keep);
+                        tma_load_2d_pair(sb, &p.tm_b, kb * 64, brow, bar, keep);
                     }
                     any = true;
                     if (++s == kS) {
@@ -443,34 +468,35 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     } else if (warp == 1) {
         if (leader && lane == 0) {
             const uint32_t type = std::is_same<TE, __nv_bfloat16>::value ? 1u : 0u;  // (fp16: 0) both operands alike
-            const uint32_t idesc = make_idesc(type, type, 256, NT) | (MAJ >= 1 ? 1u << 16 : 0u) |
-                                   (MAJ == 2 ? 1u << 15 : 0u);
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < items; t += step) {
-                const Tile p = tile_of(a, t);
+            for (int t = first; ok && t < a.items; t += step) {
+                const Tile tile = tile_of<MODE>(a, t);
+                const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
+                const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
+                                       (maj == 2 ? 1u << 15 : 0u);
                 if (!mbar_wait(&sm.tempty[acc], aph ^ 1, a.status, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * 256;
-                for (int kb = p.kb0; kb < p.kb1; ++kb) {
+                for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
                     if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint8_t *sa = sm.stage[s], *sb = sm.stage[s] + kABytes;
+                    // 16 of K: 32 bytes further along a K-major row, 16 rows (2 KB) further in an MN-major box
+                    uint64_t da = maj == 2 ? smem_desc_sw128_mn(sa, kABytes / 2) : smem_desc_sw128(sa);
+                    uint64_t db = maj >= 1 ? smem_desc_sw128_mn(sb, 8192) : smem_desc_sw128(sb);
+                    const uint64_t ia = maj == 2 ? 2048 >> 4 : 32 >> 4, ib = maj >= 1 ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        // 16 of K: 32 bytes further along a K-major row, 16 rows further in an MN-major box
-                        const uint64_t da = MAJ == 2 ? smem_desc_sw128_mn(sa + kk * 2048, kABytes / 2)
-                                                     : smem_desc_sw128(sa + kk * 32);
-                        const uint64_t db = MAJ >= 1 ? smem_desc_sw128_mn(sb + kk * 2048, 8192)
-                                                     : smem_desc_sw128(sb + kk * 32);
-                        mma_pair<0>(d, da, db, idesc, (kb > p.kb0 || kk > 0) ? 1u : 0u);
+                        mma_pair<0>(d, da, db, idesc, (kb > tile.kb0 || kk > 0) ? 1u : 0u);
+                        da += ia, db += ib;  // (the start address is the descriptor's lowest field)
                     }
                     any = true;
                     mma_commit_pair(&sm.empty[s], 0x3);
@@ -495,22 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
         }
     } else {
-        const int q = warp & 3;  // TMEM lane quadrant of this warp
+        const int q = warp & 3;          // TMEM lane quadrant of this warp
+        const int half = (warp - 2) / 4; // its half of the columns
         const int r = q * 32 + lane;
         int acc = 0;
         uint32_t aph = 0;
-        for (int t = first; t < items; t += step) {
-            const Tile p = tile_of(a, t);
-            const int64_t row = p.m0 + rank * 128 + r;
-            const bool live = row < a.M;
-            const int c0 = p.nt * kCols<MODE, NT>;
-            if (MODE == kGatedBwd && a.S == 1 && live) {
-                // the kept gate | up of this thread's part of the tile: into L2 while the MMAs run
-                const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * a.N + c0;
-                for (int c = 0; c < NT && c0 + c < a.N; c += 64) {
+        for (int t = first; t < a.items; t += step) {
+            const Tile tile = tile_of<MODE>(a, t);
+            const Product &p = a.p[tile.prod];
+            const int64_t row = tile.m0 + rank * 128 + r;
+            const bool live = row < p.M;
+            constexpr int kMine = kCols<MODE, NT> / 2;              // columns of D of this warp
+            const int c0 = tile.nt * kCols<MODE, NT> + half * kMine;  // the first of them
+            // what the epilogue will read of memory: into L2 while the MMAs run
+            if (MODE == kGatedBwd && p.S == 1 && live) {
+                const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * p.N + c0;
+                for (int c = 0; c < kMine && c0 + c < p.N; c += 64) {
                     prefetch_l2(kept + c);
-                    prefetch_l2(kept + a.N + c);
+                    prefetch_l2(kept + p.N + c);
                 }
+            }
+            if (MODE == kStore && p.S == 1 && live && p.add) {
+                const int es = p.d_f32 ? 4 : 2;
+                const char *add = static_cast<const char *>(p.add) + (row * p.ld_add + c0) * es;
+                for (int c = 0; c < kMine && c0 + c < p.N; c += 128 / es)
+                    prefetch_l2(add + c * es);
             }
             int target = -1;
             float lse = 0.0f, factor = 0.0f;
@@ -529,10 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 break;
             tc_fence_after();
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
-            if (a.S > 1) {
-                float4 *dst = part_of<NT>(a, p, rank, p.s) + r;
+            if (p.S > 1) {
+                float4 *dst = part_of<NT>(a, t, rank) + r;
 #pragma unroll 1
-                for (int c = 0; c < NT; c += 32) {
+                for (int c = half * kHalf; c < (half + 1) * kHalf; c += 32) {
                     float v[32];
                     tmem_ld32(tacc + c, v);
                     if (!live)
@@ -543,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             } else if (MODE == kGated) {
 #pragma unroll 1
-                for (int c = 0; c < kHalf && c0 + c < a.N; c += 32) {
+                for (int c = 0; c < kMine && c0 + c < p.N; c += 32) {
                     float g[32], u[32];
-                    tmem_ld32(tacc + c, g);
-                    tmem_ld32(tacc + kHalf + c, u);
+                    tmem_ld32(tacc + half * kMine + c, g);
+                    tmem_ld32(tacc + kHalf + half * kMine + c, u);
                     if (live)
                         epi_gated<TE>(a, row, c0 + c, g, u);
                 }
@@ -554,22 +589,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 float m = -INFINITY, s = 0.0f, own = 0.0f;
                 bool has = false;
 #pragma unroll 1
-                for (int c = 0; c < NT && c0 + c < a.N; c += 32) {
+                for (int c = 0; c < kMine && c0 + c < p.N; c += 32) {
                     float v[32];
-                    tmem_ld32(tacc + c, v);
+                    tmem_ld32(tacc + half * kMine + c, v);
                     if (!live)
                         continue;
                     if (MODE == kStore)
-                        epi_store<TE>(a, row, c0 + c, v);
+                        epi_store<TE>(p, row, c0 + c, v);
                     else if (MODE == kGatedBwd)
                         epi_gated_bwd<TE>(a, row, c0 + c, v);
                     else if (MODE == kLse)
-                        epi_lse(a, c0 + c, target, v, m, s, own, has);
+                        epi_lse(p.N, c0 + c, target, v, m, s, own, has);
                     else
                         epi_dlogits<TE>(a, row, c0 + c, target, lse, factor, v);
                 }
                 if (MODE == kLse && live) {
-                    a.stats[row * a.tiles_n + p.nt] = make_float2(m, s);
+                    a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, s);
                     if (has)
                         a.target_logit[row] = own;
                 }
@@ -595,39 +630,50 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 }
 
 // The partial sums of a tile added up in ascending order, then the epilogue: a block of 128 threads (rows) for
-// 32 columns of one CTA's part of a tile.
+// 8 columns of one CTA's part of a tile (32 columns a thread, with the parts in line: 8-17 us instead of 4).
+constexpr int kJoinCols = 8;
+
+struct JoinBlocks {
+    int first[kProducts + 1];  // first block of each product (none for one that is not split)
+};
+
 template <int MODE, class TE, int NT>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a, JoinBlocks jb)
 {
-    constexpr int kChunks = kCols<MODE, NT> / 32;
+    constexpr int kChunks = kCols<MODE, NT> / kJoinCols;
     pdl_wait();
     pdl_trigger();
-    const int c = blockIdx.x % kChunks * 32, rank = blockIdx.x / kChunks & 1, t = blockIdx.x / kChunks / 2;
-    Tile p;
-    p.m0 = t / a.tiles_n * 256;
-    p.nt = t % a.tiles_n;
-    const int64_t row = p.m0 + rank * 128 + threadIdx.x;
-    const int col = p.nt * kCols<MODE, NT> + c;
-    if (row >= a.M || col >= a.N)
+    int prod = 0;
+    while ((int)blockIdx.x >= jb.first[prod + 1])
+        ++prod;
+    const Product &p = a.p[prod];
+    const int b = blockIdx.x - jb.first[prod];
+    const int c = b % kChunks * kJoinCols, rank = b / kChunks & 1, t = b / kChunks / 2;
+    const Tile tile = tile_of<MODE>(a, p.first + t);
+    const int64_t row = tile.m0 + rank * 128 + threadIdx.x;
+    const int col = tile.nt * kCols<MODE, NT> + c;
+    if (row >= p.M || col >= p.N)
         return;
-    float v[32] = {}, u[32] = {};
-    for (int s = 0; s < a.S; ++s) {
-        const float4 *src = part_of<NT>(a, p, rank, s) + threadIdx.x;
+    const int tiles = p.tiles_m * p.tiles_n;
+    float v[kJoinCols] = {}, u[kJoinCols] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.S; ++s) {
+        const float4 *src = part_of<NT>(a, p.first + s * tiles + t, rank) + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 f = src[(c + i) / 4 * 128];
+        for (int i = 0; i < kJoinCols; i += 4) {
+            const float4 f = __ldcs(src + (c + i) / 4 * 128);
             v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
         }
         if (MODE == kGated) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 f = src[(NT / 2 + c + i) / 4 * 128];
+            for (int i = 0; i < kJoinCols; i += 4) {
+                const float4 f = __ldcs(src + (NT / 2 + c + i) / 4 * 128);
                 u[i] += f.x, u[i + 1] += f.y, u[i + 2] += f.z, u[i + 3] += f.w;
             }
         }
     }
     if (MODE == kStore)
-        epi_store<TE>(a, row, col, v);
+        epi_store<TE>(p, row, col, v);
     else if (MODE == kGated)
         epi_gated<TE>(a, row, col, v, u);
     else
@@ -636,8 +682,30 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 
 // ------------------------------------------------------------------- host
 
+// One more product of the launch: D [M][N] = A B^T over K, the operands' rows ld_a and ld_b elements apart.
+inline Product &product(Args &a, int64_t M, int N, int K, int maj, const void *A, int64_t ld_a, const void *B,
+                        int64_t ld_b)
+{
+    Product &p = a.p[a.n++];
+    p.M = M, p.N = N, p.K = K, p.maj = maj;
+    p.A = A, p.ld_a = ld_a, p.B = B, p.ld_b = ld_b;
+    return p;
+}
+
+// Tensor maps of a product's operands in boxes of 64 elements x 128 rows (B: half a tile's), MN-major ones 64 x 64.
+template <int MODE, int NT>
+bool make_maps(Product &p)
+{
+    const auto map = [](CUtensorMap *m, const void *at, int64_t inner, int64_t rows, int64_t pitch, int box_rows) {
+        return encode_tmap_2d_pitched(m, at, 2, inner, rows, pitch, 64, box_rows);
+    };
+    const int64_t b_rows = MODE == kGated ? 2 * (int64_t)p.N : p.N;
+    return (p.maj == 2 ? map(&p.tm_a, p.A, p.M, p.K, p.ld_a, 64) : map(&p.tm_a, p.A, p.K, p.M, p.ld_a, 128)) &&
+           (p.maj >= 1 ? map(&p.tm_b, p.B, p.N, p.K, p.ld_b, 64) : map(&p.tm_b, p.B, p.K, b_rows, p.ld_b, NT / 2));
+}
+
 // Clusters of two that can be resident at once, kept per device.
-template <int MODE, int MAJ, class TE, int NT>
+template <int MODE, class TE, int NT>
 int max_pairs()
 {
     static std::atomic<int> cache[64];  // zero until first computed
@@ -646,7 +714,7 @@ int max_pairs()
         return 0;
     int n = cache[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        auto kern = gemm_kernel<MODE, MAJ, TE, NT>;
+        auto kern = gemm_kernel<MODE, TE, NT>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>) !=
             cudaSuccess)
             return 0;
@@ -668,38 +736,36 @@ int max_pairs()
     return n;
 }
 
-// Workspace of the partial sums: as many tiles as there are pairs, at most.
-constexpr size_t kPartBytes = (size_t)80 * 256 * 256 * 4;
+// Workspace of the partial sums: there are at most as many parts as pairs.
+constexpr int kMostPairs = 80;
+constexpr size_t kPartBytes = (size_t)kMostPairs * 256 * 256 * 4;
 
-// Pairs that share a tile's K: as many as would be idle otherwise, with at least four blocks of 64 each.
-inline int k_split(int64_t tiles, int K, int pairs)
+template <int MODE, class TE, int NT>
+cudaError_t launch_nt(Args &a, int S, int pairs, cudaStream_t st)
 {
-    int S = (int)(pairs / tiles);
-    const int most = (K + 63) / 64 / 4;
-    if (S > most)
-        S = most;
-    if (S > 16)
-        S = 16;
-    return S < 1 ? 1 : S;
-}
-
-// D = A B^T by the rule above.  a: everything but the tiles; part: kPartBytes or null (no split).
-template <int MODE, int MAJ, class TE, int NT>
-cudaError_t launch(Args &a, float *part, cudaStream_t st)
-{
-    auto kern = gemm_kernel<MODE, MAJ, TE, NT>;
-    int pairs = max_pairs<MODE, MAJ, TE, NT>();
-    if (pairs <= 0)
-        return cudaErrorInvalidConfiguration;
-    if (pairs > 80)
-        pairs = 80;
-    const int64_t tm = (a.M + 255) / 256, tn = (a.N + kCols<MODE, NT> - 1) / kCols<MODE, NT>;
-    if (tm * tn > 1 << 30)
-        return cudaErrorInvalidValue;
-    a.tiles_m = (int)tm, a.tiles_n = (int)tn;
-    a.S = part ? k_split(tm * tn, a.K, pairs) : 1;
-    a.part = part;
-    const int64_t items = tm * tn * a.S;
+    auto kern = gemm_kernel<MODE, TE, NT>;
+    JoinBlocks jb = {};
+    int64_t items = 0;
+    bool split = false;
+    for (int i = 0; i < a.n; ++i) {
+        Product &p = a.p[i];
+        const int64_t tm = (p.M + 255) / 256, tn = (p.N + kCols<MODE, NT> - 1) / kCols<MODE, NT>;
+        const int most = (p.K + 63) / 64;
+        if (!make_maps<MODE, NT>(p))
+            return cudaErrorInvalidValue;
+        p.tiles_m = (int)tm, p.tiles_n = (int)tn;
+        p.S = S < most ? S : most;
+        p.first = (int)items;
+        items += tm * tn * p.S;
+        if (items > 1 << 30)
+            return cudaErrorInvalidValue;
+        split = split || p.S > 1;
+        jb.first[i + 1] = jb.first[i] + (p.S > 1 ? (int)(tm * tn * 2 * (kCols<MODE, NT> / kJoinCols)) : 0);
+    }
+    for (int i = a.n; i < kProducts; ++i)
+        jb.first[i + 1] = jb.first[i];
+    a.items = (int)items;
+    a.pairs = a.p[0].tiles_n * 2;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>);
     if (err != cudaSuccess)
         return err;
@@ -718,12 +784,59 @@ cudaError_t launch(Args &a, float *part, cudaStream_t st)
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     err = cudaLaunchKernelEx(&cfg, kern, a);
-    if (err != cudaSuccess || a.S == 1)
+    if (err != cudaSuccess || !split)
         return err;
     if constexpr (MODE == kStore || MODE == kGated || MODE == kGatedBwd)
-        return launch_kernel(true, join_kernel<MODE, TE, NT>, dim3((unsigned)(tm * tn * 2 * (kCols<MODE, NT> / 32))),
-                             dim3(128), 0, st, a);
+        return launch_kernel(true, join_kernel<MODE, TE, NT>, dim3((unsigned)jb.first[kProducts]), dim3(128), 0, st, a,
+                             jb);
     return cudaErrorInvalidValue;
+}
+
+// The launch's time by its parts: waves of tiles, each the blocks of K in line (KB) and an epilogue that nothing
+// hides in the last wave; a split's second kernel.  In 10 ns.
+inline int64_t cost_of(int64_t tiles, int64_t KB, int S, bool wide, int pairs)
+{
+    const int64_t waves = (tiles * S + pairs - 1) / pairs;
+    return waves * ((KB + S - 1) / S) * (wide ? 28 : 19) + (wide ? 250 : 150) + (S > 1 ? 400 : 0);
+}
+
+// The products of `a` (p[0] .. p[n - 1] but for their tiles), longest K first.  part: kPartBytes, or null (no
+// split).
+template <int MODE, class TE>
+cudaError_t launch(Args &a, float *part, cudaStream_t st)
+{
+    int pairs = max_pairs<MODE, TE, 256>();  // (one CTA an SM at either width)
+    if (pairs <= 0)
+        return cudaErrorInvalidConfiguration;
+    if (pairs > kMostPairs)
+        pairs = kMostPairs;
+    a.part = part;
+    for (int i = 1; i < a.n; ++i)
+        for (int j = i; j > 0 && a.p[j].K > a.p[j - 1].K; --j) {
+            const Product t = a.p[j];
+            a.p[j] = a.p[j - 1], a.p[j - 1] = t;
+        }
+    int64_t best = INT64_MAX;
+    int S = 1;
+    bool wide = true;
+    for (int w = MODE == kLse ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
+        const int cols = (w ? 256 : 128) / (MODE == kGated ? 2 : 1);
+        int64_t tiles = 0, blocks = 0;
+        for (int i = 0; i < a.n; ++i) {
+            const int64_t n = (a.p[i].M + 255) / 256 * ((a.p[i].N + cols - 1) / cols);
+            tiles += n, blocks += n * ((a.p[i].K + 63) / 64);
+        }
+        const int64_t KB = (blocks + tiles - 1) / tiles;
+        for (int s = 1; s <= 16 && (s == 1 || (part && tiles * s <= pairs && KB / s >= 4)); ++s) {
+            const int64_t c = cost_of(tiles, KB, s, w, pairs);
+            if (c < best)
+                best = c, S = s, wide = w;
+        }
+    }
+    if constexpr (MODE != kLse)
+        if (!wide)
+            return launch_nt<MODE, TE, 128>(a, S, pairs, st);
+    return launch_nt<MODE, TE, 256>(a, S, pairs, st);
 }
 
 }  // namespace dense

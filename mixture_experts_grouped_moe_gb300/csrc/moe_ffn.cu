@@ -3,8 +3,8 @@
 // and its gradients
 //   dh = dout Wd,  dg = dh u act'(g),  du = dh act(g),
 //   dx = [dg | du] Wgu,  dWgu = [dg | du]^T x,  dWd = dout^T h.
-// Six products of dense_gemm.cuh; the activation and its gradient are epilogues, and every matrix is read as it
-// lies.  h, and in the backward [dg | du], are rounded to the rows' type between the products (they are operands
+// Products of dense_gemm.cuh in four launches (the three gradients in one); the activation and its gradient are
+// epilogues, and every matrix is read as it lies.  h, and in the backward [dg | du], are rounded to the rows' type between the products (they are operands
 // of 16-bit MMAs): errors of half a step an element, independent ones, that a sum over I or T averages.
 #include "dense_few.cuh"
 
@@ -19,12 +19,6 @@ int64_t up1k(int64_t v) { return (v + 1023) / 1024 * 1024; }
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-// A matrix of 16-bit elements in boxes of 64 x box_rows.
-bool map16(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t pitch, int box_rows)
-{
-    return encode_tmap_2d_pitched(m, p, 2, inner, rows, pitch, 64, box_rows);
-}
-
 bool bad_sizes(int64_t T, int H, int I)
 {
     return H % 8 != 0 || I % 8 != 0 || H > 1 << 20 || I > 1 << 20 || T > 1 << 30;
@@ -37,30 +31,17 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
                     int64_t ld_add, int64_t T, int H, int I, int act, void *gu, void *h, void *out, int64_t ld_out,
                     float *part, cudaStream_t st)
 {
-    Args a = base;
-    a.M = T, a.N = I, a.K = H;
-    a.act = act, a.h = h, a.gu = gu;
-    if (T <= kFewMost) {
-        const cudaError_t err = launch_few<kGated, TE>(a, x, ld_x, Wgu, 2 * (int64_t)I, false, st);
-        if (err != cudaSuccess)
-            return err;
-        a = base;
-        a.M = T, a.N = H, a.K = I;
-        a.d = out, a.ld_d = ld_out, a.add = add, a.ld_add = ld_add;
-        // (the kernel before it waits for whatever wrote W_down, and lets this one start only then)
-        return launch_few<kStore, TE>(a, h, I, Wd, H, true, st);
-    }
-    if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, Wgu, H, 2 * (int64_t)I, H, 128))
-        return cudaErrorInvalidValue;
-    cudaError_t err = launch<kGated, 0, TE, 256>(a, part, st);
+    Args gated = base, down = base;
+    gated.act = act, gated.h = h, gated.gu = gu;
+    product(gated, T, I, H, 0, x, ld_x, Wgu, H);
+    Product &q = product(down, T, H, I, 0, h, I, Wd, I);
+    q.d = out, q.ld_d = ld_out, q.add = add, q.ld_add = ld_add;
+    const bool few = T <= kFewMost;
+    const cudaError_t err = few ? launch_few<kGated, TE>(gated, false, st) : launch<kGated, TE>(gated, part, st);
     if (err != cudaSuccess)
         return err;
-    a = base;
-    a.M = T, a.N = H, a.K = I;
-    a.d = out, a.ld_d = ld_out, a.add = add, a.ld_add = ld_add;
-    if (!map16(&a.tm_a, h, I, T, I, 128) || !map16(&a.tm_b, Wd, I, H, I, 128))
-        return cudaErrorInvalidValue;
-    return launch<kStore, 0, TE, 256>(a, part, st);
+    // (the kernel before it waits for whatever wrote W_down, and lets this one start only then)
+    return few ? launch_few<kStore, TE>(down, true, st) : launch<kStore, TE>(down, part, st);
 }
 
 template <class TE>
@@ -69,41 +50,30 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
                      int64_t ld_dx, bool f32, bool accumulate, void *dWgu, void *dWd, void *dgu, float *part,
                      cudaStream_t st)
 {
-    cudaError_t err = cudaSuccess;
-    Args a = base;
+    const int64_t I2 = 2 * (int64_t)I;
     if (dx || dWgu) {
-        a.M = T, a.N = I, a.K = H;
+        Args a = base;
         a.act = act, a.gu = const_cast<void *>(gu), a.dgu = dgu;
-        if (!map16(&a.tm_a, dout, H, T, ld_dout, 128) || !map16(&a.tm_b, Wd, I, H, I, 64))
-            return cudaErrorInvalidValue;
-        if ((err = launch<kGatedBwd, 1, TE, 256>(a, part, st)) != cudaSuccess)
+        product(a, T, I, H, 1, dout, ld_dout, Wd, I);
+        const cudaError_t err = launch<kGatedBwd, TE>(a, part, st);
+        if (err != cudaSuccess)
             return err;
     }
+    Args a = base;
     if (dx) {
-        a = base;
-        a.M = T, a.N = H, a.K = 2 * I;
-        a.d = dx, a.ld_d = ld_dx;
-        if (!map16(&a.tm_a, dgu, 2 * (int64_t)I, T, 2 * (int64_t)I, 128) ||
-            !map16(&a.tm_b, Wgu, H, 2 * (int64_t)I, H, 64))
-            return cudaErrorInvalidValue;
-        if ((err = launch<kStore, 1, TE, 256>(a, part, st)) != cudaSuccess)
-            return err;
+        Product &p = product(a, T, H, (int)I2, 1, dgu, I2, Wgu, H);
+        p.d = dx, p.ld_d = ld_dx;
     }
-    const auto wgrad = [&](const void *d, int64_t rows, int64_t ld, const void *v, int cols, int64_t ld_v, void *dW) {
-        a = base;
-        a.M = rows, a.N = cols, a.K = (int)T;
-        a.d = dW, a.ld_d = cols, a.d_f32 = f32;
+    const auto wgrad = [&](Product &p, void *dW) {
+        p.d = dW, p.ld_d = p.N, p.d_f32 = f32;
         if (accumulate)
-            a.add = dW, a.ld_add = cols;
-        if (!map16(&a.tm_a, d, rows, T, ld, 64) || !map16(&a.tm_b, v, cols, T, ld_v, 64))
-            return cudaErrorInvalidValue;
-        return launch<kStore, 2, TE, 256>(a, part, st);
+            p.add = dW, p.ld_add = p.N;
     };
-    if (dWgu && (err = wgrad(dgu, 2 * (int64_t)I, 2 * (int64_t)I, x, H, ld_x, dWgu)) != cudaSuccess)
-        return err;
+    if (dWgu)
+        wgrad(product(a, I2, H, (int)T, 2, dgu, I2, x, ld_x), dWgu);
     if (dWd)
-        err = wgrad(dout, H, ld_dout, h, I, I, dWd);
-    return err;
+        wgrad(product(a, H, I, (int)T, 2, dout, ld_dout, h, I), dWd);
+    return a.n ? launch<kStore, TE>(a, part, st) : cudaSuccess;
 }
 
 }  // namespace

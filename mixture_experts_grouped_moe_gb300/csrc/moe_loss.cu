@@ -109,15 +109,13 @@ __global__ void __launch_bounds__(256) kept_rows_kernel(const uint4 *x, int64_t 
     }
 }
 
-bool map16(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t pitch, int box_rows)
-{
-    return encode_tmap_2d_pitched(m, p, 2, inner, rows, pitch, 64, box_rows);
-}
-
 bool bad_sizes(int64_t T, int H, int V) { return H % 8 != 0 || H > 1 << 20 || V > 1 << 24 || T > 1 << 30; }
 
-// (maximum, sum) pairs that the forward may keep of a row: one for each tile, or each part of one
-int64_t pairs_of(int64_t T, int V) { return T <= kFewMost ? ((int64_t)V + 127) / 128 * 8 : ((int64_t)V + 255) / 256; }
+// (maximum, sum) pairs that the forward may keep of a row: one for each part of a tile's rows, or two a tile
+int64_t pairs_of(int64_t T, int V)
+{
+    return T <= kFewMost ? ((int64_t)V + 127) / 128 * 8 : ((int64_t)V + 255) / 256 * 2;
+}
 
 // Byte offsets of the workspace (forward: stats and target logits; backward: dl of a piece, kept rows, dx's sum).
 struct Forward {
@@ -147,20 +145,14 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
                     int H, int V, float2 *stats, float *own, float *loss, float *lse, cudaStream_t st)
 {
     Args a = base;
-    a.M = T, a.N = V, a.K = H, a.V = V;
+    product(a, T, V, H, 0, x, ld_x, W, H);
+    a.V = V;
     a.targets = targets, a.stats = stats, a.target_logit = own;
-    cudaError_t err;
-    if (T <= kFewMost) {
-        err = launch_few<kLse, TE>(a, x, ld_x, W, V, false, st);
-    } else {
-        if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, W, H, V, H, 128))
-            return cudaErrorInvalidValue;
-        err = launch<kLse, 0, TE, 256>(a, nullptr, st);
-    }
+    const cudaError_t err = T <= kFewMost ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, nullptr, st);
     if (err != cudaSuccess)
         return err;
     return launch_kernel(true, finish_kernel, dim3((unsigned)((T + 7) / 8)), dim3(256), 0, st, (const float2 *)stats,
-                         (const float *)own, targets, T, a.tiles_n * a.S, V, loss, lse);
+                         (const float *)own, targets, T, a.pairs, V, loss, lse);
 }
 
 template <class TE>
@@ -189,37 +181,28 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         const int n = (int)(V - v0 < piece ? V - v0 : piece);
         const uint8_t *Wp = static_cast<const uint8_t *>(W) + v0 * H * 2;
         Args a = base;
-        a.M = T, a.N = n, a.K = H;
+        Product &p = product(a, T, n, H, 0, x, ld_x, Wp, H);
         a.targets = targets, a.lse = lse, a.dloss = dloss, a.dscale = factor, a.v0 = (int)v0, a.V = V;
-        a.d = dl, a.ld_d = pitch;
-        if (!map16(&a.tm_a, x, H, T, ld_x, 128) || !map16(&a.tm_b, Wp, H, n, H, 128))
-            return cudaErrorInvalidValue;
-        if ((err = launch<kDlogits, 0, TE, 256>(a, nullptr, st)) != cudaSuccess)
+        p.d = dl, p.ld_d = pitch;
+        if ((err = launch<kDlogits, TE>(a, nullptr, st)) != cudaSuccess)
             return err;
+        a = base;
         if (dx) {  // the sum over the pieces, scaled back and rounded with the last one
             const bool last = v0 + n == V;
-            a = base;
-            a.M = T, a.N = H, a.K = n;
-            a.acc_in = v0 ? sum : nullptr;
-            a.d = last ? dx : sum, a.ld_d = last ? ld_dx : H, a.d_f32 = !last;
-            a.scale = last ? factor + 1 : nullptr;
-            if (!map16(&a.tm_a, dl, n, T, pitch, 128) || !map16(&a.tm_b, Wp, H, n, H, 64))
-                return cudaErrorInvalidValue;
-            if ((err = launch<kStore, 1, TE, 256>(a, part, st)) != cudaSuccess)
-                return err;
+            Product &q = product(a, T, H, n, 1, dl, pitch, Wp, H);
+            q.acc_in = v0 ? sum : nullptr;
+            q.d = last ? dx : sum, q.ld_d = last ? ld_dx : H, q.d_f32 = !last;
+            q.scale = last ? factor + 1 : nullptr;
         }
         if (dW) {
-            a = base;
-            a.M = n, a.N = H, a.K = (int)T;
-            a.d = static_cast<uint8_t *>(dW) + v0 * H * es, a.ld_d = H, a.d_f32 = f32;
-            a.scale = factor + 1;
+            Product &q = product(a, n, H, (int)T, 2, dl, pitch, ws + L.rows, H);
+            q.d = static_cast<uint8_t *>(dW) + v0 * H * es, q.ld_d = H, q.d_f32 = f32;
+            q.scale = factor + 1;
             if (accumulate)
-                a.add = a.d, a.ld_add = H;
-            if (!map16(&a.tm_a, dl, n, T, pitch, 64) || !map16(&a.tm_b, ws + L.rows, H, T, H, 64))
-                return cudaErrorInvalidValue;
-            if ((err = launch<kStore, 2, TE, 256>(a, part, st)) != cudaSuccess)
-                return err;
+                q.add = q.d, q.ld_add = H;
         }
+        if (a.n && (err = launch<kStore, TE>(a, part, st)) != cudaSuccess)
+            return err;
     }
     return err;
 }
