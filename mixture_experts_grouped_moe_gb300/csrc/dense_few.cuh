@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Product &p = a.p[0];
-    const int S = p.S;
+    const int S = a.S;
     const int rank = blockIdx.x % S, tile = blockIdx.x / S;
     volatile int *abort_flag = &sm.abort;
 
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                 sum8(col, half + i, u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    h[j] = act_of(g[j], a.act) * u[j];
+                    h[j] = g[j];
+                gate(a.act, h, u);
                 store8(static_cast<TE *>(a.h) + (int64_t)col * p.N + f, h);
                 if (a.gu) {
                     TE *kept = static_cast<TE *>(a.gu) + (int64_t)col * 2 * p.N + f;
@@ -296,8 +297,8 @@ cudaError_t launch_few_np(Args &a, bool early, cudaStream_t st)
     Product &p = a.p[0];
     p.tiles_n = (p.N + kTile - 1) / kTile;
     p.tiles_m = 1;
-    p.S = few_split(p.tiles_n, p.K, sms * (NP <= 64 ? 2 : 1));
-    a.pairs = p.tiles_n * p.S;
+    a.S = few_split(p.tiles_n, p.K, sms * (NP <= 64 ? 2 : 1));
+    a.pairs = p.tiles_n * a.S;
     const int64_t w_rows = MODE == kGated ? 2 * (int64_t)p.N : p.N;
     if (!encode_tmap_2d_pitched(&p.tm_a, p.A, 2, p.K, p.M, p.ld_a, 64, NP) ||
         !encode_tmap_2d_pitched(&p.tm_b, p.B, 2, p.K, w_rows, p.ld_b, 64, kTile))
@@ -306,7 +307,7 @@ cudaError_t launch_few_np(Args &a, bool early, cudaStream_t st)
     if (err != cudaSuccess)
         return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.tiles_n * p.S));
+    cfg.gridDim = dim3((unsigned)(p.tiles_n * a.S));
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = kFewSmemBytes<NP>;
     cfg.stream = st;
@@ -314,7 +315,7 @@ cudaError_t launch_few_np(Args &a, bool early, cudaStream_t st)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.S;
+    attr[1].val.clusterDim.x = a.S;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;

@@ -16,9 +16,10 @@
 // 8 x 10 tiles' rows through L2.  Products that do not depend on one another (the gradients of x and of the
 // weights) go into one launch, longest K first: one start, one tail and one rounding up to whole waves.
 //
-// Few tiles (a short batch, a narrow matrix) leave pairs idle: tiles are then half as wide, or K is split over S
-// pairs a tile, which store fp32 partial sums, and a second kernel adds them in ascending order and applies the
-// epilogue.  Every sum has a fixed order: results are bitwise reproducible.
+// Few tiles (a short batch, a narrow matrix) leave pairs idle: tiles are then half as wide, or K is split over the
+// S = 2 or 4 pairs of a cluster.  Each then owns 1/S of the tile's columns: the others' fp32 parts of them come
+// through distributed shared memory, into the stages that no MMA reads any more, and are added in ascending order
+// before the epilogue.  Every sum has a fixed order: results are bitwise reproducible.
 #pragma once
 
 #include <atomic>
@@ -53,8 +54,7 @@ struct Product {
     int K;
     int maj;              // 0, 1 or 2, as above
     int tiles_m, tiles_n;
-    int S;                // pairs that share a tile's K
-    int first;            // its first item; an item is a tile, or a part of K of one
+    int first;            // its first tile
     // kStore: d [M] rows of N at pitch ld_d, of the rows' type or fp32; add of d's type
     void *d;
     int64_t ld_d;
@@ -67,8 +67,8 @@ struct Product {
 
 struct Args {
     Product p[kProducts];
-    int n, items;
-    float *part;          // partial sums, one accumulator an item
+    int n, tiles;
+    int S;                // pairs that share a tile's K, one cluster
     int *status;
     // gated
     int act;
@@ -92,11 +92,13 @@ constexpr int kABytes = 128 * 128;  // 128 rows x 64 elements of K
 template <int NT>
 constexpr int kStageBytes = kABytes + NT / 2 * 128;
 template <int NT>
-constexpr int kStages = NT == 256 ? 7 : 9;
+constexpr int kStages = NT == 256 ? 6 : 8;
+constexpr int kRowsBytes = 4096;    // an epilogue warp's 32 rows of 32 columns of up to 32 bits
 
 template <int NT>
 struct __align__(1024) Smem {
     uint8_t stage[kStages<NT>][kStageBytes<NT>];
+    uint8_t rows[kEpiWarps][kRowsBytes];
     uint64_t full[kStages<NT>];   // leader: both CTAs' bytes of the stage
     uint64_t empty[kStages<NT>];  // both: the MMAs have read the stage
     uint64_t tfull[2];            // both: accumulator complete
@@ -119,24 +121,26 @@ __device__ __forceinline__ float sigmoid_of(float q) { return __fdividef(1.0f, 1
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.044715f;
 
-__device__ __forceinline__ float act_of(float g, int act)
+template <int ACT>
+__device__ __forceinline__ float act_of(float g)
 {
-    if (act == MOE_ACT_RELU)
+    if (ACT == MOE_ACT_RELU)
         return g <= 0.0f ? 0.0f : g;  // (a NaN stays one)
-    const float q = act == MOE_ACT_SILU ? g : kGeluA * fmaf(kGeluB * g * g, g, g);
+    const float q = ACT == MOE_ACT_SILU ? g : kGeluA * fmaf(kGeluB * g * g, g, g);
     return g * sigmoid_of(q);
 }
 
 // act(g) and its derivative s + g s (1 - s) q'(g)
-__device__ __forceinline__ void act_grad(float g, int act, float &a, float &da)
+template <int ACT>
+__device__ __forceinline__ void act_grad(float g, float &a, float &da)
 {
-    if (act == MOE_ACT_RELU) {
+    if (ACT == MOE_ACT_RELU) {
         a = g <= 0.0f ? 0.0f : g;
         da = g <= 0.0f ? 0.0f : 1.0f;
         return;
     }
     float q = g, dq = 1.0f;
-    if (act != MOE_ACT_SILU) {
+    if (ACT != MOE_ACT_SILU) {
         const float g2 = g * g;
         q = kGeluA * fmaf(kGeluB * g2, g, g);
         dq = kGeluA * fmaf(3.0f * kGeluB, g2, 1.0f);
@@ -145,6 +149,30 @@ __device__ __forceinline__ void act_grad(float g, int act, float &a, float &da)
     a = g * s;
     const float slope = s * (1.0f - s);
     da = slope == 0.0f ? s : fmaf(a * (1.0f - s), dq, s);  // (dq may be infinite where the slope is zero)
+}
+
+// fn(a constant of the activation): the choice outside the loops over elements (inside, the branches kept a warp's
+// exponentials apart: 3.7 us of a 256 x 256 tile's epilogue against 1.2).
+template <class F>
+__device__ __forceinline__ void with_act(int act, F fn)
+{
+    if (act == MOE_ACT_SILU)
+        fn(std::integral_constant<int, MOE_ACT_SILU>());
+    else if (act == MOE_ACT_GELU_TANH)
+        fn(std::integral_constant<int, MOE_ACT_GELU_TANH>());
+    else
+        fn(std::integral_constant<int, MOE_ACT_RELU>());
+}
+
+// g = act(g) * u
+template <int W>
+__device__ __forceinline__ void gate(int act, float (&g)[W], const float (&u)[W])
+{
+    with_act(act, [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            g[i] = act_of<decltype(kind)::value>(g[i]) * u[i];
+    });
 }
 
 // --------------------------------------------------------------- epilogue
@@ -158,14 +186,95 @@ __device__ __forceinline__ void store8(TE *dst, const float *v)
 }
 
 template <class TE>
-__device__ __forceinline__ void load8(const TE *src, float *v)
+__device__ __forceinline__ void unpack8(const uint4 &w, float *v)
 {
-    const uint4 w = *reinterpret_cast<const uint4 *>(src);
     unpack_word(w.x, v[0], v[1], TE{});
     unpack_word(w.y, v[2], v[3], TE{});
     unpack_word(w.z, v[4], v[5], TE{});
     unpack_word(w.w, v[6], v[7], TE{});
 }
+
+template <class TE>
+__device__ __forceinline__ void load8(const TE *src, float *v)
+{
+    unpack8<TE>(*reinterpret_cast<const uint4 *>(src), v);
+}
+
+// 32 rows x 32 columns between memory and a warp's registers, through its shared memory.  The accumulator gives a
+// thread a row; 16 bytes of 32 different rows at a time would touch 32 lines a request and thrash the little L1
+// that is left (a 256 x 256 tile's epilogue with `add` took 13 us, the gated backward's 23 us).  Here a request
+// covers whole rows (64 or 128 bytes), and the pieces of 16 bytes are swizzled so that both orders are free of
+// bank conflicts.
+template <class T>
+struct Rows {
+    static constexpr int kP = sizeof(T) == 4 ? 8 : 4;    // pieces of a row; also: requests
+    static constexpr int kV = 16 / (int)sizeof(T);       // elements of a piece
+    __device__ __forceinline__ static int at(int r, int c) { return r * kP + (kP == 8 ? c ^ (r & 7) : c ^ (r >> 1 & 3)); }
+
+    // Rows 0 .. rows - 1 and columns 0 .. cols - 1 of p; zeros elsewhere.
+    __device__ __forceinline__ static void load(const T *p, int64_t ld, int rows, int cols, int lane, uint4 *w)
+    {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            const int r = i * (32 / kP) + lane / kP, c = lane % kP * kV;
+            w[i] = r < rows && c < cols ? *reinterpret_cast<const uint4 *>(p + r * ld + c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // As loaded -> the thread's own row.
+    __device__ __forceinline__ static void to_row(uint4 *buf, uint4 *w, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            buf[at(i * (32 / kP) + lane / kP, lane % kP)] = w[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            w[i] = buf[at(lane, i)];
+        __syncwarp();
+    }
+    // The thread's own row -> memory.
+    __device__ __forceinline__ static void store(uint4 *buf, const uint4 *w, T *p, int64_t ld, int rows, int cols, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            buf[at(lane, i)] = w[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            const int r = i * (32 / kP) + lane / kP, c = lane % kP * kV;
+            const uint4 v = buf[at(r, lane % kP)];
+            if (r < rows && c < cols)
+                *reinterpret_cast<uint4 *>(p + r * ld + c) = v;
+        }
+        __syncwarp();
+    }
+};
+
+template <class TE>
+__device__ __forceinline__ uint4 pack8(const float *v)
+{
+    return make_uint4(pack_word(v[0], v[1], TE{}), pack_word(v[2], v[3], TE{}), pack_word(v[4], v[5], TE{}),
+                      pack_word(v[6], v[7], TE{}));
+}
+
+// 32 values of the thread's row, each rounded, to memory.
+template <class TE>
+__device__ __forceinline__ void put_rows(uint4 *buf, const float *v, TE *p, int64_t ld, int rows, int cols, int lane)
+{
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = pack8<TE>(v + 8 * i);
+    Rows<TE>::store(buf, w, p, ld, rows, cols, lane);
+}
+
+__device__ __forceinline__ void add4(float *v, const uint4 &w)
+{
+    v[0] += __uint_as_float(w.x), v[1] += __uint_as_float(w.y);
+    v[2] += __uint_as_float(w.z), v[3] += __uint_as_float(w.w);
+}
+
+// The forms that follow are of one thread's row in pieces of its own (the few columns of a split tile's owner).
 
 // W columns from `col` of row `row` (N % 8 == 0; row < M).
 template <class TE, int W>
@@ -188,33 +297,44 @@ __device__ __forceinline__ void epi_store(const Product &a, int64_t row, int col
     }
     if (a.d_f32) {
         float *dst = static_cast<float *>(a.d) + row * a.ld_d + col;
-        const float *add = static_cast<const float *>(a.add) + row * a.ld_add + col;
+        if (a.add) {
+            const float *add = static_cast<const float *>(a.add) + row * a.ld_add + col;
+            float4 f[W / 4];
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+                if (col + i < a.N)
+                    f[i / 4] = *reinterpret_cast<const float4 *>(add + i);
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+                v[i] += f[i / 4].x, v[i + 1] += f[i / 4].y, v[i + 2] += f[i / 4].z, v[i + 3] += f[i / 4].w;
+        }
 #pragma unroll
         for (int i = 0; i < W; i += 4)
-            if (col + i < a.N) {
-                float4 f = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                if (a.add) {
-                    const float4 g = *reinterpret_cast<const float4 *>(add + i);
-                    f.x += g.x, f.y += g.y, f.z += g.z, f.w += g.w;
-                }
-                *reinterpret_cast<float4 *>(dst + i) = f;
-            }
+            if (col + i < a.N)
+                *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         return;
     }
     TE *dst = static_cast<TE *>(a.d) + row * a.ld_d + col;
-    const TE *add = static_cast<const TE *>(a.add) + row * a.ld_add + col;
+    if (a.add) {
+        const TE *add = static_cast<const TE *>(a.add) + row * a.ld_add + col;
+        uint4 w[W / 8];
+#pragma unroll
+        for (int i = 0; i < W; i += 8)
+            if (col + i < a.N)
+                w[i / 8] = *reinterpret_cast<const uint4 *>(add + i);
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            float f[8];
+            unpack8<TE>(w[i / 8], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i + j] += f[j];
+        }
+    }
 #pragma unroll
     for (int i = 0; i < W; i += 8)
-        if (col + i < a.N) {
-            if (a.add) {
-                float f[8];
-                load8(add + i, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[i + j] += f[j];
-            }
+        if (col + i < a.N)
             store8(dst + i, v + i);
-        }
 }
 
 // h = act(g) u, from the unrounded products; g and u are rounded only where they are kept.
@@ -232,37 +352,56 @@ __device__ __forceinline__ void epi_gated(const Args &a, int64_t row, int col, f
                 store8(kept + N + i, u + i);
             }
     }
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-        g[i] = act_of(g[i], a.act) * u[i];
+    gate(a.act, g, u);
 #pragma unroll
     for (int i = 0; i < W; i += 8)
         if (col + i < N)
             store8(hd + i, g + i);
 }
 
-// d gate = dh u act'(g), d up = dh act(g): rounded to 16 bits as the operands of the products that follow.
+// d gate = dh u act'(g), d up = dh act(g) of 8 columns, in the place of g and u: rounded to 16 bits as the operands
+// of the products that follow.
+template <class TE, int ACT>
+__device__ __forceinline__ void gated_grad8(const float *dh, uint4 &wg, uint4 &wu)
+{
+    float g[8], u[8];
+    unpack8<TE>(wg, g);
+    unpack8<TE>(wu, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float v, slope;
+        act_grad<ACT>(g[j], v, slope);
+        g[j] = dh[j] * u[j] * slope;
+        u[j] = dh[j] * v;
+    }
+    wg = pack8<TE>(g);
+    wu = pack8<TE>(u);
+}
+
 template <class TE, int W>
 __device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int col, const float (&dh)[W])
 {
     const int N = a.p[0].N;
     const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * N + col;
     TE *out = static_cast<TE *>(a.dgu) + row * 2 * N + col;
+    uint4 wg[W / 8], wu[W / 8];
 #pragma unroll
     for (int i = 0; i < W; i += 8)
         if (col + i < N) {
-            float g[8], u[8];
-            load8(kept + i, g);
-            load8(kept + N + i, u);
+            wg[i / 8] = *reinterpret_cast<const uint4 *>(kept + i);
+            wu[i / 8] = *reinterpret_cast<const uint4 *>(kept + N + i);
+        }
+    with_act(a.act, [&](auto kind) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float act, slope;
-                act_grad(g[j], a.act, act, slope);
-                g[j] = dh[i + j] * u[j] * slope;
-                u[j] = dh[i + j] * act;
-            }
-            store8(out + i, g);
-            store8(out + N + i, u);
+        for (int i = 0; i < W; i += 8)
+            if (col + i < N)
+                gated_grad8<TE, decltype(kind)::value>(dh + i, wg[i / 8], wu[i / 8]);
+    });
+#pragma unroll
+    for (int i = 0; i < W; i += 8)
+        if (col + i < N) {
+            *reinterpret_cast<uint4 *>(out + i) = wg[i / 8];
+            *reinterpret_cast<uint4 *>(out + N + i) = wu[i / 8];
         }
 }
 
@@ -307,10 +446,8 @@ __device__ __forceinline__ void epi_lse(int N, int col, int target, float (&v)[3
     s = fmaf(s, exp2_fast(fmaf(was, kLog2e, -base)), (part[0] + part[1]) + (part[2] + part[3]));
 }
 
-// factor (softmax - one at the target), 32 columns; the pitch of the rows (ld_d) is a multiple of 8.
-template <class TE>
-__device__ __forceinline__ void epi_dlogits(const Args &a, int64_t row, int col, int target, float lse, float factor,
-                                            float (&v)[32])
+// factor (softmax - one at the target), 32 columns.
+__device__ __forceinline__ void epi_dlogits(int col, int target, float lse, float factor, float (&v)[32])
 {
     const float base = lse * kLog2e;
     const int at = target - col;
@@ -321,11 +458,6 @@ __device__ __forceinline__ void epi_dlogits(const Args &a, int64_t row, int col,
             p -= 1.0f;
         v[i] = factor == 0.0f ? 0.0f : factor * p;  // (a row left out adds nothing, whatever its logits)
     }
-    TE *dst = static_cast<TE *>(a.p[0].d) + row * a.p[0].ld_d + col;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (col + i < a.p[0].N)
-            store8(dst + i, v + i);
 }
 
 // -------------------------------------------------------------- the tiles
@@ -336,8 +468,9 @@ struct Tile {
     int kb0, kb1;  // blocks of 64 of K
 };
 
+// Tile t, and the part of K that falls to pair s of the cluster.
 template <int MODE>
-__device__ __forceinline__ Tile tile_of(const Args &a, int t)
+__device__ __forceinline__ Tile tile_of(const Args &a, int t, int s)
 {
     Tile r;
     r.prod = 0;
@@ -346,12 +479,9 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t)
             ++r.prod;
     const Product &p = a.p[r.prod];
     t -= p.first;
-    const int per = p.tiles_m * p.tiles_n;
     const int nkb = (p.K + 63) / 64;
-    const int s = t / per;
-    t -= s * per;
-    r.kb0 = (int)((int64_t)nkb * s / p.S);
-    r.kb1 = (int)((int64_t)nkb * (s + 1) / p.S);
+    r.kb0 = (int)((int64_t)nkb * s / a.S);
+    r.kb1 = (int)((int64_t)nkb * (s + 1) / a.S);
     const int g = t / (kGroup * p.tiles_n);
     const int size = min(kGroup, p.tiles_m - g * kGroup);
     t -= g * kGroup * p.tiles_n;
@@ -364,12 +494,75 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t)
 template <int MODE, int NT>
 constexpr int kCols = MODE == kGated ? NT / 2 : NT;
 
-// Partial sums of CTA `rank` of an item: [NT / 4][128 rows] of four columns, so that neighbouring threads (rows)
-// touch neighbouring 16 bytes.
-template <int NT>
-__device__ __forceinline__ float4 *part_of(const Args &a, int item, int rank)
+// Modes whose tiles may be split (the others' tiles, of a vocabulary, are many).
+template <int MODE>
+constexpr bool kSplits = MODE == kStore || MODE == kGated || MODE == kGatedBwd;
+
+// The parts of a split tile's accumulator to the pairs that own their columns, and the owners' epilogue.  All
+// threads of the cluster.  buf: [S sources][columns / 4][128 rows] of four columns, so that neighbouring threads
+// (rows) touch neighbouring 16 bytes.
+template <int MODE, class TE, int NT>
+__device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_base, const Tile &tile, int rank,
+                                     int pair, int warp, int lane)
 {
-    return reinterpret_cast<float4 *>(a.part) + ((int64_t)item * 2 + rank) * (NT / 4 * 128);
+    const int S = a.S, q = warp & 3, half = (warp - 2) / 4, r = q * 32 + lane;
+    // accumulator columns that a pair owns: gated, as many of the gate's as of the up's
+    constexpr int kSides = MODE == kGated ? 2 : 1;
+    constexpr int kSide = NT / kSides;
+    const int own = kSide / S;  // of each side, 32 or more
+    if (warp >= 2) {
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+        for (int c = half * (NT / 2); c < (half + 1) * (NT / 2); c += 16) {
+            float v[16];
+            tmem_ld16(tacc + c, v);
+            const int side = c / kSide, at = c % kSide, owner = at / own, local = side * own + at % own;
+            const uint32_t dst = cluster_map(buf, (uint32_t)(owner * 2 + rank)) +
+                                 (uint32_t)(((pair * kSides * own + local) / 4 * 128 + r) * 16);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)(i / 4 * 2048)),
+                             "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3])
+                             : "memory");
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp < 2)
+        return;
+    const Product &p = a.p[tile.prod];
+    const int64_t row = tile.m0 + rank * 128 + r;
+    const int mine = own / 2;  // columns of this warp
+    const int col = tile.nt * kCols<MODE, NT> + pair * own + half * mine;
+    if (row >= p.M)
+        return;
+    const auto sum16 = [&](int local, float(&v)[16]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = 0.0f;
+        for (int s = 0; s < S; ++s) {
+            const float4 *src = reinterpret_cast<const float4 *>(buf) + (s * kSides * own + local) / 4 * 128 + r;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 f = src[i / 4 * 128];
+                v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
+            }
+        }
+    };
+#pragma unroll 1
+    for (int c = 0; c < mine && col + c < p.N; c += 16) {
+        float v[16];
+        sum16(half * mine + c, v);
+        if constexpr (MODE == kGated) {
+            float u[16];
+            sum16(own + half * mine + c, u);
+            epi_gated<TE>(a, row, col + c, v, u);
+        } else if constexpr (MODE == kStore) {
+            epi_store<TE>(p, row, col + c, v);
+        } else {
+            epi_gated_bwd<TE>(a, row, col + c, v);
+        }
+    }
 }
 
 template <int MODE, class TE, int NT>
@@ -381,7 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank();
+    const int S = a.S;
+    const int in_cluster = (int)cluster_ctarank();
+    const int rank = in_cluster & 1, pair = in_cluster >> 1;
+    const uint32_t lead = (uint32_t)(pair * 2);  // the pair's leader
+    const uint16_t both = (uint16_t)(3u << (pair * 2));
     const bool leader = rank == 0;
     volatile int *abort_flag = &sm.abort;
 
@@ -411,10 +608,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     cluster_sync();  // both CTAs' barriers exist before any signal between them
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
+    // (S > 1: a tile a cluster)
+    const int first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
+    {
+        // the first tile's arithmetic before the wait: it brings the parameters it reads into the constant cache
+        const Tile t = tile_of<MODE>(a, first, pair);
+        const Product &p = a.p[t.prod];
+        asm volatile("" ::"r"(t.kb1), "r"(t.m0), "r"(p.N), "r"(p.maj), "l"(p.M), "l"(p.d), "l"(p.add), "l"(a.status)
+                     : "memory");
+    }
     pdl_wait();
     pdl_trigger();
-
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -422,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int s = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < a.items; t += step) {
-                const Tile tile = tile_of<MODE>(a, t);
+            for (int t = first; ok && t < a.tiles; t += step) {
+                const Tile tile = tile_of<MODE>(a, t, pair);
                 const Product &p = a.p[tile.prod];
                 const int maj = MODE == kStore ? p.maj : MODE == kGatedBwd ? 1 : 0;
                 const int arow = tile.m0 + rank * 128;
@@ -435,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         break;
                     }
                     uint8_t *sa = sm.stage[s], *sb = sm.stage[s] + kABytes;
-                    const uint32_t bar = cluster_map(&sm.full[s], 0);
+                    const uint32_t bar = cluster_map(&sm.full[s], lead);
                     if (leader)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * kStageBytes<NT>);
                     if (maj == 2) {
@@ -471,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < a.items; t += step) {
-                const Tile tile = tile_of<MODE>(a, t);
+            for (int t = first; ok && t < a.tiles; t += step) {
+                const Tile tile = tile_of<MODE>(a, t, pair);
                 const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
                 const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
                                        (maj == 2 ? 1u << 15 : 0u);
@@ -499,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         da += ia, db += ib;  // (the start address is the descriptor's lowest field)
                     }
                     any = true;
-                    mma_commit_pair(&sm.empty[s], 0x3);
+                    mma_commit_pair(&sm.empty[s], both);
                     if (++s == kS) {
                         s = 0;
                         ph ^= 1;
@@ -507,14 +711,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
                 if (!ok)
                     break;
-                mma_commit_pair(&sm.tfull[acc], 0x3);
+                mma_commit_pair(&sm.tfull[acc], both);
                 if (++acc == 2) {
                     acc = 0;
                     aph ^= 1;
                 }
             }
             if (!ok && any) {
-                mma_commit_pair(&sm.drain, 0x1);
+                mma_commit_pair(&sm.drain, (uint16_t)(1u << lead));
                 const unsigned long long t0 = global_timer_ns();
                 while (!mbar_try_wait(&sm.drain, 0) && global_timer_ns() - t0 < 100000000ull) {
                 }
@@ -526,22 +730,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int r = q * 32 + lane;
         int acc = 0;
         uint32_t aph = 0;
-        for (int t = first; t < a.items; t += step) {
-            const Tile tile = tile_of<MODE>(a, t);
+        for (int t = first; t < a.tiles; t += step) {
+            const Tile tile = tile_of<MODE>(a, t, pair);
             const Product &p = a.p[tile.prod];
             const int64_t row = tile.m0 + rank * 128 + r;
             const bool live = row < p.M;
             constexpr int kMine = kCols<MODE, NT> / 2;              // columns of D of this warp
             const int c0 = tile.nt * kCols<MODE, NT> + half * kMine;  // the first of them
             // what the epilogue will read of memory: into L2 while the MMAs run
-            if (MODE == kGatedBwd && p.S == 1 && live) {
+            if (MODE == kGatedBwd && S == 1 && live) {
                 const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * p.N + c0;
                 for (int c = 0; c < kMine && c0 + c < p.N; c += 64) {
                     prefetch_l2(kept + c);
                     prefetch_l2(kept + p.N + c);
                 }
             }
-            if (MODE == kStore && p.S == 1 && live && p.add) {
+            if (MODE == kStore && S == 1 && live && p.add) {
                 const int es = p.d_f32 ? 4 : 2;
                 const char *add = static_cast<const char *>(p.add) + (row * p.ld_add + c0) * es;
                 for (int c = 0; c < kMine && c0 + c < p.N; c += 128 / es)
@@ -558,61 +762,131 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
                 target = counts ? target - a.v0 : -1;
             }
+            uint4 *buf = reinterpret_cast<uint4 *>(sm.rows[warp - 2]);
+            const int64_t row0 = tile.m0 + rank * 128 + q * 32;  // the warp's rows
+            const int rows = (int)max((int64_t)0, min((int64_t)32, p.M - row0));
+            // the first columns of what is read, before the wait for the accumulator
+            uint4 pre[8];
+            const auto read = [&](int c) {
+                if (rows == 0 || S > 1 || c >= kMine || c0 + c >= p.N)
+                    return;
+                if (MODE == kStore && p.add) {
+                    const int64_t at = row0 * p.ld_add + c0 + c;
+                    if (p.d_f32)
+                        Rows<float>::load(static_cast<const float *>(p.add) + at, p.ld_add, rows, p.N - c0 - c, lane, pre);
+                    else
+                        Rows<TE>::load(static_cast<const TE *>(p.add) + at, p.ld_add, rows, p.N - c0 - c, lane, pre);
+                }
+                if (MODE == kGatedBwd) {
+                    const TE *kept = static_cast<const TE *>(a.gu) + row0 * 2 * p.N + c0 + c;
+                    Rows<TE>::load(kept, 2 * (int64_t)p.N, rows, p.N - c0 - c, lane, pre);
+                    Rows<TE>::load(kept + p.N, 2 * (int64_t)p.N, rows, p.N - c0 - c, lane, pre + 4);
+                }
+            };
+            read(0);
             bool ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             tc_fence_after();
-            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
-            if (p.S > 1) {
-                float4 *dst = part_of<NT>(a, t, rank) + r;
+            if (S > 1)
+                break;  // the parts meet below
+            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
+            float m = -INFINITY, s = 0.0f, own = 0.0f;
+            bool has = false;
 #pragma unroll 1
-                for (int c = half * kHalf; c < (half + 1) * kHalf; c += 32) {
-                    float v[32];
-                    tmem_ld32(tacc + c, v);
-                    if (!live)
-                        continue;
+            for (int c = 0; c < kMine && c0 + c < p.N && rows > 0; c += 32) {
+                const int col = c0 + c, cols = p.N - col;
+                float v[32];
+                tmem_ld32(tacc + c, v);
+                if constexpr (MODE == kStore) {
+                    if (p.acc_in) {
+                        uint4 w[8];
+                        Rows<float>::load(p.acc_in + row0 * p.N + col, p.N, rows, cols, lane, w);
+                        Rows<float>::to_row(buf, w, lane);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        dst[(c + i) / 4 * 128] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            add4(v + 4 * i, w[i]);
+                    }
+                    if (p.scale) {
+                        const float sc = *p.scale;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] *= sc;
+                    }
+                    if (p.d_f32) {
+                        if (p.add) {
+                            Rows<float>::to_row(buf, pre, lane);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                add4(v + 4 * i, pre[i]);
+                            read(c + 32);
+                        }
+                        uint4 w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                              __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                        Rows<float>::store(buf, w, static_cast<float *>(p.d) + row0 * p.ld_d + col, p.ld_d, rows, cols,
+                                           lane);
+                    } else {
+                        if (p.add) {
+                            Rows<TE>::to_row(buf, pre, lane);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float f[8];
+                                unpack8<TE>(pre[i], f);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    v[8 * i + j] += f[j];
+                            }
+                            read(c + 32);
+                        }
+                        put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + col, p.ld_d, rows, cols, lane);
+                    }
+                } else if constexpr (MODE == kGated) {
+                    float u[32];
+                    tmem_ld32(tacc + kHalf + c, u);
+                    if (a.gu) {
+                        TE *kept = static_cast<TE *>(a.gu) + row0 * 2 * p.N + col;
+                        put_rows(buf, v, kept, 2 * (int64_t)p.N, rows, cols, lane);
+                        put_rows(buf, u, kept + p.N, 2 * (int64_t)p.N, rows, cols, lane);
+                    }
+                    gate(a.act, v, u);
+                    put_rows(buf, v, static_cast<TE *>(a.h) + row0 * p.N + col, p.N, rows, cols, lane);
+                } else if constexpr (MODE == kGatedBwd) {
+                    uint4 wg[4], wu[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        wg[i] = pre[i], wu[i] = pre[4 + i];
+                    read(c + 32);
+                    Rows<TE>::to_row(buf, wg, lane);
+                    Rows<TE>::to_row(buf, wu, lane);
+                    with_act(a.act, [&](auto kind) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            gated_grad8<TE, decltype(kind)::value>(v + 8 * i, wg[i], wu[i]);
+                    });
+                    TE *out = static_cast<TE *>(a.dgu) + row0 * 2 * p.N + col;
+                    Rows<TE>::store(buf, wg, out, 2 * (int64_t)p.N, rows, cols, lane);
+                    Rows<TE>::store(buf, wu, out + p.N, 2 * (int64_t)p.N, rows, cols, lane);
+                } else if constexpr (MODE == kLse) {
+                    epi_lse(p.N, col, target, v, m, s, own, has);
+                } else {
+                    epi_dlogits(col, target, lse, factor, v);
+                    // (a last piece of 8 columns may go past N, into the rows' padding)
+                    put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + col, p.ld_d, rows, cols, lane);
                 }
-            } else if (MODE == kGated) {
-#pragma unroll 1
-                for (int c = 0; c < kMine && c0 + c < p.N; c += 32) {
-                    float g[32], u[32];
-                    tmem_ld32(tacc + half * kMine + c, g);
-                    tmem_ld32(tacc + kHalf + half * kMine + c, u);
-                    if (live)
-                        epi_gated<TE>(a, row, c0 + c, g, u);
-                }
-            } else {
-                float m = -INFINITY, s = 0.0f, own = 0.0f;
-                bool has = false;
-#pragma unroll 1
-                for (int c = 0; c < kMine && c0 + c < p.N; c += 32) {
-                    float v[32];
-                    tmem_ld32(tacc + half * kMine + c, v);
-                    if (!live)
-                        continue;
-                    if (MODE == kStore)
-                        epi_store<TE>(p, row, c0 + c, v);
-                    else if (MODE == kGatedBwd)
-                        epi_gated_bwd<TE>(a, row, c0 + c, v);
-                    else if (MODE == kLse)
-                        epi_lse(p.N, c0 + c, target, v, m, s, own, has);
-                    else
-                        epi_dlogits<TE>(a, row, c0 + c, target, lse, factor, v);
-                }
-                if (MODE == kLse && live) {
-                    a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, s);
-                    if (has)
-                        a.target_logit[row] = own;
-                }
+            }
+            if (MODE == kLse && live) {
+                a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, s);
+                if (has)
+                    a.target_logit[row] = own;
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_remote(cluster_map(&sm.tempty[acc], 0));
+                mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
             if (++acc == 2) {
                 acc = 0;
                 aph ^= 1;
@@ -620,64 +894,25 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
     }
 
+    if constexpr (kSplits<MODE>) {
+        if (S > 1) {
+            // every MMA of the cluster has read its stages (the pair's accumulator is complete: what the epilogue
+            // warps waited for)
+            __syncwarp();
+            tc_fence_before();
+            cluster_sync();
+            tc_fence_after();
+            meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
+        }
+    }
     // both CTAs stay until the pair's last MMA, copy and remote arrive are done
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
     if (warp == 1)
         tmem_dealloc_pair(tmem_base, 512);
-}
-
-// The partial sums of a tile added up in ascending order, then the epilogue: a block of 128 threads (rows) for
-// 8 columns of one CTA's part of a tile (32 columns a thread, with the parts in line: 8-17 us instead of 4).
-constexpr int kJoinCols = 8;
-
-struct JoinBlocks {
-    int first[kProducts + 1];  // first block of each product (none for one that is not split)
-};
-
-template <int MODE, class TE, int NT>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a, JoinBlocks jb)
-{
-    constexpr int kChunks = kCols<MODE, NT> / kJoinCols;
-    pdl_wait();
-    pdl_trigger();
-    int prod = 0;
-    while ((int)blockIdx.x >= jb.first[prod + 1])
-        ++prod;
-    const Product &p = a.p[prod];
-    const int b = blockIdx.x - jb.first[prod];
-    const int c = b % kChunks * kJoinCols, rank = b / kChunks & 1, t = b / kChunks / 2;
-    const Tile tile = tile_of<MODE>(a, p.first + t);
-    const int64_t row = tile.m0 + rank * 128 + threadIdx.x;
-    const int col = tile.nt * kCols<MODE, NT> + c;
-    if (row >= p.M || col >= p.N)
-        return;
-    const int tiles = p.tiles_m * p.tiles_n;
-    float v[kJoinCols] = {}, u[kJoinCols] = {};
-#pragma unroll 4
-    for (int s = 0; s < p.S; ++s) {
-        const float4 *src = part_of<NT>(a, p.first + s * tiles + t, rank) + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < kJoinCols; i += 4) {
-            const float4 f = __ldcs(src + (c + i) / 4 * 128);
-            v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
-        }
-        if (MODE == kGated) {
-#pragma unroll
-            for (int i = 0; i < kJoinCols; i += 4) {
-                const float4 f = __ldcs(src + (NT / 2 + c + i) / 4 * 128);
-                u[i] += f.x, u[i + 1] += f.y, u[i + 2] += f.z, u[i + 3] += f.w;
-            }
-        }
-    }
-    if (MODE == kStore)
-        epi_store<TE>(p, row, col, v);
-    else if (MODE == kGated)
-        epi_gated<TE>(a, row, col, v, u);
-    else
-        epi_gated_bwd<TE>(a, row, col, v);
 }
 
 // ------------------------------------------------------------------- host
@@ -704,139 +939,176 @@ bool make_maps(Product &p)
            (p.maj >= 1 ? map(&p.tm_b, p.B, p.N, p.K, p.ld_b, 64) : map(&p.tm_b, p.B, p.K, b_rows, p.ld_b, NT / 2));
 }
 
-// Clusters of two that can be resident at once, kept per device.
 template <int MODE, class TE, int NT>
-int max_pairs()
+cudaLaunchConfig_t config_of(cudaLaunchAttribute (&attr)[2], int S, int64_t clusters, cudaStream_t st)
 {
-    static std::atomic<int> cache[64];  // zero until first computed
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * S * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes<NT>;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// Clusters of S = 1, 2 or 4 pairs that can be resident at once, kept per device (one CTA an SM in every mode and at
+// every width, so one kernel is asked for all of them).
+template <class TE>
+int max_clusters(int S)
+{
+    static std::atomic<int> cache[64][3];  // zero until first computed
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return 0;
-    int n = cache[dev].load(std::memory_order_relaxed);
+    std::atomic<int> &kept = cache[dev][S / 2];
+    int n = kept.load(std::memory_order_relaxed);
     if (n == 0) {
-        auto kern = gemm_kernel<MODE, TE, NT>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>) !=
-            cudaSuccess)
-            return 0;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes<NT>;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
+        auto kern = gemm_kernel<kStore, TE, 256>;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config_of<kStore, TE, 256>(attr, S, 1, nullptr);
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<256>) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
             return 0;
-        cache[dev].store(n, std::memory_order_relaxed);
+        kept.store(n, std::memory_order_relaxed);
     }
     return n;
 }
 
-// Workspace of the partial sums: there are at most as many parts as pairs.
-constexpr int kMostPairs = 80;
-constexpr size_t kPartBytes = (size_t)kMostPairs * 256 * 256 * 4;
-
 template <int MODE, class TE, int NT>
-cudaError_t launch_nt(Args &a, int S, int pairs, cudaStream_t st)
+cudaError_t launch_nt(Args &a, int S, int clusters, cudaStream_t st)
 {
     auto kern = gemm_kernel<MODE, TE, NT>;
-    JoinBlocks jb = {};
-    int64_t items = 0;
-    bool split = false;
+    int64_t tiles = 0;
     for (int i = 0; i < a.n; ++i) {
         Product &p = a.p[i];
         const int64_t tm = (p.M + 255) / 256, tn = (p.N + kCols<MODE, NT> - 1) / kCols<MODE, NT>;
-        const int most = (p.K + 63) / 64;
         if (!make_maps<MODE, NT>(p))
             return cudaErrorInvalidValue;
         p.tiles_m = (int)tm, p.tiles_n = (int)tn;
-        p.S = S < most ? S : most;
-        p.first = (int)items;
-        items += tm * tn * p.S;
-        if (items > 1 << 30)
+        p.first = (int)tiles;
+        tiles += tm * tn;
+        if (tiles > 1 << 30)
             return cudaErrorInvalidValue;
-        split = split || p.S > 1;
-        jb.first[i + 1] = jb.first[i] + (p.S > 1 ? (int)(tm * tn * 2 * (kCols<MODE, NT> / kJoinCols)) : 0);
     }
-    for (int i = a.n; i < kProducts; ++i)
-        jb.first[i + 1] = jb.first[i];
-    a.items = (int)items;
+    a.tiles = (int)tiles;
+    a.S = S;
     a.pairs = a.p[0].tiles_n * 2;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>);
     if (err != cudaSuccess)
         return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (items < pairs ? items : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes<NT>;
-    cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, kern, a);
-    if (err != cudaSuccess || !split)
-        return err;
-    if constexpr (MODE == kStore || MODE == kGated || MODE == kGatedBwd)
-        return launch_kernel(true, join_kernel<MODE, TE, NT>, dim3((unsigned)jb.first[kProducts]), dim3(128), 0, st, a,
-                             jb);
-    return cudaErrorInvalidValue;
+    const cudaLaunchConfig_t cfg =
+        config_of<MODE, TE, NT>(attr, S, S > 1 || tiles < clusters ? tiles : clusters, st);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// The launch's time by its parts: waves of tiles, each the blocks of K in line (KB) and an epilogue that nothing
-// hides in the last wave; a split's second kernel.  In 10 ns.
-inline int64_t cost_of(int64_t tiles, int64_t KB, int S, bool wide, int pairs)
+// Blocks of K that the busiest of `clusters` clusters goes through when tiles of 256 rows x cols are dealt
+// round-robin, product after product: one of those at which a product starts.
+inline int64_t longest_share(const Product *p, int n, int cols, int S, int clusters)
 {
-    const int64_t waves = (tiles * S + pairs - 1) / pairs;
-    return waves * ((KB + S - 1) / S) * (wide ? 28 : 19) + (wide ? 250 : 150) + (S > 1 ? 400 : 0);
+    int64_t tiles[kProducts], blocks[kProducts], start[kProducts], before = 0, most = 0;
+    for (int i = 0; i < n; ++i) {
+        tiles[i] = (p[i].M + 255) / 256 * ((p[i].N + cols - 1) / cols);
+        blocks[i] = ((p[i].K + 63) / 64 + S - 1) / S;
+        start[i] = before % clusters;
+        before += tiles[i];
+    }
+    for (int j = 0; j < n; ++j) {
+        int64_t share = 0;
+        for (int i = 0; i < n; ++i) {
+            const int64_t first = start[j] >= start[i] ? start[j] - start[i] : start[j] - start[i] + clusters;
+            share += (tiles[i] - first + clusters - 1) / clusters * blocks[i];
+        }
+        most = share > most ? share : most;
+    }
+    return most;
 }
 
-// The products of `a` (p[0] .. p[n - 1] but for their tiles), longest K first.  part: kPartBytes, or null (no
-// split).
+struct Plan {
+    int64_t cost;  // in 10 ns
+    int S;
+    bool wide;
+};
+
+// How to launch n products together.  The time is that of the busiest cluster's blocks of K, of an epilogue that
+// nothing hides after the last of them, of the meeting of a split tile's pairs, and of a launch.
+template <int MODE>
+Plan plan(const Product *p, int n, const int *clusters)
+{
+    Plan best = {INT64_MAX, 1, true};
+    int least = p[0].K;
+    for (int i = 1; i < n; ++i)
+        least = p[i].K < least ? p[i].K : least;
+    for (int w = MODE == kLse ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
+        const int cols = (w ? 256 : 128) / (MODE == kGated ? 2 : 1);
+        // (a warp of an owner finishes 16 columns at least, of each side)
+        const int most = !kSplits<MODE> ? 1 : MODE == kGated && !w ? 2 : 4;
+        for (int s = 1; s <= most && (s == 1 || (clusters[s] > 0 && (least + 63) / 64 / s >= 2)); s *= 2) {
+            // (clusters that share a tile take one each: with more tiles than clusters they would start in turns)
+            int64_t tiles = 0;
+            for (int i = 0; i < n; ++i)
+                tiles += (p[i].M + 255) / 256 * ((p[i].N + cols - 1) / cols);
+            if (s > 1 && tiles > clusters[s])
+                continue;
+            const int64_t c = longest_share(p, n, cols, s, clusters[s]) * (w ? 29 : 22) + (w ? 250 : 150) +
+                              (s > 1 ? 230 : 0) + 450;
+            if (c < best.cost)
+                best = {c, s, w != 0};
+        }
+    }
+    return best;
+}
+
+// The products of `a` (p[0] .. p[n - 1]), in one launch, longest K first, or each in its own where that is faster (a
+// product of few tiles and a long K wants it split, one of many tiles does not).
 template <int MODE, class TE>
-cudaError_t launch(Args &a, float *part, cudaStream_t st)
+cudaError_t launch(Args &a, cudaStream_t st)
 {
-    int pairs = max_pairs<MODE, TE, 256>();  // (one CTA an SM at either width)
-    if (pairs <= 0)
-        return cudaErrorInvalidConfiguration;
-    if (pairs > kMostPairs)
-        pairs = kMostPairs;
-    a.part = part;
+    int clusters[5] = {};
+    for (int s = 1; s <= 4; s *= 2)
+        if ((clusters[s] = max_clusters<TE>(s)) <= 0 && s == 1)
+            return cudaErrorInvalidConfiguration;
     for (int i = 1; i < a.n; ++i)
         for (int j = i; j > 0 && a.p[j].K > a.p[j - 1].K; --j) {
             const Product t = a.p[j];
             a.p[j] = a.p[j - 1], a.p[j - 1] = t;
         }
-    int64_t best = INT64_MAX;
-    int S = 1;
-    bool wide = true;
-    for (int w = MODE == kLse ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
-        const int cols = (w ? 256 : 128) / (MODE == kGated ? 2 : 1);
-        int64_t tiles = 0, blocks = 0;
-        for (int i = 0; i < a.n; ++i) {
-            const int64_t n = (a.p[i].M + 255) / 256 * ((a.p[i].N + cols - 1) / cols);
-            tiles += n, blocks += n * ((a.p[i].K + 63) / 64);
-        }
-        const int64_t KB = (blocks + tiles - 1) / tiles;
-        for (int s = 1; s <= 16 && (s == 1 || (part && tiles * s <= pairs && KB / s >= 4)); ++s) {
-            const int64_t c = cost_of(tiles, KB, s, w, pairs);
-            if (c < best)
-                best = c, S = s, wide = w;
-        }
+    const auto go = [&](Args &args, const Plan &how) {
+        if constexpr (MODE != kLse)
+            if (!how.wide)
+                return launch_nt<MODE, TE, 128>(args, how.S, clusters[how.S], st);
+        return launch_nt<MODE, TE, 256>(args, how.S, clusters[how.S], st);
+    };
+    const Plan all = plan<MODE>(a.p, a.n, clusters);
+    if (a.n == 1)
+        return go(a, all);
+    Plan each[kProducts];
+    int64_t sum = 0;
+    for (int i = 0; i < a.n; ++i) {
+        each[i] = plan<MODE>(a.p + i, 1, clusters);
+        sum += each[i].cost;
     }
-    if constexpr (MODE != kLse)
-        if (!wide)
-            return launch_nt<MODE, TE, 128>(a, S, pairs, st);
-    return launch_nt<MODE, TE, 256>(a, S, pairs, st);
+    if (all.cost <= sum)
+        return go(a, all);
+    for (int i = 0; i < a.n; ++i) {
+        Args one = a;
+        one.n = 1;
+        one.p[0] = a.p[i];
+        const cudaError_t err = go(one, each[i]);
+        if (err != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace dense

@@ -29,7 +29,7 @@ int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; 
 template <class TE>
 cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *Wgu, const void *Wd, const void *add,
                     int64_t ld_add, int64_t T, int H, int I, int act, void *gu, void *h, void *out, int64_t ld_out,
-                    float *part, cudaStream_t st)
+                    cudaStream_t st)
 {
     Args gated = base, down = base;
     gated.act = act, gated.h = h, gated.gu = gu;
@@ -37,17 +37,17 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     Product &q = product(down, T, H, I, 0, h, I, Wd, I);
     q.d = out, q.ld_d = ld_out, q.add = add, q.ld_add = ld_add;
     const bool few = T <= kFewMost;
-    const cudaError_t err = few ? launch_few<kGated, TE>(gated, false, st) : launch<kGated, TE>(gated, part, st);
+    const cudaError_t err = few ? launch_few<kGated, TE>(gated, false, st) : launch<kGated, TE>(gated, st);
     if (err != cudaSuccess)
         return err;
     // (the kernel before it waits for whatever wrote W_down, and lets this one start only then)
-    return few ? launch_few<kStore, TE>(down, true, st) : launch<kStore, TE>(down, part, st);
+    return few ? launch_few<kStore, TE>(down, true, st) : launch<kStore, TE>(down, st);
 }
 
 template <class TE>
 cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *Wgu, const void *Wd, const void *gu,
                      const void *h, const void *dout, int64_t ld_dout, int64_t T, int H, int I, int act, void *dx,
-                     int64_t ld_dx, bool f32, bool accumulate, void *dWgu, void *dWd, void *dgu, float *part,
+                     int64_t ld_dx, bool f32, bool accumulate, void *dWgu, void *dWd, void *dgu,
                      cudaStream_t st)
 {
     const int64_t I2 = 2 * (int64_t)I;
@@ -55,7 +55,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         Args a = base;
         a.act = act, a.gu = const_cast<void *>(gu), a.dgu = dgu;
         product(a, T, I, H, 1, dout, ld_dout, Wd, I);
-        const cudaError_t err = launch<kGatedBwd, TE>(a, part, st);
+        const cudaError_t err = launch<kGatedBwd, TE>(a, st);
         if (err != cudaSuccess)
             return err;
     }
@@ -73,7 +73,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         wgrad(product(a, I2, H, (int)T, 2, dgu, I2, x, ld_x), dWgu);
     if (dWd)
         wgrad(product(a, H, I, (int)T, 2, dout, ld_dout, h, I), dWd);
-    return a.n ? launch<kStore, TE>(a, part, st) : cudaSuccess;
+    return a.n ? launch<kStore, TE>(a, st) : cudaSuccess;
 }
 
 }  // namespace
@@ -87,7 +87,7 @@ size_t moe_ffn_workspace_size(int64_t T, int H, int I, int training)
 {
     if (T < 0 || H <= 0 || I <= 0 || training < 0 || training > 1 || bad_sizes(T, H, I))
         return 0;
-    return (size_t)(kHead + (int64_t)kPartBytes + up1k(T * I * 2 * (training ? 2 : 1)));
+    return (size_t)(kHead + up1k(T * I * 2 * (training ? 2 : 1)));
 }
 
 int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
@@ -103,19 +103,18 @@ int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_ga
     if (row_type == MOE_ROW_FP32 || bad_sizes(T, H, I) || ld_x % 8 != 0 || ld_out % 8 != 0 ||
         (add && ld_add % 8 != 0) || ld_x > 1ll << 36 || ld_out > 1ll << 36 || ld_add > 1ll << 36)
         return MOE_ERR_UNSUPPORTED;
-    if (ws_bytes < kHead + kPartBytes + (h ? 0 : (size_t)up1k(T * I * 2)))
+    if (ws_bytes < kHead + (h ? 0 : (size_t)up1k(T * I * 2)))
         return MOE_ERR_WORKSPACE;
     if (T == 0)
         return MOE_OK;
     uint8_t *at = static_cast<uint8_t *>(ws);
     Args base = {};
     base.status = reinterpret_cast<int *>(at);
-    float *part = reinterpret_cast<float *>(at + kHead);
     if (!h)
-        h = at + kHead + kPartBytes;
+        h = at + kHead;
     const auto st = static_cast<cudaStream_t>(stream);
     const auto go = row_type == MOE_ROW_BF16 ? forward<__nv_bfloat16> : forward<__half>;
-    return to_status(go(base, x, ld_x, W_gate_up, W_down, add, ld_add, T, H, I, act, gu, h, out, ld_out, part, st));
+    return to_status(go(base, x, ld_x, W_gate_up, W_down, add, ld_add, T, H, I, act, gu, h, out, ld_out, st));
 }
 
 int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
@@ -148,11 +147,10 @@ int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const v
     uint8_t *at = static_cast<uint8_t *>(ws);
     Args base = {};
     base.status = reinterpret_cast<int *>(at);
-    float *part = reinterpret_cast<float *>(at + kHead);
-    void *dgu = at + kHead + kPartBytes;
+    void *dgu = at + kHead;
     const auto go = row_type == MOE_ROW_BF16 ? backward<__nv_bfloat16> : backward<__half>;
     return to_status(go(base, x, ld_x, W_gate_up, W_down, gu, h, dout, ld_dout, T, H, I, act, dx, ld_dx,
-                        grad_type == MOE_ROW_FP32, accumulate != 0, dW_gate_up, dW_down, dgu, part, st));
+                        grad_type == MOE_ROW_FP32, accumulate != 0, dW_gate_up, dW_down, dgu, st));
 }
 
 }  // extern "C"

@@ -128,12 +128,11 @@ struct Forward {
     }
 };
 struct Backward {
-    int64_t part, dl, rows, sum, total;
+    int64_t dl, rows, sum, total;
     Backward(int64_t T, int H, int V, int piece)
     {
         const int64_t pitch = up64(piece < V ? piece : V);
-        part = kHead;
-        dl = part + (int64_t)kPartBytes;
+        dl = kHead;
         rows = dl + up1k(T * pitch * 2);
         sum = rows + up1k(T * H * 2);
         total = sum + (piece < V ? up1k(T * H * 4) : 0);
@@ -148,7 +147,7 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     product(a, T, V, H, 0, x, ld_x, W, H);
     a.V = V;
     a.targets = targets, a.stats = stats, a.target_logit = own;
-    const cudaError_t err = T <= kFewMost ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, nullptr, st);
+    const cudaError_t err = T <= kFewMost ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, st);
     if (err != cudaSuccess)
         return err;
     return launch_kernel(true, finish_kernel, dim3((unsigned)((T + 7) / 8)), dim3(256), 0, st, (const float2 *)stats,
@@ -162,7 +161,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
 {
     const Backward L(T, H, V, piece);
     float *factor = reinterpret_cast<float *>(ws + 64);
-    float *part = reinterpret_cast<float *>(ws + L.part), *sum = reinterpret_cast<float *>(ws + L.sum);
+    float *sum = reinterpret_cast<float *>(ws + L.sum);
     void *dl = ws + L.dl;
     const int64_t pitch = up64(piece < V ? piece : V);
     cudaError_t err = launch_kernel(true, factor_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, factor);
@@ -184,7 +183,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         Product &p = product(a, T, n, H, 0, x, ld_x, Wp, H);
         a.targets = targets, a.lse = lse, a.dloss = dloss, a.dscale = factor, a.v0 = (int)v0, a.V = V;
         p.d = dl, p.ld_d = pitch;
-        if ((err = launch<kDlogits, TE>(a, nullptr, st)) != cudaSuccess)
+        if ((err = launch<kDlogits, TE>(a, st)) != cudaSuccess)
             return err;
         a = base;
         if (dx) {  // the sum over the pieces, scaled back and rounded with the last one
@@ -201,7 +200,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
             if (accumulate)
                 q.add = q.d, q.ld_add = H;
         }
-        if (a.n && (err = launch<kStore, TE>(a, part, st)) != cudaSuccess)
+        if (a.n && (err = launch<kStore, TE>(a, st)) != cudaSuccess)
             return err;
     }
     return err;
