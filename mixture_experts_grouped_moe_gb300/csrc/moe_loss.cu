@@ -64,15 +64,27 @@ __global__ void __launch_bounds__(256) finish_kernel(const float2 *stats, const 
     }
 }
 
-// The factor of dl: a power of two, from the largest finite |dloss| of the rows that count.  One block.
-__global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, const int32_t *targets, int64_t T, int V,
-                                                      float *factor)
+// What the backward needs before its products.  Block 0: the factor of dl, a power of two, from the largest finite
+// |dloss| of the rows that count.  The others: x with zeros in the rows left out, so that whatever they hold (padding
+// may be a NaN) adds nothing to dW.
+__global__ void __launch_bounds__(512) prepare_kernel(const float *dloss, const int32_t *targets, int64_t T, int V,
+                                                      float *factor, const uint4 *x, int64_t ld, int pieces,
+                                                      uint4 *out)
 {
-    __shared__ float most[32];
+    __shared__ float most[16];
     pdl_wait();
     pdl_trigger();
+    if (blockIdx.x > 0) {
+        for (int64_t row = blockIdx.x - 1; row < T; row += gridDim.x - 1) {
+            const int t = targets[row];
+            const bool counts = t >= 0 && t < V;
+            for (int i = threadIdx.x; i < pieces; i += 512)
+                out[row * pieces + i] = counts ? x[row * ld + i] : make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
     float m = 0.0f;
-    for (int64_t i = threadIdx.x; i < T; i += 1024) {
+    for (int64_t i = threadIdx.x; i < T; i += 512) {
         const int t = targets[i];
         const float v = fabsf(dloss[i]);
         if (t >= 0 && t < V && v <= 3.4028235e38f)  // (not a NaN or an infinity)
@@ -85,27 +97,13 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, const 
         most[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < 32; ++i)
+        for (int i = 1; i < 16; ++i)
             m = fmaxf(m, most[i]);
         // 2^(14 - e) with m in [2^e, 2^(e+1)); both it and its inverse stay normal numbers
         int e = m > 0.0f ? ilogbf(m) : 0;
         e = e < -100 ? -100 : e;
         factor[0] = ldexpf(1.0f, 14 - e);
         factor[1] = ldexpf(1.0f, e - 14);
-    }
-}
-
-// x with zeros in the rows left out, so that whatever they hold (padding may be a NaN) adds nothing to dW.
-__global__ void __launch_bounds__(256) kept_rows_kernel(const uint4 *x, int64_t ld, const int32_t *targets, int64_t T,
-                                                        int pieces, int V, uint4 *out)
-{
-    pdl_wait();
-    pdl_trigger();
-    for (int64_t row = blockIdx.x; row < T; row += gridDim.x) {
-        const int t = targets[row];
-        const bool counts = t >= 0 && t < V;
-        for (int i = threadIdx.x; i < pieces; i += 256)
-            out[row * pieces + i] = counts ? x[row * ld + i] : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -164,17 +162,13 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
     float *sum = reinterpret_cast<float *>(ws + L.sum);
     void *dl = ws + L.dl;
     const int64_t pitch = up64(piece < V ? piece : V);
-    cudaError_t err = launch_kernel(true, factor_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, factor);
+    // (152 SMs x 4 blocks for the rows; dx alone reads x as it is)
+    const int64_t blocks = !dW ? 0 : T < 608 ? T : 608;
+    cudaError_t err = launch_kernel(true, prepare_kernel, dim3((unsigned)(1 + blocks)), dim3(512), 0, st, dloss, targets,
+                                    T, V, factor, static_cast<const uint4 *>(x), ld_x / 8, H / 8,
+                                    reinterpret_cast<uint4 *>(ws + L.rows));
     if (err != cudaSuccess)
         return err;
-    if (dW) {
-        const int64_t blocks = T < 1216 ? T : 1216;  // 152 SMs x 8 blocks
-        err = launch_kernel(true, kept_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, st,
-                            static_cast<const uint4 *>(x), ld_x / 8, targets, T, H / 8, V,
-                            reinterpret_cast<uint4 *>(ws + L.rows));
-        if (err != cudaSuccess)
-            return err;
-    }
     const int es = f32 ? 4 : 2;
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         const int n = (int)(V - v0 < piece ? V - v0 : piece);

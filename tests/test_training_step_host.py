@@ -46,17 +46,17 @@ def test_ffn(moe):
         (dict(h=None), INVALID), (dict(h=P + 8), INVALID), (dict(ws=P + 8), INVALID), (dict(wsb=64), WORKSPACE),
         (dict(ld=1 << 40), UNSUPPORTED)])
     need = moe.moe_ffn_workspace_size(100, 64, 32)
-    lib_call = dict(good, T=100, h=None, gu=None, wsb=need - 1)
-    assert lib.moe_ffn(*lib_call.values()) == WORKSPACE
+    assert lib.moe_ffn(*dict(good, T=100, h=None, gu=None, wsb=need - 1).values()) == WORKSPACE
     bwd = dict(t=0, act=0, x=P, ld=64, wgu=P, wd=P, gu=P, h=P, d=P, ld_d=64, T=0, H=64, I=32, dx=P, ld_dx=64, gt=0,
                acc=1, dwgu=P, dwd=P, ws=P, wsb=1 << 30, st=None)
     assert lib.moe_ffn_backward(*bwd.values()) == 0
     assert lib.moe_ffn_backward(*dict(bwd, gt=2, dx=None, ld_dx=0, dwgu=None, dwd=None).values()) == 0
+    assert lib.moe_ffn_backward(*dict(bwd, T=100, wsb=moe.moe_ffn_workspace_size(100, 64, 32, True) - 1).values()) == WORKSPACE
     refused(lib.moe_ffn_backward, bwd, [
         (dict(gt=1), INVALID), (dict(t=2, gt=2), UNSUPPORTED), (dict(acc=2), INVALID), (dict(gu=None), INVALID),
         (dict(h=None), INVALID), (dict(d=None), INVALID), (dict(ld_d=8), INVALID), (dict(ld_d=68), UNSUPPORTED),
         (dict(ld_dx=8), INVALID), (dict(ld_dx=68), UNSUPPORTED), (dict(dwd=P + 8), INVALID), (dict(dwgu=P + 4), INVALID),
-        (dict(wsb=1024), WORKSPACE), (dict(I=7), UNSUPPORTED), (dict(T=-1), INVALID)])
+        (dict(wsb=512), WORKSPACE), (dict(I=7), UNSUPPORTED), (dict(T=-1), INVALID)])
     assert moe.moe_ffn_workspace_size(8, 64, 32, True) > moe.moe_ffn_workspace_size(8, 64, 32) - 1 > 0
     for bad in ((-1, 64, 32), (8, 0, 32), (8, 60, 32), (8, 64, 33)):
         assert moe.moe_ffn_workspace_size(*bad) == 0
@@ -79,7 +79,9 @@ def test_vocab_loss(moe):
     refused(lib.moe_vocab_loss_backward, bwd, [
         (dict(piece=0), INVALID), (dict(piece=-64), INVALID), (dict(piece=100), UNSUPPORTED), (dict(gt=1), INVALID),
         (dict(acc=-1), INVALID), (dict(dl=None), INVALID), (dict(lse=None), INVALID), (dict(ld_dx=63), INVALID),
-        (dict(ld_dx=65), UNSUPPORTED), (dict(dx=P + 8), INVALID), (dict(dW=P + 8), INVALID), (dict(wsb=1 << 20), WORKSPACE)])
+        (dict(ld_dx=65), UNSUPPORTED), (dict(dx=P + 8), INVALID), (dict(dW=P + 8), INVALID), (dict(wsb=512), WORKSPACE)])
+    need = moe.moe_vocab_loss_workspace_size(100, 64, 1000, 512)
+    assert lib.moe_vocab_loss_backward(*dict(bwd, T=100, wsb=need - 1).values()) == WORKSPACE
     assert 0 < moe.moe_vocab_loss_workspace_size(8, 64, 100) < moe.moe_vocab_loss_workspace_size(8, 64, 100, 64)
     for bad in ((-1, 64, 100), (8, 65, 100), (8, 64, 0), (8, 64, 100, 65), (8, 64, 100, -64)):
         assert moe.moe_vocab_loss_workspace_size(*bad) == 0
