@@ -119,6 +119,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         }
     } else if (warp == 1) {
         if (lane == 0) {
+            // (the tokens come after this wait: the limit of the waits below counts from here, not from a start that
+            // may be long before the end of what precedes the kernel)
+            pdl_wait();
             const uint32_t type = std::is_same<TE, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t idesc = make_idesc(type, type, 128, NP);
             int s = 0;

@@ -522,17 +522,19 @@ def moe_clip_workspace_size(n) -> int:
 
 
 def _addresses(tensors):
-    return array.array("Q", [t.data_ptr() for t in tensors])
+    import torch
+    return array.array("Q", map(torch.Tensor.data_ptr, tensors))
 
 
 def _tensor_table(tensors):
     """The C arrays (types, numbers of elements, addresses) of contiguous tensors."""
-    # (arrays of the module array instead of ctypes: 60 tensors 40 -> 17 us of host time)
-    get = _row_types.get
-    types = [get(t.dtype) for t in tensors]
+    # (arrays of the module array instead of ctypes, filled by map: 60 small tensors clipped in 54 -> 33 us, all of
+    # it the host's time)
+    import torch
+    types = list(map(_row_types.get, [t.dtype for t in tensors]))
     if None in types:
         types = [_row_type(t.dtype) for t in tensors]
-    return array.array("i", types), array.array("q", [t.numel() for t in tensors]), _addresses(tensors)
+    return (array.array("i", types), array.array("q", map(torch.Tensor.numel, tensors)), _addresses(tensors))
 
 
 def _at(table):
@@ -1232,9 +1234,17 @@ class GradientClip:
         for i, (g, t) in enumerate(zip(grads, to)):
             if t is not g:
                 _expect(f"out[{i}]", t, g.shape, g.dtype)
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in to if t.numel())
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("tensors to write overlap: each would be scaled more than once")
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+        spans = [(*span(t), True) for t in to if t.numel()]
+        if to is not grads:  # (what is only read may be listed twice)
+            spans += [(*span(g), False) for g, t in zip(grads, to) if g.numel() and g.data_ptr() != t.data_ptr()]
+        written = any_end = 0  # ends of the furthest tensor to write, and of all
+        for start, end, writes in sorted(spans):
+            if start < (any_end if writes else written):
+                raise ValueError("a tensor to write overlaps another one: it would be scaled more than once, or read "
+                                 "after it was written")
+            any_end = max(any_end, end)
+            written = max(written, end) if writes else written
         tensors = {f"grads[{i}]": t for i, t in enumerate(grads)}
         if to is not grads:
             tensors.update({f"out[{i}]": t for i, t in enumerate(to)})

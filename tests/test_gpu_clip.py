@@ -122,3 +122,15 @@ def test_replayed_graph(moe):
         n2 = moe.GradientClip(1.0).clip(want)
         torch.cuda.synchronize()
         assert torch.equal(norm, n2) and all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_a_gradient_listed_twice(moe):
+    """Read twice and written to two places it counts twice in the norm; in place it is refused (on the host)."""
+    g = tensors([5000], ["fp32"], 14)[0]
+    out = [torch.empty_like(g) for _ in range(2)]
+    norm = moe.GradientClip(1.0).clip([g, g], out)
+    want = tr.norm([g, g])
+    tr.bounded(norm, want.reshape(1), want.reshape(1) * NORM, "norm")
+    assert torch.equal(out[0], out[1])
+    with pytest.raises(ValueError):
+        moe.GradientClip(1.0).clip([g, g])

@@ -150,7 +150,8 @@ def test_objects(moe):
             call()
     c = moe.GradientClip(1.0, n=2, device="cpu")
     for call in (lambda: c.clip([d, d, d]), lambda: c.norm([z(4, 4).t()[:, :2]]), lambda: c.clip([d, d]),
-                 lambda: c.clip([d[:3], d[2:]]), lambda: c.clip([d], [d, d]), lambda: c.clip([d], [z(3, dt=torch.float32)]),
+                 lambda: c.clip([d[:3], d[2:]]), lambda: c.clip([d[:2], d[2:]], [d[2:], d[:2]]),
+                 lambda: c.clip([d[:2], d[1:3]], [d[1:3], z(2, dt=torch.float32)]), lambda: c.clip([d], [d, d]), lambda: c.clip([d], [z(3, dt=torch.float32)]),
                  lambda: c.norm([d]), lambda: c.clip([d]), lambda: moe.GradientClip(-1.0, device="cpu"),
                  lambda: moe.GradientClip(1.0, eps=float("nan"), device="cpu"),
                  lambda: moe.GradientClip(1.0, n=1 << 20, device="cpu")):
