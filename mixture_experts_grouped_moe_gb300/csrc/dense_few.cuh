@@ -15,7 +15,11 @@
 namespace moe {
 namespace dense {
 
-constexpr int kFewMost = 128;  // tokens
+// The most tokens that go this way (us here / by pair tiles: 80 tokens through 4096 x 14336 82 / 94, through 1024 x
+// 4096 16.4 / 22.0, 128 through 7168 x 2048 29.2 / 39.8).  Logits up to 32: their epilogue takes a warp a token
+// (4096 x 32000: 16 rows 49, 64 rows 62 / 55, 128 rows 107 / 54).
+template <int MODE>
+constexpr int64_t kFewMost = MODE == kLse ? 32 : 128;
 constexpr int kFewThreads = 192;
 
 template <int NP>
@@ -326,15 +330,15 @@ cudaError_t launch_few_np(Args &a, bool early, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kern, a, early ? 1 : 0);
 }
 
-// The product p[0] of M <= kFewMost tokens (A) with weights (B).
+// The product p[0] of M <= kFewMost<MODE> tokens (A) with weights (B).
 template <int MODE, class TE>
 cudaError_t launch_few(Args &a, bool early, cudaStream_t st)
 {
     const int64_t T = a.p[0].M;
-    return T <= 16   ? launch_few_np<MODE, TE, 16>(a, early, st)
-           : T <= 32 ? launch_few_np<MODE, TE, 32>(a, early, st)
-           : T <= 64 ? launch_few_np<MODE, TE, 64>(a, early, st)
-                     : launch_few_np<MODE, TE, 128>(a, early, st);
+    if constexpr (kFewMost<MODE> > 32)
+        if (T > 32)
+            return T <= 64 ? launch_few_np<MODE, TE, 64>(a, early, st) : launch_few_np<MODE, TE, 128>(a, early, st);
+    return T <= 16 ? launch_few_np<MODE, TE, 16>(a, early, st) : launch_few_np<MODE, TE, 32>(a, early, st);
 }
 
 }  // namespace dense

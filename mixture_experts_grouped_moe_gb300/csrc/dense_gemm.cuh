@@ -414,50 +414,74 @@ __device__ __forceinline__ float exp2_fast(float v)
     return r;
 }
 
-// One more 32 columns of a row's running maximum m and sum s of exp(v - m).  Columns past N count as -inf.
-__device__ __forceinline__ void epi_lse(int N, int col, int target, float (&v)[32], float &m, float &s, float &own,
+// One more W columns of a row's running maximum m and sum s of exp(v - m).  Columns past N count as -inf.
+template <int W>
+__device__ __forceinline__ void epi_lse(int N, int col, int target, float (&v)[W], float &m, float &s, float &own,
                                         bool &has)
 {
-    if (col + 32 > N) {
+    if (col + W > N) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < W; ++i)
             if (col + i >= N)
                 v[i] = -INFINITY;
     }
     const int at = target - col;
-    if (at >= 0 && at < 32) {
+    if (at >= 0 && at < W) {
         has = true;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < W; ++i)
             if (i == at)
                 own = v[i];
     }
     float top = v[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i)
+    for (int i = 1; i < W; ++i)
         top = fmaxf(top, v[i]);
     const float was = m;
     m = fmaxf(m, top);
     const float base = m == -INFINITY ? 0.0f : m * kLog2e;  // (nothing but -inf so far: every term is 0)
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < W; ++i)
         part[i & 3] += exp2_fast(fmaf(v[i], kLog2e, -base));
     s = fmaf(s, exp2_fast(fmaf(was, kLog2e, -base)), (part[0] + part[1]) + (part[2] + part[3]));
 }
 
-// factor (softmax - one at the target), 32 columns.
-__device__ __forceinline__ void epi_dlogits(int col, int target, float lse, float factor, float (&v)[32])
+// factor (softmax - one at the target), W columns.
+template <int W>
+__device__ __forceinline__ void epi_dlogits(int col, int target, float lse, float factor, float (&v)[W])
 {
     const float base = lse * kLog2e;
     const int at = target - col;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < W; ++i) {
         float p = exp2_fast(fmaf(v[i], kLog2e, -base));
         if (i == at)
             p -= 1.0f;
         v[i] = factor == 0.0f ? 0.0f : factor * p;  // (a row left out adds nothing, whatever its logits)
     }
+}
+
+// What the logits' epilogues know of a row: its target's column in the piece (-1: none, or left out), lse and the
+// factor of its gradient.
+struct RowOf {
+    int target;
+    float lse, factor;
+};
+template <int MODE>
+__device__ __forceinline__ RowOf row_of(const Args &a, int64_t row)
+{
+    RowOf r = {-1, 0.0f, 0.0f};
+    if (row < a.p[0].M) {
+        const int t = a.targets[row];
+        const bool counts = t >= 0 && t < a.V;
+        if (MODE == kDlogits) {
+            r.lse = a.lse[row];
+            r.factor = counts ? a.dloss[row] * a.dscale[0] : 0.0f;
+        }
+        r.target = counts ? t - a.v0 : -1;
+    }
+    return r;
 }
 
 // -------------------------------------------------------------- the tiles
@@ -493,10 +517,6 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t, int s)
 // Columns of D that a tile covers.
 template <int MODE, int NT>
 constexpr int kCols = MODE == kGated ? NT / 2 : NT;
-
-// Modes whose tiles may be split (the others' tiles, of a vocabulary, are many).
-template <int MODE>
-constexpr bool kSplits = MODE == kStore || MODE == kGated || MODE == kGatedBwd;
 
 // The parts of a split tile's accumulator to the pairs that own their columns, and the owners' epilogue.  All
 // threads of the cluster.  buf: [S sources][columns / 4][128 rows] of four columns, so that neighbouring threads
@@ -549,6 +569,11 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
             }
         }
     };
+    RowOf of = {};
+    if (MODE == kLse || MODE == kDlogits)
+        of = row_of<MODE>(a, row);
+    float top = -INFINITY, exps = 0.0f, target_logit = 0.0f;
+    bool has = false;
 #pragma unroll 1
     for (int c = 0; c < mine && col + c < p.N; c += 16) {
         float v[16];
@@ -559,9 +584,23 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
             epi_gated<TE>(a, row, col + c, v, u);
         } else if constexpr (MODE == kStore) {
             epi_store<TE>(p, row, col + c, v);
-        } else {
+        } else if constexpr (MODE == kGatedBwd) {
             epi_gated_bwd<TE>(a, row, col + c, v);
+        } else if constexpr (MODE == kLse) {
+            epi_lse(p.N, col + c, of.target, v, top, exps, target_logit, has);
+        } else {
+            epi_dlogits(col + c, of.target, of.lse, of.factor, v);
+            TE *dst = static_cast<TE *>(p.d) + row * p.ld_d + col + c;  // (8 columns may go past N, into the padding)
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+                if (col + c + i < p.N)
+                    store8(dst + i, v + i);
         }
+    }
+    if (MODE == kLse) {
+        a.stats[row * a.pairs + (tile.nt * S + pair) * 2 + half] = make_float2(top, exps);
+        if (has)
+            a.target_logit[row] = target_logit;
     }
 }
 
@@ -751,17 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 for (int c = 0; c < kMine && c0 + c < p.N; c += 128 / es)
                     prefetch_l2(add + c * es);
             }
-            int target = -1;
-            float lse = 0.0f, factor = 0.0f;
-            if ((MODE == kLse || MODE == kDlogits) && live) {
-                target = a.targets[row];
-                const bool counts = target >= 0 && target < a.V;
-                if (MODE == kDlogits) {
-                    lse = a.lse[row];
-                    factor = counts ? a.dloss[row] * a.dscale[0] : 0.0f;
-                }
-                target = counts ? target - a.v0 : -1;
-            }
+            RowOf of = {};
+            if (MODE == kLse || MODE == kDlogits)
+                of = row_of<MODE>(a, row);
             uint4 *buf = reinterpret_cast<uint4 *>(sm.rows[warp - 2]);
             const int64_t row0 = tile.m0 + rank * 128 + q * 32;  // the warp's rows
             const int rows = (int)max((int64_t)0, min((int64_t)32, p.M - row0));
@@ -871,9 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     Rows<TE>::store(buf, wg, out, 2 * (int64_t)p.N, rows, cols, lane);
                     Rows<TE>::store(buf, wu, out + p.N, 2 * (int64_t)p.N, rows, cols, lane);
                 } else if constexpr (MODE == kLse) {
-                    epi_lse(p.N, col, target, v, m, s, own, has);
+                    epi_lse(p.N, col, of.target, v, m, s, own, has);
                 } else {
-                    epi_dlogits(col, target, lse, factor, v);
+                    epi_dlogits(col, of.target, of.lse, of.factor, v);
                     // (a last piece of 8 columns may go past N, into the rows' padding)
                     put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + col, p.ld_d, rows, cols, lane);
                 }
@@ -894,16 +925,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
     }
 
-    if constexpr (kSplits<MODE>) {
-        if (S > 1) {
-            // every MMA of the cluster has read its stages (the pair's accumulator is complete: what the epilogue
-            // warps waited for)
-            __syncwarp();
-            tc_fence_before();
-            cluster_sync();
-            tc_fence_after();
-            meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
-        }
+    if (S > 1) {
+        // every MMA of the cluster has read its stages (the pair's accumulator is complete: what the epilogue warps
+        // waited for)
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync();
+        tc_fence_after();
+        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
     }
     // both CTAs stay until the pair's last MMA, copy and remote arrive are done
     __syncwarp();
@@ -1001,7 +1030,7 @@ cudaError_t launch_nt(Args &a, int S, int clusters, cudaStream_t st)
     }
     a.tiles = (int)tiles;
     a.S = S;
-    a.pairs = a.p[0].tiles_n * 2;
+    a.pairs = a.p[0].tiles_n * S * 2;
     const cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>);
     if (err != cudaSuccess)
@@ -1034,6 +1063,8 @@ inline int64_t longest_share(const Product *p, int n, int cols, int S, int clust
     return most;
 }
 
+constexpr int kMostSplit = 38;  // tiles that may be split: clusters of four CTAs that 152 SMs hold
+
 struct Plan {
     int64_t cost;  // in 10 ns
     int S;
@@ -1052,13 +1083,13 @@ Plan plan(const Product *p, int n, const int *clusters)
     for (int w = MODE == kLse ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
         const int cols = (w ? 256 : 128) / (MODE == kGated ? 2 : 1);
         // (a warp of an owner finishes 16 columns at least, of each side)
-        const int most = !kSplits<MODE> ? 1 : MODE == kGated && !w ? 2 : 4;
+        const int most = MODE == kGated && !w ? 2 : 4;
         for (int s = 1; s <= most && (s == 1 || (clusters[s] > 0 && (least + 63) / 64 / s >= 2)); s *= 2) {
             // (clusters that share a tile take one each: with more tiles than clusters they would start in turns)
             int64_t tiles = 0;
             for (int i = 0; i < n; ++i)
                 tiles += (p[i].M + 255) / 256 * ((p[i].N + cols - 1) / cols);
-            if (s > 1 && tiles > clusters[s])
+            if (s > 1 && (tiles > clusters[s] || tiles > kMostSplit))
                 continue;
             const int64_t c = longest_share(p, n, cols, s, clusters[s]) * (w ? 29 : 22) + (w ? 250 : 150) +
                               (s > 1 ? 230 : 0) + 450;

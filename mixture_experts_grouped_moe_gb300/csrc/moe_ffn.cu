@@ -36,7 +36,7 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     product(gated, T, I, H, 0, x, ld_x, Wgu, H);
     Product &q = product(down, T, H, I, 0, h, I, Wd, I);
     q.d = out, q.ld_d = ld_out, q.add = add, q.ld_add = ld_add;
-    const bool few = T <= kFewMost;
+    const bool few = T <= kFewMost<kGated>;
     const cudaError_t err = few ? launch_few<kGated, TE>(gated, false, st) : launch<kGated, TE>(gated, st);
     if (err != cudaSuccess)
         return err;

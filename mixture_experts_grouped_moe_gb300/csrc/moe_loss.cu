@@ -109,10 +109,12 @@ __global__ void __launch_bounds__(512) prepare_kernel(const float *dloss, const 
 
 bool bad_sizes(int64_t T, int H, int V) { return H % 8 != 0 || H > 1 << 20 || V > 1 << 24 || T > 1 << 30; }
 
-// (maximum, sum) pairs that the forward may keep of a row: one for each part of a tile's rows, or two a tile
+// (maximum, sum) pairs that the forward may keep of a row: one for each part of a tile's rows (few rows), or two a
+// tile, times the pairs of CTAs that share it (4 at most, and only while all tiles' clusters are resident).
 int64_t pairs_of(int64_t T, int V)
 {
-    return T <= kFewMost ? ((int64_t)V + 127) / 128 * 8 : ((int64_t)V + 255) / 256 * 2;
+    const int64_t tiles = ((int64_t)V + 255) / 256;
+    return T <= kFewMost<kLse> ? ((int64_t)V + 127) / 128 * 8 : tiles * (tiles <= kMostSplit ? 8 : 2);
 }
 
 // Byte offsets of the workspace (forward: stats and target logits; backward: dl of a piece, kept rows, dx's sum).
@@ -145,7 +147,7 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     product(a, T, V, H, 0, x, ld_x, W, H);
     a.V = V;
     a.targets = targets, a.stats = stats, a.target_logit = own;
-    const cudaError_t err = T <= kFewMost ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, st);
+    const cudaError_t err = T <= kFewMost<kLse> ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, st);
     if (err != cudaSuccess)
         return err;
     return launch_kernel(true, finish_kernel, dim3((unsigned)((T + 7) / 8)), dim3(256), 0, st, (const float2 *)stats,

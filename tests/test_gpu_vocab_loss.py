@@ -8,9 +8,10 @@ import training_reference as tr
 
 pytestmark = pytest.mark.gpu
 
-# (T, H, V): one row and one word; vocabularies that end inside a tile and a block; pieces of 64 and more
+# (T, H, V): one row and one word; vocabularies that end inside a tile and a block; K long enough to be split over
+# pairs, with few rows and with more
 SIZES = [(1, 8, 1), (1, 64, 257), (3, 72, 1000), (16, 264, 4099), (127, 136, 255), (129, 64, 256), (256, 520, 513),
-         (300, 1000, 777), (520, 64, 3001)]
+         (300, 1000, 777), (520, 64, 3001), (33, 2048, 300), (64, 4096, 1100), (40, 1024, 129)]
 TYPE = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 
