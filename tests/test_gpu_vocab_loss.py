@@ -131,7 +131,8 @@ def test_large_logits(moe):
     x = x * 64
     f = moe.VocabularyLoss(T, H, V, training=True)
     loss = f.forward(x, w, targets)
-    tr.bounded(loss, tr.loss(x.double(), w.double(), targets)[0], tr.loss_bound(x.double(), w.double(), targets)[0], "loss")
+    d = x.double(), w.double(), targets
+    tr.bounded(loss, tr.loss(*d)[0], tr.loss_bound(*d)[0], "loss")
     g = f.backward(x, w, targets, dloss)
     assert all(v.isfinite().all() for v in g.values())
 

@@ -38,8 +38,9 @@ def test_ffn(moe):
     refused(lib.moe_ffn, good, [
         (dict(t=3), INVALID), (dict(t=-1), INVALID), (dict(t=2), UNSUPPORTED), (dict(act=3), INVALID),
         (dict(act=-1), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(I=0), INVALID),
-        (dict(H=60, ld=60), UNSUPPORTED), (dict(I=12), UNSUPPORTED), (dict(H=1 << 21, ld=1 << 21, ld_out=1 << 21, ld_add=1 << 21), UNSUPPORTED),
-        (dict(T=1 << 31), UNSUPPORTED), (dict(ld=56), INVALID), (dict(ld=68), UNSUPPORTED), (dict(ld_out=68), UNSUPPORTED),
+        (dict(H=60, ld=60), UNSUPPORTED), (dict(I=12), UNSUPPORTED),
+        (dict(H=1 << 21, ld=1 << 21, ld_out=1 << 21, ld_add=1 << 21), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED),
+        (dict(ld=56), INVALID), (dict(ld=68), UNSUPPORTED), (dict(ld_out=68), UNSUPPORTED),
         (dict(ld_add=63), INVALID), (dict(ld_add=65), UNSUPPORTED), (dict(ld_out=8), INVALID), (dict(x=None), INVALID),
         (dict(wgu=None), INVALID), (dict(wd=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
         (dict(x=P + 2), INVALID), (dict(wgu=P + 8), INVALID), (dict(add=P + 4), INVALID), (dict(out=P + 8), INVALID),
@@ -51,7 +52,8 @@ def test_ffn(moe):
                acc=1, dwgu=P, dwd=P, ws=P, wsb=1 << 30, st=None)
     assert lib.moe_ffn_backward(*bwd.values()) == 0
     assert lib.moe_ffn_backward(*dict(bwd, gt=2, dx=None, ld_dx=0, dwgu=None, dwd=None).values()) == 0
-    assert lib.moe_ffn_backward(*dict(bwd, T=100, wsb=moe.moe_ffn_workspace_size(100, 64, 32, True) - 1).values()) == WORKSPACE
+    need = moe.moe_ffn_workspace_size(100, 64, 32, True)
+    assert lib.moe_ffn_backward(*dict(bwd, T=100, wsb=need - 1).values()) == WORKSPACE
     refused(lib.moe_ffn_backward, bwd, [
         (dict(gt=1), INVALID), (dict(t=2, gt=2), UNSUPPORTED), (dict(acc=2), INVALID), (dict(gu=None), INVALID),
         (dict(h=None), INVALID), (dict(d=None), INVALID), (dict(ld_d=8), INVALID), (dict(ld_d=68), UNSUPPORTED),
@@ -100,7 +102,8 @@ def test_clip(moe):
            (dict(numel=arr(ctypes.c_int64, 3, 1 << 41)), UNSUPPORTED)]
     refused(lib.moe_clip_gradients, good, bad + [
         (dict(out=None), INVALID), (dict(out=arr(ctypes.c_void_p, P, None)), INVALID), (dict(max_norm=-1.0), INVALID),
-        (dict(max_norm=float("nan")), INVALID), (dict(eps=-1.0), INVALID), (dict(out=arr(ctypes.c_void_p, P, P + 2)), INVALID)])
+        (dict(max_norm=float("nan")), INVALID), (dict(eps=-1.0), INVALID),
+        (dict(out=arr(ctypes.c_void_p, P, P + 2)), INVALID)])
     norm = {k: v for k, v in good.items() if k not in ("out", "max_norm", "eps")}
     refused(lib.moe_grad_norm, norm, bad)
 
@@ -149,10 +152,12 @@ def test_objects(moe):
         with pytest.raises(TypeError):
             call()
     c = moe.GradientClip(1.0, n=2, device="cpu")
-    for call in (lambda: c.clip([d, d, d]), lambda: c.norm([z(4, 4).t()[:, :2]]), lambda: c.clip([d, d]),
-                 lambda: c.clip([d[:3], d[2:]]), lambda: c.clip([d[:2], d[2:]], [d[2:], d[:2]]),
-                 lambda: c.clip([d[:2], d[1:3]], [d[1:3], z(2, dt=torch.float32)]), lambda: c.clip([d], [d, d]), lambda: c.clip([d], [z(3, dt=torch.float32)]),
-                 lambda: c.norm([d]), lambda: c.clip([d]), lambda: moe.GradientClip(-1.0, device="cpu"),
+    for call in (lambda: c.clip([d, d]), lambda: c.clip([d[:3], d[2:]]), lambda: c.clip([d[:2], d[2:]], [d[2:], d[:2]]),
+                 lambda: c.clip([d[:2], d[1:3]], [d[1:3], z(2, dt=torch.float32)])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    for call in (lambda: c.clip([d, d, d]), lambda: c.norm([z(4, 4).t()[:, :2]]), lambda: c.clip([d], [d, d]),
+                 lambda: c.clip([d], [z(3, dt=torch.float32)]), lambda: c.norm([d]), lambda: c.clip([d]), lambda: moe.GradientClip(-1.0, device="cpu"),
                  lambda: moe.GradientClip(1.0, eps=float("nan"), device="cpu"),
                  lambda: moe.GradientClip(1.0, n=1 << 20, device="cpu")):
         with pytest.raises(ValueError):

@@ -117,7 +117,8 @@ def loss_grads_bound(x, w, targets, dloss, t, grad_t, old=None):
     dl, g = loss_grads(x, w, targets, dloss)
     p = torch.softmax(x @ w.t(), 1)
     mag = x.abs() @ w.abs().t()
-    el = ACC * (mag + mag.amax(1, keepdim=True)) + 2.0 ** -17 + 2.0 ** -20 * ((x @ w.t()).abs().amax(1, keepdim=True) + 20)
+    top = (x @ w.t()).abs().amax(1, keepdim=True)
+    el = ACC * (mag + mag.amax(1, keepdim=True)) + 2.0 ** -17 + 2.0 ** -20 * (top + 20)
     ok = ((targets >= 0) & (targets < w.shape[0]))[:, None]
     # a power of two brings the largest factor to [2^14, 2^15): below, 16-bit steps are TINY of that scale
     most = dloss[ok[:, 0]].abs().max() if ok.any() else dloss.new_ones(())
@@ -143,4 +144,5 @@ def bounded(got, want, bound, label):
     """Every element within its bound, and none a NaN."""
     err = (got.double() - want).abs()
     worst = (err / bound).nan_to_num(nan=float("inf")).max() if err.numel() else torch.zeros(())
-    assert (err <= bound).all(), (label, f"worst error / bound {float(worst):.3g}", f"{int((~(err <= bound)).sum())} of {err.numel()}")
+    off = int((~(err <= bound)).sum())
+    assert not off, (label, f"worst error / bound {float(worst):.3g}", f"{off} of {err.numel()}")
