@@ -674,7 +674,9 @@ int moe_block_norm_backward(int row_type, const void *h, const void *residual, c
  * I are multiples of 8, and so are the pitches of rows.  T is any number, also
  * 0.  Each workspace starts with a status word that the caller zeroes once
  * before the first call; a call whose wait runs out leaves MOE_ERR_TIMEOUT in
- * it (read with moe_workspace_status).  Results are bitwise reproducible.
+ * it (read with moe_workspace_status).  A workspace serves one call at a time:
+ * calls that may overlap on the GPU need one each.  Results are bitwise
+ * reproducible.
  */
 #define MOE_ACT_SILU 0       /* g sigmoid(g) */
 #define MOE_ACT_GELU_TANH 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
