@@ -10,7 +10,7 @@
 // square loses is below 2^-149 and so nothing against the sum).  Everything above a thread's chunk is summed in 64
 // bits in a fixed order: results are bitwise reproducible.
 //
-// 5.6 GB of fp32 in 2.48 ms (6.8 TB/s, the copy rate), 134 MB in 74 us, 60 tensors of up to 6000 elements in 9.7.
+// 5.6 GB of fp32 in 2.48 ms (6.8 TB/s, the copy rate), 134 MB in 68 us, 60 tensors of up to 6000 elements in 9.7.
 #include "moe_internal.h"
 #include "rows.cuh"
 
@@ -22,6 +22,17 @@ constexpr int kLoads = 8;                              // 16-byte loads of a thr
 constexpr int kChunkBytes = kThreads * kLoads * 16;    // 32 KB
 constexpr int kMaxTensors = 512;                       // of one launch
 constexpr int kBlocks = 152 * 8;                       // most blocks of a launch
+constexpr int kResident = 152 * 2;                     // blocks that run at once
+
+// Blocks of a launch: those that run at once, or, where each of four times as many has 8 chunks or more, so many, which
+// even out unequal speeds (us with 304 / 1216: 67 MB fp32 35.2 / 44.3, 134 MB 67.7 / 74.0, 268 MB 130 / 132, 537 MB
+// 252 / 248, 4.3 GB 1922 / 1886).
+unsigned blocks_for(int64_t chunks)
+{
+    if (chunks >= 8 * kBlocks)
+        return kBlocks;
+    return (unsigned)(chunks < kResident ? (chunks ? chunks : 1) : kResident);
+}
 
 struct Tensors {
     int n;
@@ -284,14 +295,12 @@ int run(int n, const int *types, const void *const *g, void *const *out, bool sc
                   "one double for each block of each launch");
     double *part = static_cast<double *>(ws);
     Tensors t;
-    t.chunks = 0;
     int parts = 0;
-    const auto blocks = [&] { return (unsigned)(t.chunks < kBlocks ? (t.chunks ? t.chunks : 1) : kBlocks); };
     for (int from = 0; from < n; from += kMaxTensors) {
         collect(t, from, n - from < kMaxTensors ? n - from : kMaxTensors, types, g, out, numel);
-        if (launch_kernel(true, squares_kernel, dim3(blocks()), dim3(kThreads), 0, st, t, part + parts) != cudaSuccess)
+        if (launch_kernel(true, squares_kernel, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, st, t, part + parts) != cudaSuccess)
             return MOE_ERR_CUDA;
-        parts += (int)blocks();
+        parts += (int)blocks_for(t.chunks);
     }
     if (!scaled || n == 0)
         return launch_kernel(true, norm_kernel, dim3(1), dim3(kThreads), 0, st, (const double *)part, parts, norm) ==
@@ -300,7 +309,7 @@ int run(int n, const int *types, const void *const *g, void *const *out, bool sc
                    : MOE_ERR_CUDA;
     for (int from = (n - 1) / kMaxTensors * kMaxTensors; from >= 0; from -= kMaxTensors) {
         collect(t, from, n - from < kMaxTensors ? n - from : kMaxTensors, types, g, out, numel);
-        if (launch_kernel(true, scale_kernel, dim3(blocks()), dim3(kThreads), 0, st, t, (const double *)part, parts,
+        if (launch_kernel(true, scale_kernel, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, st, t, (const double *)part, parts,
                           max_norm, eps, norm) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
