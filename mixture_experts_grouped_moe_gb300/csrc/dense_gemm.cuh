@@ -11,8 +11,8 @@
 //
 // Roles (320 threads a CTA, one CTA an SM): warp 0 TMA producer, warp 1 issues the pair's MMAs (in the
 // leader), warps 2..9 the epilogue of the CTA's 128 rows (two warps a row, each half of the columns), which
-// overlaps the next tile's MMAs through a second accumulator.  Tiles are dealt round-robin (those of a product
-// cost the same); groups of 16 row tiles walk the columns together, so that 76 pairs in flight share about
+// overlaps the next tile's MMAs through a second accumulator.  Tiles are dealt to the clusters beforehand (those of a
+// product cost the same); groups of 16 row tiles walk the columns together, so that 76 pairs in flight share about
 // 16 x 5 tiles' rows through L2, where they are kept (evict-last).  Products that do not depend on one another (the
 // gradients of x and of the weights) go into one launch, longest K first: one start, one tail and one rounding up to
 // whole waves.
@@ -71,9 +71,35 @@ struct Product {
     int d_f32;
 };
 
+// Which tiles a cluster goes through.  The first product's (the longest K) are dealt round-robin.  Where its last
+// round leaves some clusters without one, those first get as many rounds of the others' tiles as take the same time;
+// the rest is dealt round-robin to all, from those clusters on.
+struct Deal {
+    int P;     // clusters
+    int n0;    // the first product's tiles: q whole rounds and r more
+    int q, r;
+    int E;     // rounds that the clusters from r on get ahead of the rest
+
+    // Tile k of cluster c; a number past the last tile when there is none (then there is none for any larger k).
+    __host__ __device__ int tile(int c, int k) const
+    {
+        const int mine = q + (c < r ? 1 : 0);
+        if (k < mine)
+            return k * P + c;
+        k -= mine;
+        if (c >= r) {
+            if (k < E)
+                return n0 + k * (P - r) + c - r;
+            k -= E;
+        }
+        return n0 + E * (P - r) + k * P + (c >= r ? c - r : c - r + P);
+    }
+};
+
 struct Args {
     Product p[kProducts];
     int n, tiles;
+    Deal deal;
     int S;                // pairs that share a tile's K, one cluster
     int *status;
     // gated
@@ -659,8 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     cluster_sync();  // both CTAs' barriers exist before any signal between them
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
-    // (S > 1: a tile a cluster)
-    const int first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
+    const int cluster = blockIdx.x / (2 * S), first = a.deal.tile(cluster, 0);
     {
         // the first tile's arithmetic before the wait: it brings the parameters it reads into the constant cache
         const Tile t = tile_of<MODE>(a, first, pair);
@@ -679,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int s = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < a.tiles; t += step) {
+            for (int t = first, k = 0; ok && t < a.tiles; t = a.deal.tile(cluster, ++k)) {
                 const Tile tile = tile_of<MODE>(a, t, pair);
                 const Product &p = a.p[tile.prod];
                 const int maj = MODE == kStore ? p.maj : MODE == kGatedBwd ? 1 : 0;
@@ -728,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, any = false;
-            for (int t = first; ok && t < a.tiles; t += step) {
+            for (int t = first, k = 0; ok && t < a.tiles; t = a.deal.tile(cluster, ++k)) {
                 const Tile tile = tile_of<MODE>(a, t, pair);
                 const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
                 const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
@@ -783,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int r = q * 32 + lane;
         int acc = 0;
         uint32_t aph = 0;
-        for (int t = first; t < a.tiles; t += step) {
+        for (int t = first, k = 0; t < a.tiles; t = a.deal.tile(cluster, ++k)) {
             const Tile tile = tile_of<MODE>(a, t, pair);
             const Product &p = a.p[tile.prod];
             const int64_t row = tile.m0 + rank * 128 + r;
@@ -1045,6 +1070,8 @@ cudaError_t launch_nt(Args &a, int S, int clusters, cudaStream_t st)
     }
     a.tiles = (int)tiles;
     a.S = S;
+    int64_t busiest;
+    a.deal = deal_of(a.p, a.n, kCols<MODE, NT>, S, S > 1 ? tiles : clusters, &busiest);
     a.pairs = a.p[0].tiles_n * S * 2;
     const cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NT>);
@@ -1052,30 +1079,43 @@ cudaError_t launch_nt(Args &a, int S, int clusters, cudaStream_t st)
         return err;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg =
-        config_of<MODE, TE, NT>(attr, S, S > 1 || tiles < clusters ? tiles : clusters, st);
+        config_of<MODE, TE, NT>(attr, S, a.deal.P, st);
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Blocks of K that the busiest of `clusters` clusters goes through when tiles of 256 rows x cols are dealt
-// round-robin, product after product: one of those at which a product starts.
-inline int64_t longest_share(const Product *p, int n, int cols, int S, int clusters)
+// Tiles of one product, and what one costs: its blocks of K, or its epilogue where that takes longer (one tile's
+// overlaps the next one's products).
+struct Load {
+    int64_t tiles, blocks;
+};
+inline Load load_of(const Product &p, int cols, int S)
 {
-    int64_t tiles[kProducts], blocks[kProducts], start[kProducts], before = 0, most = 0;
-    for (int i = 0; i < n; ++i) {
-        tiles[i] = (p[i].M + 255) / 256 * ((p[i].N + cols - 1) / cols);
-        blocks[i] = ((p[i].K + 63) / 64 + S - 1) / S;
-        start[i] = before % clusters;
-        before += tiles[i];
+    const int64_t KB = ((p.K + 63) / 64 + S - 1) / S, epilogue = cols > 128 ? 8 : 6;
+    return {(p.M + 255) / 256 * ((p.N + cols - 1) / cols), KB > epilogue ? KB : epilogue};
+}
+
+// The deal of n products over at most `clusters` clusters, and the blocks of K that the busiest goes through.
+inline Deal deal_of(const Product *p, int n, int cols, int S, int64_t clusters, int64_t *busiest)
+{
+    const Load first = load_of(p[0], cols, S);
+    int64_t others = 0, blocks = 0;
+    for (int i = 1; i < n; ++i) {
+        const Load l = load_of(p[i], cols, S);
+        others += l.tiles, blocks += l.tiles * l.blocks;
     }
-    for (int j = 0; j < n; ++j) {
-        int64_t share = 0;
-        for (int i = 0; i < n; ++i) {
-            const int64_t first = start[j] >= start[i] ? start[j] - start[i] : start[j] - start[i] + clusters;
-            share += (tiles[i] - first + clusters - 1) / clusters * blocks[i];
-        }
-        most = share > most ? share : most;
+    const int64_t P = first.tiles + others < clusters ? first.tiles + others : clusters;
+    const int64_t q = first.tiles / P, r = first.tiles % P;
+    int64_t E = 0;
+    if (r > 0 && others > 0) {
+        const int64_t same = first.blocks / load_of(p[1], cols, S).blocks, most = others / (P - r);
+        E = same < most ? same : most;
     }
-    return most;
+    const int64_t rest = others - E * (P - r), rounds = rest / P, more = rest % P;
+    const int64_t each = others ? (blocks + others - 1) / others : 0;
+    const int64_t with = r > 0 ? (q + 1) * first.blocks + (rounds + (more > P - r ? 1 : 0)) * each : 0;
+    const int64_t without = q * first.blocks + (E + rounds + (more > 0 ? 1 : 0)) * each;
+    *busiest = with > without ? with : without;
+    return {(int)P, (int)first.tiles, (int)q, (int)r, (int)E};
 }
 
 constexpr int kMostSplit = 38;  // tiles that may be split: clusters of four CTAs that 152 SMs hold
@@ -1109,8 +1149,9 @@ Plan plan(const Product *p, int n, const int *clusters)
                 tiles += (p[i].M + 255) / 256 * ((p[i].N + cols - 1) / cols);
             if (s > 1 && (tiles > clusters[s] || tiles > kMostSplit))
                 continue;
-            const int64_t c = longest_share(p, n, cols, s, clusters[s]) * (w ? 29 : 22) + (w ? 250 : 150) +
-                              (s > 1 ? 230 : 0) + 450;
+            int64_t busiest;
+            deal_of(p, n, cols, s, clusters[s], &busiest);
+            const int64_t c = busiest * (w ? 29 : 22) + (w ? 250 : 150) + (s > 1 ? 230 : 0) + 450;
             if (c < best.cost)
                 best = {c, s, w != 0};
         }
@@ -1118,8 +1159,8 @@ Plan plan(const Product *p, int n, const int *clusters)
     return best;
 }
 
-// The products of `a` (p[0] .. p[n - 1]), in one launch, longest K first, or each in its own where that is faster (a
-// product of few tiles and a long K wants it split, one of many tiles does not).
+// The products of `a` (p[0] .. p[n - 1]), longest K first: in one launch, the first apart from the others, or each in
+// its own, whichever is fastest (a product of few tiles and a long K wants it split, one of many tiles does not).
 template <int MODE, class TE>
 cudaError_t launch(Args &a, cudaStream_t st)
 {
@@ -1132,32 +1173,39 @@ cudaError_t launch(Args &a, cudaStream_t st)
             const Product t = a.p[j];
             a.p[j] = a.p[j - 1], a.p[j - 1] = t;
         }
-    const auto go = [&](Args &args, const Plan &how) {
-        if constexpr (MODE != kLse)
+    // products [from, from + n) of a in one launch
+    const auto go = [&](int from, int n, const Plan &how) {
+        Args part = a;
+        for (int i = 0; from && i < n; ++i)
+            part.p[i] = a.p[from + i];
+        part.n = n;
+        if constexpr (MODE != kLse) {
             if (!how.wide)
-                return launch_nt<MODE, TE, 128>(args, how.S, clusters[how.S], st);
-        return launch_nt<MODE, TE, 256>(args, how.S, clusters[how.S], st);
+                return launch_nt<MODE, TE, 128>(part, how.S, clusters[how.S], st);
+        }
+        const cudaError_t err = launch_nt<MODE, TE, 256>(part, how.S, clusters[how.S], st);
+        a.pairs = part.pairs;
+        return err;
     };
     const Plan all = plan<MODE>(a.p, a.n, clusters);
     if (a.n == 1)
-        return go(a, all);
-    Plan each[kProducts];
-    int64_t sum = 0;
-    for (int i = 0; i < a.n; ++i) {
-        each[i] = plan<MODE>(a.p + i, 1, clusters);
-        sum += each[i].cost;
+        return go(0, 1, all);
+    const Plan first = plan<MODE>(a.p, 1, clusters), others = plan<MODE>(a.p + 1, a.n - 1, clusters);
+    Plan each[kProducts] = {first, others, others};
+    int64_t apart = first.cost;
+    for (int i = 1; i < a.n; ++i) {
+        if (a.n > 2)
+            each[i] = plan<MODE>(a.p + i, 1, clusters);
+        apart += each[i].cost;
     }
-    if (all.cost <= sum)
-        return go(a, all);
-    for (int i = 0; i < a.n; ++i) {
-        Args one = a;
-        one.n = 1;
-        one.p[0] = a.p[i];
-        const cudaError_t err = go(one, each[i]);
-        if (err != cudaSuccess)
-            return err;
-    }
-    return cudaSuccess;
+    if (all.cost <= apart && all.cost <= first.cost + others.cost)
+        return go(0, a.n, all);
+    cudaError_t err = go(0, 1, first);
+    if (first.cost + others.cost <= apart)
+        return err != cudaSuccess ? err : go(1, a.n - 1, others);
+    for (int i = 1; i < a.n && err == cudaSuccess; ++i)
+        err = go(i, 1, each[i]);
+    return err;
 }
 
 }  // namespace dense
