@@ -542,8 +542,9 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t, int s)
     const Product &p = a.p[r.prod];
     t -= p.first;
     const int nkb = (p.K + 63) / 64;
-    r.kb0 = (int)((int64_t)nkb * s / a.S);
-    r.kb1 = (int)((int64_t)nkb * (s + 1) / a.S);
+    const int shift = a.S >> 1;  // log2 of S = 1, 2 or 4 (nkb < 2^24)
+    r.kb0 = nkb * s >> shift;
+    r.kb1 = nkb * (s + 1) >> shift;
     const int g = t / (kGroup * p.tiles_n);
     const int size = min(kGroup, p.tiles_m - g * kGroup);
     t -= g * kGroup * p.tiles_n;
