@@ -31,13 +31,18 @@ constexpr int kFewStageBytes = 16384 + NP * 128;
 template <int NP>
 constexpr int kFewStages = NP == 16 ? 5 : NP == 32 ? 4 : NP == 64 ? 3 : 4;
 
+// Logits are summed in parts of K here too, at no cost.
+template <int MODE>
+constexpr bool kFewInParts = MODE == kLse;
+
 template <int NP>
 struct __align__(1024) FewSmem {
     uint8_t stage[kFewStages<NP>][kFewStageBytes<NP>];
     float red[128 * NP];  // [S][NP][128 / S]: every CTA's part of the rows that this one finishes
     uint64_t full[kFewStages<NP>];
     uint64_t empty[kFewStages<NP>];
-    uint64_t done;
+    uint64_t done[2];     // the accumulator (of a part of K) is complete
+    uint64_t read[2];     // and has been read
     uint32_t tmem_base;
     int abort;
 };
@@ -55,6 +60,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     using SmemT = FewSmem<NP>;
     constexpr int kS = kFewStages<NP>;
     constexpr int kTile = MODE == kGated ? 64 : 128;  // features of a tile
+    constexpr int kColumns = kFewInParts<MODE> ? 2 * NP : NP < 32 ? 32 : NP;  // of TMEM
     extern __shared__ uint8_t smem_raw[];
     SmemT &sm = *reinterpret_cast<SmemT *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -68,14 +74,17 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
-        mbar_init(&sm.done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.done[i], 1);
+            mbar_init(&sm.read[i], 4);
+        }
         sm.abort = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&p.tm_a);
         tma_prefetch_desc(&p.tm_b);
     }
     if (warp == 1) {
-        tmem_alloc(&sm.tmem_base, NP < 32 ? 32 : NP);
+        tmem_alloc(&sm.tmem_base, kColumns);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -132,24 +141,36 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             pdl_wait();
             const uint32_t type = std::is_same<TE, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t idesc = make_idesc(type, type, 128, NP);
-            int s = 0;
+            int s = 0, acc = 0;
             uint32_t ph = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag))
+            const int part = kFewInParts<MODE> ? kPart : kb1 - kb0;
+            bool fine = true;
+            for (int k0 = kb0, n = 0; fine && k0 < kb1; k0 += part, ++n) {
+                acc = kFewInParts<MODE> ? n & 1 : 0;
+                // (two parts go ahead; the third waits until the first has been read)
+                if (n >= 2 && !mbar_wait(&sm.read[acc], (n / 2 - 1) & 1, a.status, abort_flag))
                     break;
                 tc_fence_after();
-                const uint8_t *w = sm.stage[s], *x = sm.stage[s] + 16384;
+                const int k1 = min(k0 + part, kb1);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag)) {
+                        fine = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t *w = sm.stage[s], *x = sm.stage[s] + 16384;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16(tmem_base, smem_desc_sw128(w + kk * 32), smem_desc_sw128(x + kk * 32), idesc,
-                             (kb > kb0 || kk > 0) ? 1u : 0u);
-                mma_commit(&sm.empty[s]);
-                if (++s == kS) {
-                    s = 0;
-                    ph ^= 1;
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16(tmem_base + acc * NP, smem_desc_sw128(w + kk * 32), smem_desc_sw128(x + kk * 32),
+                                 idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&sm.empty[s]);
+                    if (++s == kS) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
+                mma_commit(&sm.done[acc]);
             }
-            mma_commit(&sm.done);
         }
     } else {
         pdl_wait();
@@ -158,9 +179,35 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         const int r = q * 32 + lane;  // weight row
         if (MODE == kLse && warp - 2 + 4 * lane < (int)p.M)
             targets = a.targets[warp - 2 + 4 * lane];
-        ok = mbar_wait(&sm.done, 0, a.status, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
+        constexpr int kC = NP < 32 ? 16 : 32;
+        float sums[kFewInParts<MODE> ? NP : 1];
+        if constexpr (kFewInParts<MODE>) {
+            for (int k0 = kb0, n = 0; k0 < kb1; k0 += kPart, ++n) {
+                ok = mbar_wait(&sm.done[n & 1], (n / 2) & 1, a.status, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float f[kC];
+                static_assert(kC == NP, "one load");
+                if constexpr (kC == 16)
+                    tmem_ld16(tacc + (n & 1) * NP, f);
+                else
+                    tmem_ld32(tacc + (n & 1) * NP, f);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    sums[i] = n == 0 ? f[i] : sums[i] + f[i];
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.read[n & 1]);
+            }
+        } else {
+            ok = mbar_wait(&sm.done[0], 0, a.status, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        }
         // rows that a CTA of the cluster finishes: 128 / S consecutive ones, gated as many gate rows and up rows
         const int own = 128 / S;
         int owner, local;
@@ -175,12 +222,14 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         __syncwarp();
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         const uint32_t dst = cluster_map(sm.red, owner) + (uint32_t)((rank * NP * own + local) * 4);
-        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
-        constexpr int kC = NP < 32 ? 16 : 32;
 #pragma unroll 1
         for (int c = 0; c < NP; c += kC) {
             float v[kC];
-            if constexpr (kC == 16)
+            if constexpr (kFewInParts<MODE>) {
+#pragma unroll
+                for (int i = 0; i < kC; ++i)
+                    v[i] = sums[i];
+            } else if constexpr (kC == 16)
                 tmem_ld16(tacc + c, v);
             else
                 tmem_ld32(tacc + c, v);
@@ -283,7 +332,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     if (warp == 1)
-        tmem_dealloc(tmem_base, NP < 32 ? 32 : NP);
+        tmem_dealloc(tmem_base, kColumns);
 }
 
 // ------------------------------------------------------------------- host

@@ -46,6 +46,7 @@ enum Mode {
     kGated,     // v = gate | up: h = act(gate) * up (and gate | up themselves, for the backward)
     kGatedBwd,  // v = dh: d gate | d up from the kept gate | up
     kLse,       // v = logits: each row's maximum and sum of exponentials in the tile, the target's logit
+    kLseLong,   // the same for a long K, summed in parts
     kDlogits,   // v = logits: (softmax - one at the target) times the row's factor
 };
 
@@ -127,6 +128,14 @@ template <int NT>
 constexpr int kStageBytes = kABytes + NT / 2 * 128;
 template <int NT>
 constexpr int kStages = NT == 256 ? 6 : 8;
+// The tensor core truncates its running sums: over K = 4096 a logit shrinks by 1.8e-6 of itself, and the loss, which
+// stays in 32 bits, with it.  Logits of a longer K than 2048 are therefore summed 2048 of it at a time, the parts in
+// registers with rounding: 0.6e-6 off for any K (what is rounded to 16 bits does not need it).  This takes half of the
+// registers, so that the kernel that follows no longer starts ahead: 4096 x 32000, 100 rows 54 -> 59 us, 2000 rows 295
+// -> 298; shorter ones keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).
+constexpr int kPart = 32;  // blocks of 64 of K
+template <int MODE>
+constexpr bool kIsLse = MODE == kLse || MODE == kLseLong;
 constexpr int kRowsBytes = 4096;    // an epilogue warp's 32 rows of 32 columns of up to 32 bits
 
 template <int NT>
@@ -609,7 +618,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
         }
     };
     RowOf of = {};
-    if (MODE == kLse || MODE == kDlogits)
+    if (kIsLse<MODE> || MODE == kDlogits)
         of = row_of<MODE>(a, row);
     float top = -INFINITY, exps = 0.0f, target_logit = 0.0f;
     bool has = false;
@@ -625,7 +634,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
             epi_store<TE>(p, row, col + c, v);
         } else if constexpr (MODE == kGatedBwd) {
             epi_gated_bwd<TE>(a, row, col + c, v);
-        } else if constexpr (MODE == kLse) {
+        } else if constexpr (kIsLse<MODE>) {
             epi_lse(p.N, col + c, of.target, v, top, exps, target_logit, has);
         } else {
             epi_dlogits(col + c, of.target, of.lse, of.factor, v);
@@ -636,7 +645,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
                     store8(dst + i, v + i);
         }
     }
-    if (MODE == kLse) {
+    if (kIsLse<MODE>) {
         a.stats[row * a.pairs + (tile.nt * S + pair) * 2 + half] = make_float2(top, exps);
         if (has)
             a.target_logit[row] = target_logit;
@@ -759,41 +768,45 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
                 const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
                                        (maj == 2 ? 1u << 15 : 0u);
-                if (!mbar_wait(&sm.tempty[acc], aph ^ 1, a.status, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem_base + acc * 256;
-                for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
-                    if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag)) {
+                const int part = MODE == kLseLong && S == 1 ? kPart : tile.kb1 - tile.kb0;
+                for (int k0 = tile.kb0; k0 < tile.kb1; k0 += part) {
+                    if (!mbar_wait(&sm.tempty[acc], aph ^ 1, a.status, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint8_t *sa = sm.stage[s], *sb = sm.stage[s] + kABytes;
-                    // 16 of K: 32 bytes further along a K-major row, 16 rows (2 KB) further in an MN-major box
-                    uint64_t da = maj == 2 ? smem_desc_sw128_mn(sa, kABytes / 2) : smem_desc_sw128(sa);
-                    uint64_t db = maj >= 1 ? smem_desc_sw128_mn(sb, 8192) : smem_desc_sw128(sb);
-                    const uint64_t ia = maj == 2 ? 2048 >> 4 : 32 >> 4, ib = maj >= 1 ? 2048 >> 4 : 32 >> 4;
+                    const uint32_t d = tmem_base + acc * 256;
+                    const int k1 = min(k0 + part, tile.kb1);
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!mbar_wait(&sm.full[s], ph, a.status, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint8_t *sa = sm.stage[s], *sb = sm.stage[s] + kABytes;
+                        // 16 of K: 32 bytes further along a K-major row, 16 rows (2 KB) further in an MN-major box
+                        uint64_t da = maj == 2 ? smem_desc_sw128_mn(sa, kABytes / 2) : smem_desc_sw128(sa);
+                        uint64_t db = maj >= 1 ? smem_desc_sw128_mn(sb, 8192) : smem_desc_sw128(sb);
+                        const uint64_t ia = maj == 2 ? 2048 >> 4 : 32 >> 4, ib = maj >= 1 ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        mma_pair<0>(d, da, db, idesc, (kb > tile.kb0 || kk > 0) ? 1u : 0u);
-                        da += ia, db += ib;  // (the start address is the descriptor's lowest field)
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma_pair<0>(d, da, db, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+                            da += ia, db += ib;  // (the start address is the descriptor's lowest field)
+                        }
+                        any = true;
+                        mma_commit_pair(&sm.empty[s], both);
+                        if (++s == kS) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    any = true;
-                    mma_commit_pair(&sm.empty[s], both);
-                    if (++s == kS) {
-                        s = 0;
-                        ph ^= 1;
+                    if (!ok)
+                        break;
+                    mma_commit_pair(&sm.tfull[acc], both);
+                    if (++acc == 2) {
+                        acc = 0;
+                        aph ^= 1;
                     }
-                }
-                if (!ok)
-                    break;
-                mma_commit_pair(&sm.tfull[acc], both);
-                if (++acc == 2) {
-                    acc = 0;
-                    aph ^= 1;
                 }
             }
             if (!ok && any) {
@@ -831,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     prefetch_l2(add + c * es);
             }
             RowOf of = {};
-            if (MODE == kLse || MODE == kDlogits)
+            if (kIsLse<MODE> || MODE == kDlogits)
                 of = row_of<MODE>(a, row);
             uint4 *buf = reinterpret_cast<uint4 *>(sm.rows[warp - 2]);
             const int64_t row0 = tile.m0 + rank * 128 + q * 32;  // the warp's rows
@@ -856,6 +869,48 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             };
             read(0);
+            if constexpr (MODE == kLseLong) {
+                if (S == 1) {
+                    float v[kMine] = {}, m = -INFINITY, e = 0.0f, own = 0.0f;
+                    bool ok = true, has = false;
+                    for (int k0 = tile.kb0; k0 < tile.kb1; k0 += kPart) {
+                        ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
+#pragma unroll
+                        for (int c = 0; c < kMine; c += 16) {
+                            float f[16];
+                            tmem_ld16(tacc + c, f);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                v[c + i] += f[i];
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
+                        if (++acc == 2) {
+                            acc = 0;
+                            aph ^= 1;
+                        }
+                    }
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int c = 0; c < kMine; c += 16)
+                        if (c0 + c < p.N)
+                            epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(v[c]), m, e, own, has);
+                    if (live) {
+                        a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
+                        if (has)
+                            a.target_logit[row] = own;
+                    }
+                    continue;
+                }
+            }
             bool ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
@@ -864,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             if (S > 1)
                 break;  // the parts meet below
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
-            float m = -INFINITY, s = 0.0f, own = 0.0f;
+            float m = -INFINITY, e = 0.0f, own = 0.0f;
             bool has = false;
 #pragma unroll 1
             for (int c = 0; c < kMine && c0 + c < p.N && rows > 0; c += 32) {
@@ -942,16 +997,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     TE *out = static_cast<TE *>(a.dgu) + row0 * 2 * p.N + col;
                     Rows<TE>::store(buf, wg, out, 2 * (int64_t)p.N, rows, cols, lane);
                     Rows<TE>::store(buf, wu, out + p.N, 2 * (int64_t)p.N, rows, cols, lane);
-                } else if constexpr (MODE == kLse) {
-                    epi_lse(p.N, col, of.target, v, m, s, own, has);
+                } else if constexpr (kIsLse<MODE>) {
+                    epi_lse(p.N, col, of.target, v, m, e, own, has);
                 } else {
                     epi_dlogits(col, of.target, of.lse, of.factor, v);
                     // (a last piece of 8 columns may go past N, into the rows' padding)
                     put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + col, p.ld_d, rows, cols, lane);
                 }
             }
-            if (MODE == kLse && live) {
-                a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, s);
+            if (kIsLse<MODE> && live) {
+                a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
                 if (has)
                     a.target_logit[row] = own;
             }
@@ -1139,7 +1194,7 @@ Plan plan(const Product *p, int n, const int *clusters)
     int least = p[0].K;
     for (int i = 1; i < n; ++i)
         least = p[i].K < least ? p[i].K : least;
-    for (int w = MODE == kLse ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
+    for (int w = kIsLse<MODE> ? 1 : 0; w < 2; ++w) {  // (a logit tile leaves two pairs a row, whatever its width)
         const int cols = (w ? 256 : 128) / (MODE == kGated ? 2 : 1);
         // (a warp of an owner finishes 16 columns at least, of each side)
         const int most = MODE == kGated && !w ? 2 : 4;
@@ -1180,7 +1235,7 @@ cudaError_t launch(Args &a, cudaStream_t st)
         for (int i = 0; from && i < n; ++i)
             part.p[i] = a.p[from + i];
         part.n = n;
-        if constexpr (MODE != kLse) {
+        if constexpr (!kIsLse<MODE>) {
             if (!how.wide)
                 return launch_nt<MODE, TE, 128>(part, how.S, clusters[how.S], st);
         }

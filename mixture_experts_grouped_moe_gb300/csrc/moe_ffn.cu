@@ -8,7 +8,7 @@
 // between the products (they are operands of 16-bit MMAs): errors of half a step an element, independent ones, that a
 // sum over I or T averages.
 //
-// 4096 tokens through 7168 x 2048, forward and gradients: 720-735 us, 1.5 PFLOP/s; forward alone see dense_gemm.cuh
+// 4096 tokens through 7168 x 2048, forward and gradients: 680-690 us, 1.6 PFLOP/s; forward alone see dense_gemm.cuh
 // and, for few tokens, dense_few.cuh.
 #include "dense_few.cuh"
 

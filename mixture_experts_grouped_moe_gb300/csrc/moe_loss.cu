@@ -14,7 +14,7 @@
 // by its inverse: a mean over many rows makes dl too small for fp16 otherwise (its smallest step, 2^-24, is then
 // at most 2^-38 of the largest row's factor).
 //
-// Bound by the tensor pipe and in a row by the board's power: 4096 x 4096 x 32000 forward and backward 2.63 ms (1.63
+// Bound by the tensor pipe and in a row by the board's power: 4096 x 4096 x 32000 forward and backward 2.55 ms (1.68
 // PFLOP/s); by memory for few rows: 16 rows 48 us for 262 MB.
 #include "dense_few.cuh"
 
@@ -151,7 +151,9 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     product(a, T, V, H, 0, x, ld_x, W, H);
     a.V = V;
     a.targets = targets, a.stats = stats, a.target_logit = own;
-    const cudaError_t err = T <= kFewMost<kLse> ? launch_few<kLse, TE>(a, false, st) : launch<kLse, TE>(a, st);
+    const cudaError_t err = T <= kFewMost<kLse>   ? launch_few<kLse, TE>(a, false, st)
+                            : H > 64 * kPart      ? launch<kLseLong, TE>(a, st)
+                                                  : launch<kLse, TE>(a, st);
     if (err != cudaSuccess)
         return err;
     return launch_kernel(true, finish_kernel, dim3((unsigned)((T + 7) / 8)), dim3(256), 0, st, (const float2 *)stats,

@@ -66,6 +66,23 @@ def test_against_64_bits(moe, T, H, V, t):
     assert serve.status() == moe.MOE_OK
 
 
+@pytest.mark.parametrize("T,H,V", [(16, 8200, 40000), (32, 4104, 5000), (300, 4104, 10001), (300, 7176, 500)])
+def test_long_rows(moe, T, H, V):
+    """A logit of so many products is summed in parts (in one piece and split over CTAs, for few rows and for more)."""
+    x, w, targets, dloss = make(T, H, V, "bf16", H + V)
+    xd, wd = x.double(), w.double()
+    f = moe.VocabularyLoss(T, H, V, training=True)
+    loss = f.forward(x, w, targets)
+    for got, want, bound, n in zip((loss, f.lse), tr.loss(xd, wd, targets), tr.loss_bound(xd, wd, targets),
+                                   ("loss", "lse")):
+        tr.bounded(got, want, bound, n)
+    g = f.backward(x, w, targets, dloss)
+    want, bound = tr.loss_grads_bound(xd, wd, targets, dloss.double(), "bf16", "fp32")
+    tr.bounded(g["dx"], want["dx"], tr.loss_grads_bound(xd, wd, targets, dloss.double(), "bf16", "bf16")[1]["dx"], "dx")
+    tr.bounded(g["dW"], want["dW"], bound["dW"], "dW")
+    assert f.status() == moe.MOE_OK
+
+
 def test_differences(moe):
     """The gradient along a direction against central differences of the losses.  x and the direction are multiples
     of 2^-4 below 4 and the step 2^-4, so that x +- step * direction are bf16 numbers; the third derivative of a
