@@ -138,6 +138,14 @@ def test_some_gradients_only(moe, T):
     for n in g:
         assert torch.equal(new[n], g[n]), n
     call(None, None, None)
+    # dx into rows of a wider buffer; a forward that keeps h alone
+    wide = torch.full((T, H + 8), float("nan"), dtype=x.dtype, device="cuda")
+    moe.moe_ffn_backward(f.row_type, f.act, x, H, wgu, wd, f.gu, f.h, dout, H, T, H, I, wide, H + 8, moe.MOE_ROW_FP32, 0,
+                         None, None, f.ws, f.ws_bytes)
+    assert torch.equal(wide[:, :H], g["dx"]) and wide[:, H:].isnan().all()
+    h, out = torch.empty_like(f.h), torch.empty_like(x)
+    moe.moe_ffn(f.row_type, f.act, x, H, wgu, wd, None, 0, T, H, I, None, h, out, H, f.ws, f.ws_bytes)
+    assert torch.equal(h, f.h) and torch.equal(out, f.forward(x, wgu, wd))
 
 
 def test_saturated_activations(moe):
@@ -202,3 +210,26 @@ def test_no_tokens(moe):
     old = torch.ones(2 * I, H, device="cuda"), torch.ones(H, I, device="cuda")
     g = f.backward(x, wgu, wd, x, *old, accumulate=True)
     assert (g["dW_gate_up"] == 1).all() and (g["dW_down"] == 1).all()
+
+
+def test_two_at_once(moe):
+    """Two objects at work on two streams at the same time, of sizes that take whole tiles, split ones and few tokens."""
+    sizes = [(700, 320, 1288), (300, 1024, 512), (20, 512, 256), (257, 64, 2056)]
+    objects, want = [], []
+    for i, (T, H, I) in enumerate(sizes):
+        a = real(T, H, I, "bf16", 20 + i)
+        f = moe.GatedFFN(T, H, I, training=True)
+        want.append((f.forward(*a[:4]).clone(), {n: v.clone() for n, v in f.backward(*a[:3], a[4]).items()}))
+        objects.append((f, a))
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s, (f, a) in zip(streams, objects):
+            got.append((f.forward(*a[:4], stream=s), f.backward(*a[:3], a[4], stream=s)))
+        torch.cuda.synchronize()
+        for (out, g), (o, w) in zip(got, want):
+            assert torch.equal(out, o)
+            for n in w:
+                assert torch.equal(g[n], w[n]), n
+    assert all(f.status() == moe.MOE_OK for f, _ in objects)

@@ -185,3 +185,32 @@ def test_no_rows(moe):
     f = moe.VocabularyLoss(0, H, V, training=True)
     assert f.forward(x, w, none).shape == (0,)
     assert not f.backward(x, w, none, f32)["dW"].any()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_some_gradients_only_and_strided(moe, T):
+    """dx without dW and dW without dx, dx into rows of a wider buffer, dW added to in the rows' type."""
+    H, V, piece = 72, 700, 256
+    x, w, targets, dloss = make(T, H, V, "fp16", 11)
+    f = moe.VocabularyLoss(T, H, V, torch.float16, training=True, piece=piece)
+    f.forward(x, w, targets)
+    want = f.backward(x, w, targets, dloss, grad_dtype=torch.float16)
+    t = moe.MOE_ROW_FP16
+
+    def call(dx, ld, dw, accumulate=0):
+        moe.moe_vocab_loss_backward(t, x, H, w, targets, f.lse, dloss, T, H, V, piece, dx, ld, t, accumulate, dw, f.ws,
+                                    f.ws_bytes)
+
+    wide = torch.full((T, H + 16), float("nan"), dtype=x.dtype, device="cuda")
+    call(wide, H + 16, None)
+    assert torch.equal(wide[:, :H], want["dx"]) and wide[:, H:].isnan().all()
+    dw = torch.full_like(w, float("nan"))
+    call(None, 0, dw)
+    assert torch.equal(dw, want["dW"])
+    old = torch.randn(V, H, generator=ref.gen(12)).half().cuda()
+    dw = old.clone()
+    call(None, 0, dw, 1)
+    xd, wd, dd = x.double(), w.double(), dloss.double()
+    g, bound = tr.loss_grads_bound(xd, wd, targets, dd, "fp16", "fp16", old.double())
+    tr.bounded(dw, g["dW"] + old.double(), bound["dW"], "dW accumulated")
+    call(None, 0, None)
