@@ -128,14 +128,20 @@ template <int NT>
 constexpr int kStageBytes = kABytes + NT / 2 * 128;
 template <int NT>
 constexpr int kStages = NT == 256 ? 6 : 8;
-// The tensor core truncates its running sums: over K = 4096 a logit shrinks by 1.8e-6 of itself, and the loss, which
-// stays in 32 bits, with it.  Logits of a longer K than 2048 are therefore summed 2048 of it at a time, the parts in
-// registers with rounding: 0.6e-6 off for any K (what is rounded to 16 bits does not need it).  This takes half of the
-// registers, so that the kernel that follows no longer starts ahead: 4096 x 32000, 100 rows 54 -> 59 us, 2000 rows 295
-// -> 298; shorter ones keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).
+// The tensor core truncates what it adds to its running sum: of positive products a sum loses 2.7e-6 of itself over
+// K = 2048, 1.0e-5 over 4096, 3.0e-5 over 8192 and 3.8e-4 over 65536, and the loss, which stays in 32 bits, with it.
+// Logits of a longer K than 2048 are therefore summed 2048 of it at a time, the parts in registers with rounding, also
+// within each pair's share of a split tile: 2.8e-6 at most, for any K.  This takes half of the registers, so that the
+// kernel that follows no longer starts ahead: 4096 x 32000, 100 rows 54 -> 59 us, 2000 rows 295 -> 298; shorter ones
+// keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).
 constexpr int kPart = 32;  // blocks of 64 of K
 template <int MODE>
 constexpr bool kIsLse = MODE == kLse || MODE == kLseLong;
+template <int MODE>
+constexpr bool kInParts = MODE == kLseLong;
+// Sums that a thread of the epilogue keeps: its row's half of a tile's columns.
+template <int MODE, int NT>
+constexpr int kSums = kInParts<MODE> ? NT / 2 : 1;
 constexpr int kRowsBytes = 4096;    // an epilogue warp's 32 rows of 32 columns of up to 32 bits
 
 template <int NT>
@@ -568,10 +574,10 @@ constexpr int kCols = MODE == kGated ? NT / 2 : NT;
 
 // The parts of a split tile's accumulator to the pairs that own their columns, and the owners' epilogue.  All
 // threads of the cluster.  buf: [S sources][columns / 4][128 rows] of four columns, so that neighbouring threads
-// (rows) touch neighbouring 16 bytes.
+// (rows) touch neighbouring 16 bytes.  The accumulator is in TMEM, or its sum over parts of K in `sums`.
 template <int MODE, class TE, int NT>
 __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_base, const Tile &tile, int rank,
-                                     int pair, int warp, int lane)
+                                     int pair, int warp, int lane, const float (&sums)[kSums<MODE, NT>])
 {
     const int S = a.S, q = warp & 3, half = (warp - 2) / 4, r = q * 32 + lane;
     // accumulator columns that a pair owns: gated, as many of the gate's as of the up's
@@ -580,10 +586,17 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
     const int own = kSide / S;  // of each side, 32 or more
     if (warp >= 2) {
         const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
-#pragma unroll 1
-        for (int c = half * (NT / 2); c < (half + 1) * (NT / 2); c += 16) {
+#pragma unroll(kInParts<MODE> ? NT / 32 : 1)
+        for (int i0 = 0; i0 < NT / 2; i0 += 16) {
+            const int c = half * (NT / 2) + i0;
             float v[16];
-            tmem_ld16(tacc + c, v);
+            if constexpr (kInParts<MODE>) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = sums[i0 + i];
+            } else {
+                tmem_ld16(tacc + c, v);
+            }
             const int side = c / kSide, at = c % kSide, owner = at / own, local = side * own + at % own;
             const uint32_t dst = cluster_map(buf, (uint32_t)(owner * 2 + rank)) +
                                  (uint32_t)(((pair * kSides * own + local) / 4 * 128 + r) * 16);
@@ -706,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
 
+    float sums[kSums<MODE, NT>];  // of the epilogue's threads
     if (warp == 0) {
         if (lane == 0) {
             // both operands are read again by the pairs around (ms as above: evict-normal 1.740, evict-last 1.699; the
@@ -768,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
                 const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
                                        (maj == 2 ? 1u << 15 : 0u);
-                const int part = MODE == kLseLong && S == 1 ? kPart : tile.kb1 - tile.kb0;
+                const int part = kInParts<MODE> ? kPart : tile.kb1 - tile.kb0;
                 for (int k0 = tile.kb0; k0 < tile.kb1; k0 += part) {
                     if (!mbar_wait(&sm.tempty[acc], aph ^ 1, a.status, abort_flag)) {
                         ok = false;
@@ -869,47 +883,49 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             };
             read(0);
-            if constexpr (MODE == kLseLong) {
-                if (S == 1) {
-                    float v[kMine] = {}, m = -INFINITY, e = 0.0f, own = 0.0f;
-                    bool ok = true, has = false;
-                    for (int k0 = tile.kb0; k0 < tile.kb1; k0 += kPart) {
-                        ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
+            if constexpr (kInParts<MODE>) {
+                bool ok = true;
 #pragma unroll
-                        for (int c = 0; c < kMine; c += 16) {
-                            float f[16];
-                            tmem_ld16(tacc + c, f);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[c + i] += f[i];
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
-                        if (++acc == 2) {
-                            acc = 0;
-                            aph ^= 1;
-                        }
-                    }
+                for (int i = 0; i < kMine; ++i)
+                    sums[i] = 0.0f;
+                for (int k0 = tile.kb0; k0 < tile.kb1; k0 += kPart) {
+                    ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
+                    tc_fence_after();
+                    const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
 #pragma unroll
-                    for (int c = 0; c < kMine; c += 16)
-                        if (c0 + c < p.N)
-                            epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(v[c]), m, e, own, has);
-                    if (live) {
-                        a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
-                        if (has)
-                            a.target_logit[row] = own;
+                    for (int c = 0; c < kMine; c += 16) {
+                        float f[16];
+                        tmem_ld16(tacc + c, f);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sums[c + i] += f[i];
                     }
-                    continue;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
+                    if (++acc == 2) {
+                        acc = 0;
+                        aph ^= 1;
+                    }
                 }
+                if (!ok || S > 1)
+                    break;  // (the parts of a split tile meet below)
+                float m = -INFINITY, e = 0.0f, own = 0.0f;
+                bool has = false;
+#pragma unroll
+                for (int c = 0; c < kMine; c += 16)
+                    if (c0 + c < p.N)
+                        epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(sums[c]), m, e, own, has);
+                if (live) {
+                    a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
+                    if (has)
+                        a.target_logit[row] = own;
+                }
+                continue;
             }
             bool ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -1028,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         tc_fence_before();
         cluster_sync();
         tc_fence_after();
-        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
+        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane, sums);
     }
     // both CTAs stay until the pair's last MMA, copy and remote arrive are done
     __syncwarp();

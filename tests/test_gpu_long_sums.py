@@ -1,0 +1,61 @@
+"""Sums over a long K, against 64 bits, with positive terms: the tensor core's truncation then adds up instead of
+averaging out, and a sum that should go in parts but does not is told apart.
+
+Bounds.  An MMA adds 16 products to a sum of K at a time and may drop up to one step of it (2^-23 of its size): a sum
+that grows evenly over n additions loses at most 2^-23 (n + 1) / 2 of itself.  Parts that are added with rounding lose
+2^-24 (m + 1) / 2 more for m of them.  The terms here lie between 1/4 and 1 of the largest, which brings a running sum
+from evenly growing by less than a tenth."""
+import pytest
+import torch
+
+import ops_reference as ref
+import training_reference as tr
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from mixture_experts_grouped_moe_gb300 import build
+    build.build()
+    from mixture_experts_grouped_moe_gb300 import moe as m
+    m.load()
+    yield m
+    torch.cuda.empty_cache()
+
+
+def loss_of(K, part):
+    """What a sum of K positive terms in parts of `part` loses at most, relative to it."""
+    return 1.1 * 2.0 ** -23 * (part / 16 + 1) / 2 + 2.0 ** -24 * (-(-K // part) + 1) / 2
+
+
+def positive(*shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return ((0.5 + 0.5 * torch.rand(*shape, generator=g, device="cuda")) * scale).bfloat16()
+
+
+def logits_64(x, w):
+    """x w^T in 64 bits, some words at a time."""
+    xd = x.double()
+    return torch.cat([xd @ v.double().t() for v in w.split(max(1, 2 ** 28 // w.shape[1]))], 1)
+
+
+LOGIT = 2048  # of K at a time
+
+
+# Few rows; few tiles, whose K 4 or 2 pairs of a cluster share; tiles enough that none is shared; and ordinary sizes
+@pytest.mark.parametrize("T,K,V", [(16, 131072, 1000), (32, 65536, 300), (300, 262144, 500), (100, 131072, 5000),
+                                   (300, 65536, 5120), (100, 7168, 8192), (100, 16384, 2000), (64, 4104, 300)])
+def test_logits(moe, T, K, V):
+    """The loss and lse of logits near 100."""
+    x, w = positive(T, K, seed=1), positive(V, K, seed=2, scale=100 / (0.5625 * K))
+    targets = torch.randint(0, V, (T,), generator=ref.gen(3), dtype=torch.int32).cuda()
+    f = moe.VocabularyLoss(T, K, V)
+    loss = f.forward(x, w, targets)
+    assert f.status() == moe.MOE_OK
+    l = logits_64(x, w)
+    lse = torch.logsumexp(l, 1)
+    top = l.amax(1)
+    e = loss_of(K, LOGIT) * top + 2.0 ** -18 + 2.0 ** -21 * (top + 20)
+    tr.bounded(f.lse, lse, e, "lse")
+    tr.bounded(loss, lse - l.gather(1, targets.long()[:, None])[:, 0], 2 * e, "loss")
