@@ -48,6 +48,7 @@ enum Mode {
     kLse,       // v = logits: each row's maximum and sum of exponentials in the tile, the target's logit
     kLseLong,   // the same for a long K, summed in parts
     kDlogits,   // v = logits: (softmax - one at the target) times the row's factor
+    kDlogitsLong,
 };
 
 constexpr int kProducts = 3;  // of one launch
@@ -133,12 +134,16 @@ constexpr int kStages = NT == 256 ? 6 : 8;
 // Logits of a longer K than 2048 are therefore summed 2048 of it at a time, the parts in registers with rounding, also
 // within each pair's share of a split tile: 2.8e-6 at most, for any K.  This takes half of the registers, so that the
 // kernel that follows no longer starts ahead: 4096 x 32000, 100 rows 54 -> 59 us, 2000 rows 295 -> 298; shorter ones
-// keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).
+// keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).  The backward's logits go the same way: p =
+// exp(l - lse) wants l as it was when lse was made of it, above all where p is near 1 and the gradient is 1 - p (a
+// logit of 30 that lost 1.0e-5 of itself makes 1 - p = 1e-3 a third larger).
 constexpr int kPart = 32;  // blocks of 64 of K
 template <int MODE>
 constexpr bool kIsLse = MODE == kLse || MODE == kLseLong;
 template <int MODE>
-constexpr bool kInParts = MODE == kLseLong;
+constexpr bool kIsDlogits = MODE == kDlogits || MODE == kDlogitsLong;
+template <int MODE>
+constexpr bool kInParts = MODE == kLseLong || MODE == kDlogitsLong;
 // Sums that a thread of the epilogue keeps: its row's half of a tile's columns.
 template <int MODE, int NT>
 constexpr int kSums = kInParts<MODE> ? NT / 2 : 1;
@@ -528,7 +533,7 @@ __device__ __forceinline__ RowOf row_of(const Args &a, int64_t row)
     if (row < a.p[0].M) {
         const int t = a.targets[row];
         const bool counts = t >= 0 && t < a.V;
-        if (MODE == kDlogits) {
+        if (kIsDlogits<MODE>) {
             r.lse = a.lse[row];
             r.factor = counts ? a.dloss[row] * a.dscale[0] : 0.0f;
         }
@@ -631,7 +636,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
         }
     };
     RowOf of = {};
-    if (kIsLse<MODE> || MODE == kDlogits)
+    if (kIsLse<MODE> || kIsDlogits<MODE>)
         of = row_of<MODE>(a, row);
     float top = -INFINITY, exps = 0.0f, target_logit = 0.0f;
     bool has = false;
@@ -858,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     prefetch_l2(add + c * es);
             }
             RowOf of = {};
-            if (kIsLse<MODE> || MODE == kDlogits)
+            if (kIsLse<MODE> || kIsDlogits<MODE>)
                 of = row_of<MODE>(a, row);
             uint4 *buf = reinterpret_cast<uint4 *>(sm.rows[warp - 2]);
             const int64_t row0 = tile.m0 + rank * 128 + q * 32;  // the warp's rows
@@ -914,16 +919,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
                 if (!ok || S > 1)
                     break;  // (the parts of a split tile meet below)
-                float m = -INFINITY, e = 0.0f, own = 0.0f;
-                bool has = false;
+                if constexpr (kIsLse<MODE>) {
+                    float m = -INFINITY, e = 0.0f, own = 0.0f;
+                    bool has = false;
 #pragma unroll
-                for (int c = 0; c < kMine; c += 16)
-                    if (c0 + c < p.N)
-                        epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(sums[c]), m, e, own, has);
-                if (live) {
-                    a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
-                    if (has)
-                        a.target_logit[row] = own;
+                    for (int c = 0; c < kMine; c += 16)
+                        if (c0 + c < p.N)
+                            epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(sums[c]), m, e, own, has);
+                    if (live) {
+                        a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
+                        if (has)
+                            a.target_logit[row] = own;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kMine; c += 32)
+                        if (c0 + c < p.N && rows > 0) {
+                            float(&v)[32] = reinterpret_cast<float(&)[32]>(sums[c]);
+                            epi_dlogits(c0 + c, of.target, of.lse, of.factor, v);
+                            put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + c0 + c, p.ld_d, rows,
+                                     p.N - c0 - c, lane);
+                        }
                 }
                 continue;
             }

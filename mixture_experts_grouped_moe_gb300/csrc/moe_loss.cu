@@ -185,7 +185,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         Product &p = product(a, T, n, H, 0, x, ld_x, Wp, H);
         a.targets = targets, a.lse = lse, a.dloss = dloss, a.dscale = factor, a.v0 = (int)v0, a.V = V;
         p.d = dl, p.ld_d = pitch;
-        if ((err = launch<kDlogits, TE>(a, st)) != cudaSuccess)
+        if ((err = H > 64 * kPart ? launch<kDlogitsLong, TE>(a, st) : launch<kDlogits, TE>(a, st)) != cudaSuccess)
             return err;
         a = base;
         if (dx) {  // the sum over the pieces, scaled back and rounded with the last one

@@ -59,3 +59,33 @@ def test_logits(moe, T, K, V):
     e = loss_of(K, LOGIT) * top + 2.0 ** -18 + 2.0 ** -21 * (top + 20)
     tr.bounded(f.lse, lse, e, "lse")
     tr.bounded(loss, lse - l.gather(1, targets.long()[:, None])[:, 0], 2 * e, "loss")
+
+
+@pytest.mark.parametrize("T,K,V", [(20, 131072, 500), (300, 131072, 500), (300, 65536, 5120), (600, 131072, 2500)])
+def test_gradient_of_sure_rows(moe, T, K, V):
+    """Rows whose target has nearly all of the probability: 1 - p of the target is a small difference, in which the
+    forward's and the backward's logits have to agree.  A logit that is off by e changes p by a factor exp(e); the
+    forward's and the backward's sums each lose between nothing and loss_of."""
+    x, w = positive(T, K, seed=4), positive(V, K, seed=5, scale=100 / (0.5625 * K))
+    w[7] *= 1.15  # 15 above the others
+    targets = torch.full((T,), 7, dtype=torch.int32, device="cuda")
+    dloss = torch.ones(T, device="cuda")
+    f = moe.VocabularyLoss(T, K, V, training=True)
+    f.forward(x, w, targets)
+    dx = f.backward(x, w, targets, dloss)["dx"]
+    assert f.status() == moe.MOE_OK
+    l = logits_64(x, w)
+    p = torch.softmax(l, 1)
+    top = l.amax(1, keepdim=True)
+    assert 1e-5 < float((1 - p[:, 7]).max()) < 1e-2
+    dl = p.clone()
+    dl[:, 7] -= 1
+    el = loss_of(K, LOGIT) * top + 2.0 ** -17 + 2.0 ** -20 * (top + 20)
+    e = ref.HALF_ULP["bf16"]
+    ed = p * (torch.expm1(el) + tr.FN) + 2.0 ** -23
+    ed = ed + e * (dl.abs() + ed) + 2.0 ** -130
+    full = dl.abs() + ed
+    for i in range(0, K, 8192):
+        wd = w[:, i:i + 8192].double()
+        want, err = dl @ wd, ed @ wd + loss_of(V, max(V, 16)) * (full @ wd)
+        tr.bounded(dx[:, i:i + 8192], want, err + e * (want.abs() + err) + ref.TINY["bf16"], "dx")
