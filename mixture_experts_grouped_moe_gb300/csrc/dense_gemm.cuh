@@ -43,6 +43,7 @@ namespace dense {
 
 enum Mode {
     kStore,     // d = (acc_in + v) * *scale + add
+    kStoreLong, // the same for a long K, summed in parts
     kGated,     // v = gate | up: h = act(gate) * up (and gate | up themselves, for the backward)
     kGatedBwd,  // v = dh: d gate | d up from the kept gate | up
     kLse,       // v = logits: each row's maximum and sum of exponentials in the tile, the target's logit
@@ -130,23 +131,28 @@ constexpr int kStageBytes = kABytes + NT / 2 * 128;
 template <int NT>
 constexpr int kStages = NT == 256 ? 6 : 8;
 // The tensor core truncates what it adds to its running sum: of positive products a sum loses 2.7e-6 of itself over
-// K = 2048, 1.0e-5 over 4096, 3.0e-5 over 8192 and 3.8e-4 over 65536, and the loss, which stays in 32 bits, with it.
-// Logits of a longer K than 2048 are therefore summed 2048 of it at a time, the parts in registers with rounding, also
-// within each pair's share of a split tile: 2.8e-6 at most, for any K.  This takes half of the registers, so that the
-// kernel that follows no longer starts ahead: 4096 x 32000, 100 rows 54 -> 59 us, 2000 rows 295 -> 298; shorter ones
-// keep the plain form (1024 x 32000, 100 rows 20 us, in the other 24).  The backward's logits go the same way: p =
-// exp(l - lse) wants l as it was when lse was made of it, above all where p is near 1 and the gradient is 1 - p (a
-// logit of 30 that lost 1.0e-5 of itself makes 1 - p = 1e-3 a third larger).
-constexpr int kPart = 32;  // blocks of 64 of K
+// K = 2048, 1.0e-5 over 4096, 3.0e-5 over 8192, 3.8e-4 over 65536 and 1.6e-3 over 262144 (of products of either sign,
+// relative to the result's 2-norm: 2.1e-6, 4.4e-6, 9.1e-6, 7.6e-5, 3.0e-4).  Results that stay in 32 bits are therefore
+// summed a part of a long K at a time, the parts in registers with rounding, also within each pair's share of a split
+// tile; the whole goes back to TMEM for the epilogue.  The sums take most of the registers, so that the kernel that
+// follows no longer starts ahead, and a change of parts costs about 0.4 us of a pair's time.
+//
+// The loss: 2048 at a time, 2.8e-6 at most for any K (4096 x 32000, 100 rows 54 -> 58 us, 2000 rows 295 -> 298; shorter
+// rows keep the plain form).  The backward's logits go the same way: p = exp(l - lse) wants l as it was when lse was
+// made of it, above all where p is near 1 and the gradient is 1 - p (a logit of 30 that lost 1.0e-5 of itself makes
+// 1 - p = 1e-3 a third larger).  Weight gradients in fp32, over K rows: 4096 at a time.
+constexpr int kPart = 32;      // blocks of 64 of K
+constexpr int kPartRows = 64;
 template <int MODE>
 constexpr bool kIsLse = MODE == kLse || MODE == kLseLong;
 template <int MODE>
 constexpr bool kIsDlogits = MODE == kDlogits || MODE == kDlogitsLong;
 template <int MODE>
-constexpr bool kInParts = MODE == kLseLong || MODE == kDlogitsLong;
-// Sums that a thread of the epilogue keeps: its row's half of a tile's columns.
-template <int MODE, int NT>
-constexpr int kSums = kInParts<MODE> ? NT / 2 : 1;
+constexpr bool kIsStore = MODE == kStore || MODE == kStoreLong;
+template <int MODE>
+constexpr bool kInParts = MODE == kStoreLong || MODE == kLseLong || MODE == kDlogitsLong;
+template <int MODE>
+constexpr int kPartOf = kIsStore<MODE> ? kPartRows : kPart;
 constexpr int kRowsBytes = 4096;    // an epilogue warp's 32 rows of 32 columns of up to 32 bits
 
 template <int NT>
@@ -556,7 +562,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t, int s)
 {
     Tile r;
     r.prod = 0;
-    if (MODE == kStore)
+    if (kIsStore<MODE>)
         while (r.prod + 1 < a.n && t >= a.p[r.prod + 1].first)
             ++r.prod;
     const Product &p = a.p[r.prod];
@@ -573,16 +579,23 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int t, int s)
     return r;
 }
 
+// Parts of K that a tile (a pair's share of it) is summed in.
+template <int MODE>
+__device__ __forceinline__ int parts_of(const Tile &t)
+{
+    return (t.kb1 - t.kb0 + kPartOf<MODE> - 1) / kPartOf<MODE>;
+}
+
 // Columns of D that a tile covers.
 template <int MODE, int NT>
 constexpr int kCols = MODE == kGated ? NT / 2 : NT;
 
 // The parts of a split tile's accumulator to the pairs that own their columns, and the owners' epilogue.  All
 // threads of the cluster.  buf: [S sources][columns / 4][128 rows] of four columns, so that neighbouring threads
-// (rows) touch neighbouring 16 bytes.  The accumulator is in TMEM, or its sum over parts of K in `sums`.
+// (rows) touch neighbouring 16 bytes.
 template <int MODE, class TE, int NT>
 __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_base, const Tile &tile, int rank,
-                                     int pair, int warp, int lane, const float (&sums)[kSums<MODE, NT>])
+                                     int pair, int warp, int lane)
 {
     const int S = a.S, q = warp & 3, half = (warp - 2) / 4, r = q * 32 + lane;
     // accumulator columns that a pair owns: gated, as many of the gate's as of the up's
@@ -590,18 +603,12 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
     constexpr int kSide = NT / kSides;
     const int own = kSide / S;  // of each side, 32 or more
     if (warp >= 2) {
-        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
-#pragma unroll(kInParts<MODE> ? NT / 32 : 1)
-        for (int i0 = 0; i0 < NT / 2; i0 += 16) {
-            const int c = half * (NT / 2) + i0;
+        const int acc = kInParts<MODE> ? (parts_of<MODE>(tile) - 1) & 1 : 0;
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+#pragma unroll 1
+        for (int c = half * (NT / 2); c < (half + 1) * (NT / 2); c += 16) {
             float v[16];
-            if constexpr (kInParts<MODE>) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = sums[i0 + i];
-            } else {
-                tmem_ld16(tacc + c, v);
-            }
+            tmem_ld16(tacc + c, v);
             const int side = c / kSide, at = c % kSide, owner = at / own, local = side * own + at % own;
             const uint32_t dst = cluster_map(buf, (uint32_t)(owner * 2 + rank)) +
                                  (uint32_t)(((pair * kSides * own + local) / 4 * 128 + r) * 16);
@@ -648,7 +655,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
             float u[16];
             sum16(own + half * mine + c, u);
             epi_gated<TE>(a, row, col + c, v, u);
-        } else if constexpr (MODE == kStore) {
+        } else if constexpr (kIsStore<MODE>) {
             epi_store<TE>(p, row, col + c, v);
         } else if constexpr (MODE == kGatedBwd) {
             epi_gated_bwd<TE>(a, row, col + c, v);
@@ -724,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
 
-    float sums[kSums<MODE, NT>];  // of the epilogue's threads
     if (warp == 0) {
         if (lane == 0) {
             // both operands are read again by the pairs around (ms as above: evict-normal 1.740, evict-last 1.699; the
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int t = first, k = 0; ok && t < a.tiles; t = a.deal.tile(cluster, ++k)) {
                 const Tile tile = tile_of<MODE>(a, t, pair);
                 const Product &p = a.p[tile.prod];
-                const int maj = MODE == kStore ? p.maj : MODE == kGatedBwd ? 1 : 0;
+                const int maj = kIsStore<MODE> ? p.maj : MODE == kGatedBwd ? 1 : 0;
                 const int arow = tile.m0 + rank * 128;
                 // gated: CTA 0 holds gate rows, CTA 1 the matching up rows
                 const int brow = MODE == kGated ? rank * p.N + tile.nt * kHalf : tile.nt * NT + rank * kHalf;
@@ -784,10 +790,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             bool ok = true, any = false;
             for (int t = first, k = 0; ok && t < a.tiles; t = a.deal.tile(cluster, ++k)) {
                 const Tile tile = tile_of<MODE>(a, t, pair);
-                const int maj = MODE == kStore ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
+                const int maj = kIsStore<MODE> ? a.p[tile.prod].maj : MODE == kGatedBwd ? 1 : 0;
                 const uint32_t idesc = make_idesc(type, type, 256, NT) | (maj >= 1 ? 1u << 16 : 0u) |
                                        (maj == 2 ? 1u << 15 : 0u);
-                const int part = kInParts<MODE> ? kPart : tile.kb1 - tile.kb0;
+                const int part = kInParts<MODE> ? kPartOf<MODE> : tile.kb1 - tile.kb0;
                 for (int k0 = tile.kb0; k0 < tile.kb1; k0 += part) {
                     if (!mbar_wait(&sm.tempty[acc], aph ^ 1, a.status, abort_flag)) {
                         ok = false;
@@ -856,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     prefetch_l2(kept + p.N + c);
                 }
             }
-            if (MODE == kStore && S == 1 && live && p.add) {
+            if (kIsStore<MODE> && S == 1 && live && p.add) {
                 const int es = p.d_f32 ? 4 : 2;
                 const char *add = static_cast<const char *>(p.add) + (row * p.ld_add + c0) * es;
                 for (int c = 0; c < kMine && c0 + c < p.N; c += 128 / es)
@@ -873,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const auto read = [&](int c) {
                 if (rows == 0 || S > 1 || c >= kMine || c0 + c >= p.N)
                     return;
-                if (MODE == kStore && p.add) {
+                if (kIsStore<MODE> && p.add) {
                     const int64_t at = row0 * p.ld_add + c0 + c;
                     const int cols = p.N - c0 - c;
                     if (p.d_f32)
@@ -887,70 +893,67 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     Rows<TE>::load(kept + p.N, 2 * (int64_t)p.N, rows, p.N - c0 - c, lane, pre + 4);
                 }
             };
-            read(0);
+            if (!kInParts<MODE>)
+                read(0);
+            // the CTA's rows of accumulator `acc`, this warp's half of the columns
+            const auto wait = [&] {
+                const bool done = __all_sync(0xffffffffu, mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag));
+                tc_fence_after();
+                return done;
+            };
+            const auto at = [&] { return tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine; };
+            const auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
+                if (++acc == 2) {
+                    acc = 0;
+                    aph ^= 1;
+                }
+            };
+            bool ok = true;
             if constexpr (kInParts<MODE>) {
-                bool ok = true;
+                if (parts_of<MODE>(tile) > 1) {
+                    // all parts but the last are added up here, then the last one, and the whole goes back to its place
+                    float sums[kMine];
 #pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    sums[i] = 0.0f;
-                for (int k0 = tile.kb0; k0 < tile.kb1; k0 += kPart) {
-                    ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
+                    for (int c = 0; c < kMine; ++c)
+                        sums[c] = 0.0f;
+                    for (int i = parts_of<MODE>(tile); i > 1 && (ok = wait()); --i) {
+#pragma unroll
+                        for (int c = 0; c < kMine; c += 16) {
+                            float f[16];
+                            tmem_ld16(at() + c, f);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sums[c + j] += f[j];
+                        }
+                        release();
+                    }
+                    if (!ok || !(ok = wait()))
                         break;
-                    tc_fence_after();
-                    const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
 #pragma unroll
                     for (int c = 0; c < kMine; c += 16) {
                         float f[16];
-                        tmem_ld16(tacc + c, f);
+                        tmem_ld16(at() + c, f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sums[c + i] += f[i];
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
-                    if (++acc == 2) {
-                        acc = 0;
-                        aph ^= 1;
-                    }
-                }
-                if (!ok || S > 1)
-                    break;  // (the parts of a split tile meet below)
-                if constexpr (kIsLse<MODE>) {
-                    float m = -INFINITY, e = 0.0f, own = 0.0f;
-                    bool has = false;
-#pragma unroll
-                    for (int c = 0; c < kMine; c += 16)
-                        if (c0 + c < p.N)
-                            epi_lse(p.N, c0 + c, of.target, reinterpret_cast<float(&)[16]>(sums[c]), m, e, own, has);
-                    if (live) {
-                        a.stats[row * a.pairs + tile.nt * 2 + half] = make_float2(m, e);
-                        if (has)
-                            a.target_logit[row] = own;
+                        for (int j = 0; j < 16; ++j)
+                            f[j] += sums[c + j];
+                        tmem_st16(at() + c, f);
                     }
                 } else {
-#pragma unroll
-                    for (int c = 0; c < kMine; c += 32)
-                        if (c0 + c < p.N && rows > 0) {
-                            float(&v)[32] = reinterpret_cast<float(&)[32]>(sums[c]);
-                            epi_dlogits(c0 + c, of.target, of.lse, of.factor, v);
-                            put_rows(buf, v, static_cast<TE *>(p.d) + row0 * p.ld_d + c0 + c, p.ld_d, rows,
-                                     p.N - c0 - c, lane);
-                        }
+                    ok = wait();
                 }
-                continue;
+                read(0);
+            } else {
+                ok = wait();
             }
-            bool ok = mbar_wait(&sm.tfull[acc], aph, a.status, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
-            tc_fence_after();
             if (S > 1)
                 break;  // the parts meet below
-            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256 + half * kMine;
+            const uint32_t tacc = at();
             float m = -INFINITY, e = 0.0f, own = 0.0f;
             bool has = false;
 #pragma unroll 1
@@ -958,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const int col = c0 + c, cols = p.N - col;
                 float v[32];
                 tmem_ld32(tacc + c, v);
-                if constexpr (MODE == kStore) {
+                if constexpr (kIsStore<MODE>) {
                     if (p.acc_in) {
                         uint4 w[8];
                         Rows<float>::load(p.acc_in + row0 * p.N + col, p.N, rows, cols, lane, w);
@@ -1042,14 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 if (has)
                     a.target_logit[row] = own;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_remote(cluster_map(&sm.tempty[acc], lead));
-            if (++acc == 2) {
-                acc = 0;
-                aph ^= 1;
-            }
+            release();
         }
     }
 
@@ -1060,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         tc_fence_before();
         cluster_sync();
         tc_fence_after();
-        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane, sums);
+        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
     }
     // both CTAs stay until the pair's last MMA, copy and remote arrive are done
     __syncwarp();
@@ -1247,6 +1243,11 @@ Plan plan(const Product *p, int n, const int *clusters)
     return best;
 }
 
+// Whether a product to memory needs its sum in parts of K: weight gradients in fp32 of more rows than one part, and
+// what is rounded to 16 bits where the truncation comes near that (1.7e-4 of positive terms at K = 32768; half a step of
+// fp16 is 4.9e-4 at most).
+inline bool wants_parts(const Product &p) { return p.K > (p.maj == 2 && p.d_f32 ? 64 * kPartRows : 32768); }
+
 // The products of `a` (p[0] .. p[n - 1]), longest K first: in one launch, the first apart from the others, or each in
 // its own, whichever is fastest (a product of few tiles and a long K wants it split, one of many tiles does not).
 template <int MODE, class TE>
@@ -1294,6 +1295,16 @@ cudaError_t launch(Args &a, cudaStream_t st)
     for (int i = 1; i < a.n && err == cudaSuccess; ++i)
         err = go(i, 1, each[i]);
     return err;
+}
+
+// The products of `a` to memory.
+template <class TE>
+cudaError_t launch_store(Args &a, cudaStream_t st)
+{
+    bool parts = false;
+    for (int i = 0; i < a.n; ++i)
+        parts = parts || wants_parts(a.p[i]);
+    return parts ? launch<kStoreLong, TE>(a, st) : launch<kStore, TE>(a, st);
 }
 
 }  // namespace dense

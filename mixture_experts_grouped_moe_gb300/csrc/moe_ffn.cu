@@ -45,7 +45,7 @@ cudaError_t forward(const Args &base, const void *x, int64_t ld_x, const void *W
     if (err != cudaSuccess)
         return err;
     // (the kernel before it waits for whatever wrote W_down, and lets this one start only then)
-    return few ? launch_few<kStore, TE>(down, true, st) : launch<kStore, TE>(down, st);
+    return few ? launch_few<kStore, TE>(down, true, st) : launch_store<TE>(down, st);
 }
 
 template <class TE>
@@ -77,7 +77,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
         wgrad(product(a, I2, H, (int)T, 2, dgu, I2, x, ld_x), dWgu);
     if (dWd)
         wgrad(product(a, H, I, (int)T, 2, dout, ld_dout, h, I), dWd);
-    return a.n ? launch<kStore, TE>(a, st) : cudaSuccess;
+    return a.n ? launch_store<TE>(a, st) : cudaSuccess;
 }
 
 }  // namespace

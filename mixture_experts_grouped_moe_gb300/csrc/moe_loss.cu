@@ -202,7 +202,7 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
             if (accumulate)
                 q.add = q.d, q.ld_add = H;
         }
-        if (a.n && (err = launch<kStore, TE>(a, st)) != cudaSuccess)
+        if (a.n && (err = launch_store<TE>(a, st)) != cudaSuccess)
             return err;
     }
     return err;

@@ -89,3 +89,77 @@ def test_gradient_of_sure_rows(moe, T, K, V):
         wd = w[:, i:i + 8192].double()
         want, err = dl @ wd, ed @ wd + loss_of(V, max(V, 16)) * (full @ wd)
         tr.bounded(dx[:, i:i + 8192], want, err + e * (want.abs() + err) + ref.TINY["bf16"], "dx")
+
+
+ROWS = 4096  # of a weight gradient in fp32 at a time
+
+
+# One tile, whose rows four pairs share, and tiles enough that none is shared
+@pytest.mark.parametrize("T,H,I", [(2 ** 21, 64, 64), (8192, 1792, 1792), (12000, 2048, 2056)])
+def test_weight_gradient_of_many_rows(moe, T, H, I):
+    """dW_down = dout^T h of rows that all add to it with the same sign."""
+    x, dout = positive(T, H, seed=6), positive(T, H, seed=7)
+    wgu, wd = positive(2 * I, H, seed=8, scale=1 / H), positive(H, I, seed=9, scale=1 / I)
+    f = moe.GatedFFN(T, H, I, moe.MOE_ACT_RELU, training=True)
+    f.forward(x, wgu, wd)
+    g = f.backward(x, wgu, wd, dout)
+    want = sum(a.double().t() @ b.double() for a, b in zip(dout.split(65536), f.h.split(65536)))
+    e = want * (loss_of(T, ROWS) * 1.1 + 2.0 ** -22)
+    tr.bounded(g["dW_down"], want, e, "dW_down")
+    old = torch.full((H, I), 3.0, device="cuda")
+    more = f.backward(x, wgu, wd, dout, torch.zeros(2 * I, H, device="cuda"), old, accumulate=True)
+    tr.bounded(more["dW_down"], want + 3, e + 2.0 ** -23 * (want + 3), "accumulated")
+    assert f.status() == moe.MOE_OK
+
+
+def test_sixteen_bit_gradient_of_many_rows(moe):
+    """The same in fp16: within a rounding of 64 bits."""
+    T, H, I = 2 ** 21, 64, 64
+    x, dout = positive(T, H, seed=6).half(), positive(T, H, seed=7, scale=2.0 ** -8).half()
+    wgu, wd = positive(2 * I, H, seed=8, scale=1 / H).half(), positive(H, I, seed=9, scale=1 / I).half()
+    f = moe.GatedFFN(T, H, I, moe.MOE_ACT_RELU, torch.float16, training=True)
+    f.forward(x, wgu, wd)
+    got = f.backward(x, wgu, wd, dout, grad_dtype=torch.float16)["dW_down"]
+    want = dout.double().t() @ f.h.double()
+    assert float(want.max()) < 60000
+    e = want * (loss_of(T, ROWS) * 1.1 + 2.0 ** -22)
+    tr.bounded(got, want, e + ref.HALF_ULP["fp16"] * (want + e), "dW_down")
+
+
+@pytest.mark.parametrize("T", [4097, 40000])
+def test_gradients_in_parts(moe, T):
+    """More rows than one sum takes, the last part a single one: every gradient of both operators, written and added,
+    within the bounds of fewer rows."""
+    H, I, V, piece = 72, 136, 300, 192
+    g = ref.gen(T)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).bfloat16().cuda()  # noqa: E731
+    x, wgu, wd, dout = r(T, H), r(2 * I, H, std=H ** -0.5), r(H, I, std=I ** -0.5), r(T, H)
+    f = moe.GatedFFN(T, H, I, training=True)
+    f.forward(x, wgu, wd)
+    d = [v.double() for v in (x, wgu, wd, f.gu, f.h, dout)]
+    got = f.backward(x, wgu, wd, dout)
+    want, bound = tr.ffn_grads_bound(*d[:3], "silu", *d[3:], "bf16", "fp32")
+    for n in want:
+        b = tr.ffn_grads_bound(*d[:3], "silu", *d[3:], "bf16", "bf16")[1][n] if n == "dx" else bound[n]
+        tr.bounded(got[n], want[n], b, n)
+    old = {n: torch.randn(got[n].shape, generator=g).cuda() for n in ("dW_gate_up", "dW_down")}
+    more = f.backward(x, wgu, wd, dout, *(v.clone() for v in old.values()), accumulate=True)
+    dold = {n: v.double() for n, v in old.items()}
+    _, bound = tr.ffn_grads_bound(*d[:3], "silu", *d[3:], "bf16", "fp32", dold)
+    for n in old:
+        tr.bounded(more[n], want[n] + dold[n], bound[n], n + " accumulated")
+    wv = r(V, H, std=2 * H ** -0.5)
+    targets = torch.randint(-1, V, (T,), generator=g, dtype=torch.int32).cuda()
+    dloss = (torch.randn(T, generator=g) / T).cuda()
+    v = moe.VocabularyLoss(T, H, V, training=True, piece=piece)
+    v.forward(x, wv, targets)
+    got = v.backward(x, wv, targets, dloss)
+    args = x.double(), wv.double(), targets, dloss.double(), "bf16"
+    want, bound = tr.loss_grads_bound(*args, "fp32")
+    tr.bounded(got["dW"], want["dW"], bound["dW"], "dW")
+    tr.bounded(got["dx"], want["dx"], tr.loss_grads_bound(*args, "bf16")[1]["dx"], "dx")
+    old = torch.randn(V, H, generator=g).cuda()
+    more = v.backward(x, wv, targets, dloss, old.clone(), accumulate=True)["dW"]
+    tr.bounded(more, want["dW"] + old.double(), tr.loss_grads_bound(*args, "fp32", old.double())[1]["dW"],
+               "dW accumulated")
+    assert f.status() == moe.MOE_OK and v.status() == moe.MOE_OK
