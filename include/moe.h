@@ -715,6 +715,11 @@ int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_ga
  *   accumulate = 1 adds the weight gradients to what is there (one rounding of
  *   the sum), 0 overwrites it;
  *   ws (device) moe_ffn_workspace_size(..., 1) bytes.
+ * The gradients of g and u are rounded to row_type before their products; in
+ * fp16 they are scaled by a power of two that brings the largest finite |dout|
+ * to [1, 2) where it is smaller, so that fp16 holds them (a product dout W_down
+ * with its factors of u and act' may then be up to 2^15 times that before it
+ * overflows).
  */
 int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const void *W_gate_up, const void *W_down,
                      const void *gu, const void *h, const void *dout, int64_t ld_dout, int64_t T, int H, int I,

@@ -109,7 +109,9 @@ struct Args {
     int act;
     void *h;              // [M][N]
     void *gu;             // [M][2N], kept by the forward (may be null) and read by the backward
-    void *dgu;            // [M][2N]
+    void *dgu;            // [M][2N], fp16: times a power of two (gradient_factor)
+    const unsigned *most; // [kMost], fp16: the largest finite |dout|, in parts, as bits
+    float *back;          // the inverse of that factor
     // cross entropy
     const int32_t *targets;
     float2 *stats;        // [M][pairs]
@@ -423,10 +425,30 @@ __device__ __forceinline__ void epi_gated(const Args &a, int64_t row, int col, f
             store8(hd + i, g + i);
 }
 
+constexpr int kMost = 128;
+
+// In fp16, d gate | d up are kept times 2^-e, with the largest finite |dout| in [2^e, 2^(e+1)) and e < 0: steps of
+// 2^-24 would otherwise be all that is left of an output gradient far below one (a step is 6 % at 1e-6).  Its products
+// are scaled back in fp32.  bf16 has fp32's range.
+template <class TE>
+constexpr bool kScaledGrad = std::is_same<TE, __half>::value;
+
+// The factor (a whole warp).
+__device__ __forceinline__ float gradient_factor(const unsigned *most, int lane)
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; i += 32)
+        m = max(m, most[i + lane]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const float v = __half2float(__ushort_as_half((unsigned short)m));
+    return v > 0.0f && v < 1.0f ? ldexpf(1.0f, -ilogbf(v)) : 1.0f;
+}
+
 // d gate = dh u act'(g), d up = dh act(g) of 8 columns, in the place of g and u: rounded to 16 bits as the operands
 // of the products that follow.
 template <class TE, int ACT>
-__device__ __forceinline__ void gated_grad8(const float *dh, uint4 &wg, uint4 &wu)
+__device__ __forceinline__ void gated_grad8(const float *dh, float factor, uint4 &wg, uint4 &wu)
 {
     float g[8], u[8];
     unpack8<TE>(wg, g);
@@ -435,15 +457,16 @@ __device__ __forceinline__ void gated_grad8(const float *dh, uint4 &wg, uint4 &w
     for (int j = 0; j < 8; ++j) {
         float v, slope;
         act_grad<ACT>(g[j], v, slope);
-        g[j] = dh[j] * u[j] * slope;
-        u[j] = dh[j] * v;
+        const float d = kScaledGrad<TE> ? dh[j] * factor : dh[j];
+        g[j] = d * u[j] * slope;
+        u[j] = d * v;
     }
     wg = pack8<TE>(g);
     wu = pack8<TE>(u);
 }
 
 template <class TE, int W>
-__device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int col, const float (&dh)[W])
+__device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int col, const float (&dh)[W], float factor)
 {
     const int N = a.p[0].N;
     const TE *kept = static_cast<const TE *>(a.gu) + row * 2 * N + col;
@@ -459,7 +482,7 @@ __device__ __forceinline__ void epi_gated_bwd(const Args &a, int64_t row, int co
 #pragma unroll
         for (int i = 0; i < W; i += 8)
             if (col + i < N)
-                gated_grad8<TE, decltype(kind)::value>(dh + i, wg[i / 8], wu[i / 8]);
+                gated_grad8<TE, decltype(kind)::value>(dh + i, factor, wg[i / 8], wu[i / 8]);
     });
 #pragma unroll
     for (int i = 0; i < W; i += 8)
@@ -595,7 +618,7 @@ constexpr int kCols = MODE == kGated ? NT / 2 : NT;
 // (rows) touch neighbouring 16 bytes.
 template <int MODE, class TE, int NT>
 __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_base, const Tile &tile, int rank,
-                                     int pair, int warp, int lane)
+                                     int pair, int warp, int lane, float factor)
 {
     const int S = a.S, q = warp & 3, half = (warp - 2) / 4, r = q * 32 + lane;
     // accumulator columns that a pair owns: gated, as many of the gate's as of the up's
@@ -658,7 +681,7 @@ __device__ __forceinline__ void meet(const Args &a, uint8_t *buf, uint32_t tmem_
         } else if constexpr (kIsStore<MODE>) {
             epi_store<TE>(p, row, col + c, v);
         } else if constexpr (MODE == kGatedBwd) {
-            epi_gated_bwd<TE>(a, row, col + c, v);
+            epi_gated_bwd<TE>(a, row, col + c, v, factor);
         } else if constexpr (kIsLse<MODE>) {
             epi_lse(p.N, col + c, of.target, v, top, exps, target_logit, has);
         } else {
@@ -731,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
 
+    float factor = 1.0f;  // of d gate | d up
     if (warp == 0) {
         if (lane == 0) {
             // both operands are read again by the pairs around (ms as above: evict-normal 1.740, evict-last 1.699; the
@@ -847,6 +871,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int r = q * 32 + lane;
         int acc = 0;
         uint32_t aph = 0;
+        if constexpr (MODE == kGatedBwd && kScaledGrad<TE>) {
+            factor = gradient_factor(a.most, lane);
+            if (blockIdx.x == 0 && warp == 2 && lane == 0)
+                *a.back = 1.0f / factor;
+        }
         for (int t = first, k = 0; t < a.tiles; t = a.deal.tile(cluster, ++k)) {
             const Tile tile = tile_of<MODE>(a, t, pair);
             const Product &p = a.p[tile.prod];
@@ -1027,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     with_act(a.act, [&](auto kind) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            gated_grad8<TE, decltype(kind)::value>(v + 8 * i, wg[i], wu[i]);
+                            gated_grad8<TE, decltype(kind)::value>(v + 8 * i, factor, wg[i], wu[i]);
                     });
                     TE *out = static_cast<TE *>(a.dgu) + row0 * 2 * p.N + col;
                     Rows<TE>::store(buf, wg, out, 2 * (int64_t)p.N, rows, cols, lane);
@@ -1056,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         tc_fence_before();
         cluster_sync();
         tc_fence_after();
-        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane);
+        meet<MODE, TE, NT>(a, sm.stage[0], tmem_base, tile_of<MODE>(a, first, pair), rank, pair, warp, lane, factor);
     }
     // both CTAs stay until the pair's last MMA, copy and remote arrive are done
     __syncwarp();
