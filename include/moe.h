@@ -727,7 +727,8 @@ int moe_ffn_backward(int row_type, int act, const void *x, int64_t ld_x, const v
                      size_t ws_bytes, void *stream);
 
 /* Workspace bytes of moe_vocab_loss (piece = 0), or of it and
- * moe_vocab_loss_backward with that piece; 0 on invalid or unsupported sizes. */
+ * moe_vocab_loss_backward with that piece; 0 on invalid or unsupported sizes.
+ * It does not fall as T grows: a workspace for T rows serves fewer as well. */
 size_t moe_vocab_loss_workspace_size(int64_t T, int H, int V, int piece);
 
 /*
