@@ -695,7 +695,7 @@ size_t moe_ffn_workspace_size(int64_t T, int H, int I, int training);
  *   add (device) [T] rows of H at a pitch of ld_add, or NULL (nothing is
  *   added; ld_add is ignored);
  *   out (device) [T] rows of H at a pitch of ld_out; it may be add, with its
- *   pitch;
+ *   pitch, but no other bytes of add (MOE_ERR_INVALID_ARG);
  *   gu (device) [T][2I] (g | u of a row, rounded) and h (device) [T][I]: kept
  *   for the backward; both may be NULL, and gu with h given.
  * h is rounded to row_type before its product.  ws (device)

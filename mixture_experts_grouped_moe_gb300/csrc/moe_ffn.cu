@@ -30,6 +30,30 @@ bool bad_sizes(int64_t T, int H, int I)
     return H % 8 != 0 || I % 8 != 0 || H > 1 << 20 || I > 1 << 20 || T > 1 << 30;
 }
 
+// Whether T rows of H 16-bit elements at `a`, lda apart, and at `b`, ldb apart, have bytes in common, except as the same
+// rows.  Rows that lie between one another's in a wider buffer do not.
+bool overlaps(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t T, int H)
+{
+    const intptr_t d = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a);  // (a multiple of 16)
+    const int64_t last_a = (T - 1) * lda, last_b = (T - 1) * ldb, off = d / 2;
+    if (T <= 1)
+        return off != 0 && off < H && off > -H;
+    if (off >= last_a + H || off + last_b + H <= 0)
+        return false;
+    if (lda == ldb) {
+        const int64_t m = (off % lda + lda) % lda;
+        return off != 0 && (m < H || m + H > lda);
+    }
+    for (int64_t i = 0; i < T; ++i) {  // (different pitches in one buffer: row by row)
+        // rows j of a with |j lda - at| < H
+        const int64_t at = off + i * ldb;
+        const int64_t low = at - H < 0 ? 0 : (at - H) / lda + 1;
+        if (low < T && low * lda < at + H)
+            return true;
+    }
+    return false;
+}
+
 int to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // The largest finite |dout| of the rows that fall to each of kMost blocks, as bits.  1 << lg threads share a row, and
@@ -168,6 +192,8 @@ int moe_ffn(int row_type, int act, const void *x, int64_t ld_x, const void *W_ga
         return MOE_ERR_WORKSPACE;
     if (T == 0)
         return MOE_OK;
+    if (add && overlaps(add, ld_add, out, ld_out, T, H))
+        return MOE_ERR_INVALID_ARG;
     uint8_t *at = static_cast<uint8_t *>(ws);
     Args base = {};
     base.status = reinterpret_cast<int *>(at);

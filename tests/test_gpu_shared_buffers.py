@@ -38,3 +38,36 @@ def test_workspace_of_the_largest_batch(moe, V):
         want = f.backward(x, w, targets, dloss, grad_dtype=torch.bfloat16)
         assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dW"])
         assert moe.moe_workspace_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [1, 5, 300])
+@pytest.mark.parametrize("ld_add,ld_out,start", [(256, 256, 128), (256, 256, 136), (256, 256, -128), (128, 128, 0),
+                                                 (512, 256, 256), (136, 264, -1), (256, 256, 256 * 4 + 120)])
+def test_ffn_output_beside_add(moe, T, ld_add, ld_out, start):
+    """add and out as rows of one buffer, `start` elements apart: between each other's rows they are computed as if
+    apart, the same rows too, and anything else in common is refused before a launch."""
+    H, I = 120, 64
+    start = -ld_out * T if start == -1 else start
+    g = ref.gen(T)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).bfloat16().cuda()  # noqa: E731
+    x, wgu, wd = r(T, H), r(2 * I, H, std=H ** -0.5), r(H, I, std=I ** -0.5)
+    buf = r(max(0, -start) + T * (ld_add + ld_out) + max(0, start) + H)
+    at = max(0, -start)
+    add = torch.as_strided(buf, (T, H), (ld_add, 1), at)
+    out = torch.as_strided(buf, (T, H), (ld_out, 1), at + start)
+    places = lambda t, ld: {t.storage_offset() + i * ld + j for i in range(T) for j in range(H)}  # noqa: E731
+    common = places(add, ld_add) & places(out, ld_out)
+    f = moe.GatedFFN(T, H, I)
+    if common and start != 0:
+        before = buf.clone()
+        with pytest.raises(moe.MoEError):
+            f.forward(x, wgu, wd, add, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(buf, before)
+        return
+    want = f.forward(x, wgu, wd, add.clone())
+    kept = torch.ones_like(buf, dtype=torch.bool)
+    torch.as_strided(kept, (T, H), (ld_out, 1), at + start).fill_(False)
+    before = buf.clone()
+    f.forward(x, wgu, wd, add, out=out)
+    assert torch.equal(out, want) and torch.equal(buf[kept], before[kept])

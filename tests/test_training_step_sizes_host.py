@@ -7,6 +7,13 @@ INVALID = -1
 P = 1024  # a non-null, aligned stand-in for a device pointer
 
 
+def refused(fn, good, cases):
+    """good: dict of a call; each case changes some arguments."""
+    for change, status in cases:
+        assert not set(change) - set(good), change
+        assert fn(*dict(good, **change).values()) == status, change
+
+
 @pytest.fixture(scope="module")
 def moe():
     moe_build.build()
@@ -30,3 +37,16 @@ def test_workspace_of_the_loss_covers_smaller_batches(moe):
         sizes = [size(T, 64, V) for V in range(1, 40000, 101)]
         assert sizes == sorted(sizes), T
 
+
+def test_ffn_output_over_add(moe):
+    """out may be add with its pitch, or lie between its rows; every other overlap is refused."""
+    lib = moe.load()
+    A = 1 << 20  # a stand-in for a device address; only refused calls are made with rows
+    good = dict(t=0, act=0, x=P, ld=64, wgu=P, wd=P, add=A, ld_add=64, T=10, H=64, I=32, gu=None, h=None, out=A,
+                ld_out=64, ws=P, wsb=1 << 30, st=None)
+    refused(lib.moe_ffn, good, [
+        (dict(out=A + 16), INVALID), (dict(out=A - 16), INVALID), (dict(out=A + 64 * 2), INVALID),
+        (dict(out=A + 9 * 128 + 112), INVALID), (dict(ld_out=72), INVALID), (dict(ld_add=72), INVALID),
+        (dict(ld_add=128, ld_out=128, out=A + 112), INVALID), (dict(ld_add=128, ld_out=128, out=A - 112), INVALID),
+        (dict(ld_add=128, ld_out=128, out=A + 5 * 256 + 144), INVALID),
+        (dict(ld_add=192, ld_out=128, out=A + 128), INVALID), (dict(T=1, out=A + 112), INVALID)])
