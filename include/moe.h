@@ -779,7 +779,7 @@ int moe_grad_norm(int n, const int *types, const void *const *grads, const int64
 /*
  * The same, then out[i] = grads[i] * min(1, max_norm / (norm + eps)), each
  * element rounded once to its tensor's type.  out (host) [n]: device addresses; out[i]
- * may be grads[i], and overlaps no other tensor.  max_norm, eps >= 0.  A norm
+ * may be grads[i], and overlaps no other tensor; nor does norm.  max_norm, eps >= 0.  A norm
  * that is infinite or a NaN scales as the formula says.
  */
 int moe_clip_gradients(int n, const int *types, const void *const *grads, void *const *out, const int64_t *numel,

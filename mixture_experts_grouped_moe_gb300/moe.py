@@ -1224,7 +1224,7 @@ class GradientClip:
 
     def clip(self, grads, out=None, norm=None, stream=None):
         """Scales the gradients by min(1, max_norm / (norm + eps)), in place or into `out`, and returns their norm
-        from before, fp32 [1].  No two of the tensors written overlap."""
+        from before, fp32 [1].  No two of the tensors written overlap (`norm` is one of them)."""
         import torch
         grads = self._tensors("gradients", grads)
         norm = _output("norm", norm, (1,), torch.float32, self.ws.device, stream)
@@ -1235,7 +1235,7 @@ class GradientClip:
             if t is not g:
                 _expect(f"out[{i}]", t, g.shape, g.dtype)
         span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
-        spans = [(*span(t), True) for t in to if t.numel()]
+        spans = [(*span(t), True) for t in to if t.numel()] + [(*span(norm), True)]
         if to is not grads:  # (what is only read may be listed twice)
             spans += [(*span(g), False) for g, t in zip(grads, to) if g.numel() and g.data_ptr() != t.data_ptr()]
         written = any_end = 0  # ends of the furthest tensor to write, and of all

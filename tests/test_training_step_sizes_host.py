@@ -1,5 +1,6 @@
 """Workspace sizes and overlapping outputs of a training step's operators, on the host (nothing is launched)."""
 import pytest
+import torch
 
 from mixture_experts_grouped_moe_gb300 import build as moe_build
 
@@ -50,3 +51,15 @@ def test_ffn_output_over_add(moe):
         (dict(ld_add=128, ld_out=128, out=A + 112), INVALID), (dict(ld_add=128, ld_out=128, out=A - 112), INVALID),
         (dict(ld_add=128, ld_out=128, out=A + 5 * 256 + 144), INVALID),
         (dict(ld_add=192, ld_out=128, out=A + 128), INVALID), (dict(T=1, out=A + 112), INVALID)])
+
+
+def test_norm_inside_a_gradient(moe):
+    """clip writes the norm while it scales: it cannot lie in a gradient or an output."""
+    v = torch.zeros(100)
+    clip = moe.GradientClip(1.0, device="cpu")
+    for call in (lambda: clip.clip([v], norm=v[3:4]), lambda: clip.clip([v[:50]], [torch.zeros(50)], norm=v[49:50]),
+                 lambda: clip.clip([torch.zeros(50)], [v[:50]], norm=v[:1])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    with pytest.raises(ValueError, match="GPU"):  # (past the checks, as far as a CPU tensor goes)
+        clip.clip([v[:50]], norm=v[50:51])
