@@ -176,8 +176,10 @@ static_assert(kSmemBytes<256> <= 227 * 1024 && kSmemBytes<128> <= 227 * 1024, "a
 // ------------------------------------------------------------ activations
 
 // act(g) = g sigmoid(q(g)) with q = g (silu) or 2 sqrt(2/pi) (g + 0.044715 g^3) (gelu, tanh form: 1 + tanh z =
-// 2 sigmoid(2z)); relu apart.  One exponential and one reciprocal an element: their errors (2^-21) vanish in the
-// 16-bit rounding that follows, also where sigmoid is small, which 0.5 + 0.5 tanh would not give.
+// 2 sigmoid(2z)); relu apart.  One exponential and one reciprocal an element, relative to the result also where sigmoid
+// is small, which 0.5 + 0.5 tanh would not be.  The fast exponential's documented error grows with its argument, 2 +
+// 1.17 |q| steps of 2^-23: 2^-20 near zero, 2^-18.4 at |q| = 20 and 2^-16.4 at 80, where bf16 still holds silu.  For
+// the gelu q's own rounding adds as much.  Half a step of the 16-bit rounding that follows is 2^-12 or more.
 __device__ __forceinline__ float sigmoid_of(float q) { return __fdividef(1.0f, 1.0f + __expf(-q)); }
 
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2/pi)
