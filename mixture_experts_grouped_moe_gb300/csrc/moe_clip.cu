@@ -10,7 +10,9 @@
 // square loses is below 2^-149 and so nothing against the sum).  Everything above a thread's chunk is summed in 64
 // bits in a fixed order: results are bitwise reproducible.
 //
-// 5.6 GB of fp32 in 2.48 ms (6.8 TB/s, the copy rate), 134 MB in 68 us, 60 tensors of up to 6000 elements in 9.7.
+// 5.6 GB of fp32 in 2.48 ms (6.8 TB/s, the copy rate), 134 MB in 68 us (the norm alone 26; tensors off 16-byte
+// boundaries, scaled element by element, 227), 60 tensors of up to 6000 elements in 9.7 replayed from a graph and 30
+// called, all of it the host's.
 #include "moe_internal.h"
 #include "rows.cuh"
 

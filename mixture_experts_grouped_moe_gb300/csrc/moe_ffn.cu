@@ -3,13 +3,15 @@
 // and its gradients
 //   dh = dout Wd,  dg = dh u act'(g),  du = dh act(g),
 //   dx = [dg | du] Wgu,  dWgu = [dg | du]^T x,  dWd = dout^T h.
-// Products of dense_gemm.cuh in four launches (the three gradients in one); the activation and its gradient are
-// epilogues, and every matrix is read as it lies.  h, and in the backward [dg | du], are rounded to the rows' type
-// between the products (they are operands of 16-bit MMAs): errors of half a step an element, independent ones, that a
-// sum over I or T averages.  In fp16, whose smallest step is 2^-24, [dg | du] is scaled by a power of two first.
+// Products of dense_gemm.cuh in four launches (the three gradients in one; fp16 has one more, for the scale); the
+// activation and its gradient are epilogues, and every matrix is read as it lies.  h, and in the backward [dg | du], are
+// rounded to the rows' type between the products (they are operands of 16-bit MMAs): errors of half a step an element,
+// independent ones, that a sum over I or T averages.  In fp16, whose smallest step is 2^-24, [dg | du] is scaled by a
+// power of two first.
 //
-// 4096 tokens through 7168 x 2048, forward and gradients: 680-690 us, 1.6 PFLOP/s; forward alone see dense_gemm.cuh
-// and, for few tokens, dense_few.cuh.
+// 4096 tokens through 7168 x 2048, forward and gradients: 675-700 us replayed from a graph, 710-735 called in a row,
+// where the board's power bounds it (1.60 and 1.50 PFLOP/s); forward alone see dense_gemm.cuh and, for few tokens,
+// dense_few.cuh.
 #include "dense_few.cuh"
 
 namespace moe {

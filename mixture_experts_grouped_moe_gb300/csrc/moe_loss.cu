@@ -7,15 +7,17 @@
 // exponentials (fp32, from the unrounded accumulators) and the target's logit; a warp a row then joins the
 // tiles' pairs in a fixed order.  Backward, a piece of the vocabulary at a time: the logits are computed once
 // more and leave as dl, rounded to 16 bits, which both gradients' products read; dx is summed over the pieces
-// in fp32.  8 T V H operations against 6 that the gradients cannot do without: keeping fp32 logits instead
-// would take 4 T V bytes.
+// in fp32.  8 T V H operations against 6 that the gradients cannot do without: keeping fp32 logits from the forward
+// would take 4 T V bytes.  (Loss and gradients in one call, whose dloss is known beforehand, could go by chunks of rows
+// and keep a chunk's logits alone.)
 //
 // dl is scaled by a power of two to at most 2^15 (the largest finite |dloss| to [2^14, 2^15)) and the gradients
 // by its inverse: a mean over many rows makes dl too small for fp16 otherwise (its smallest step, 2^-24, is then
 // at most 2^-38 of the largest row's factor).
 //
-// Bound by the tensor pipe and in a row by the board's power: 4096 x 4096 x 32000 forward and backward 2.55 ms (1.68
-// PFLOP/s); by memory for few rows: 16 rows 48 us for 262 MB.
+// Bound by the tensor pipe and in a row by the board's power: 4096 x 4096 x 32000 forward and backward 2.47-2.53 ms
+// replayed from a graph, 2.67-2.78 called in a row (1.72 and 1.57 PFLOP/s with the repeated logits, 1.29 and 1.18
+// without); by memory for few rows: 16 rows 48 us for 262 MB.
 #include "dense_few.cuh"
 
 namespace moe {

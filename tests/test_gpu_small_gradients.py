@@ -101,3 +101,27 @@ def test_scale_of_the_output_gradient(moe):
         dx = f.backward(x, wgu, wd, d)["dx"]
         rest = torch.arange(T, device="cuda") != 17
         assert torch.equal(dx[rest], want[rest]) and not dx[17].isfinite().any()
+
+
+def test_scale_in_a_replayed_graph(moe):
+    """The scale is found anew in every replay, next to an eager object at work on another stream."""
+    T, H, I = 150, 136, 72
+    x, wgu, wd, dout = inputs(T, H, I, 60000, 8)
+    f, eager = (moe.GatedFFN(T, H, I, dtype=torch.float16, training=True) for _ in range(2))
+    f.forward(x, wgu, wd)
+    eager.forward(x, wgu, wd)
+    d = dout.clone()
+    f.backward(x, wgu, wd, d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = f.backward(x, wgu, wd, d)
+    for scale in (2.0 ** -8, 1.0, 2.0 ** 10, 2.0 ** -12):
+        d.copy_(dout * scale)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        want = eager.backward(x, wgu, wd, d, stream=side)
+        torch.cuda.synchronize()
+        for n in got:
+            assert torch.equal(got[n], want[n]), (n, scale)
