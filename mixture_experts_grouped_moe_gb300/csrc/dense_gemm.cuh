@@ -1275,8 +1275,8 @@ Plan plan(const Product *p, int n, const int *clusters)
 }
 
 // Whether a product to memory needs its sum in parts of K: weight gradients in fp32 of more rows than one part, and
-// what is rounded to 16 bits where the truncation comes near that (1.7e-4 of positive terms at K = 32768; half a step of
-// fp16 is 4.9e-4 at most).
+// what is rounded to 16 bits where the truncation comes near that (1.7e-4 of positive terms at K = 32768; half a step
+// of fp16 is 4.9e-4 at most).
 inline bool wants_parts(const Product &p) { return p.K > (p.maj == 2 && p.d_f32 ? 64 * kPartRows : 32768); }
 
 // The products of `a` (p[0] .. p[n - 1]), longest K first: in one launch, the first apart from the others, or each in

@@ -32,8 +32,8 @@ bool bad_sizes(int64_t T, int H, int I)
     return H % 8 != 0 || I % 8 != 0 || H > 1 << 20 || I > 1 << 20 || T > 1 << 30;
 }
 
-// Whether T rows of H 16-bit elements at `a`, lda apart, and at `b`, ldb apart, have bytes in common, except as the same
-// rows.  Rows that lie between one another's in a wider buffer do not.
+// Whether T rows of H 16-bit elements at `a`, lda apart, and at `b`, ldb apart, have bytes in common, except as the
+// same rows.  Rows that lie between one another's in a wider buffer do not.
 bool overlaps(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t T, int H)
 {
     const intptr_t d = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a);  // (a multiple of 16)
@@ -131,8 +131,8 @@ cudaError_t backward(const Args &base, const void *x, int64_t ld_x, const void *
             while (lg < 9 && 1 << lg < H / 8)
                 ++lg;
             const cudaError_t err =
-                launch_kernel(true, most_kernel, dim3(kMost), dim3(kMostThreads), 0, st, static_cast<const uint4 *>(dout),
-                              ld_dout / 8, T, H / 8, lg, most);
+                launch_kernel(true, most_kernel, dim3(kMost), dim3(kMostThreads), 0, st,
+                              static_cast<const uint4 *>(dout), ld_dout / 8, T, H / 8, lg, most);
             if (err != cudaSuccess)
                 return err;
             a.most = most;

@@ -115,15 +115,15 @@ __global__ void __launch_bounds__(512) prepare_kernel(const float *dloss, const 
 
 bool bad_sizes(int64_t T, int H, int V) { return H % 8 != 0 || H > 1 << 20 || V > 1 << 24 || T > 1 << 30; }
 
-// (maximum, sum) pairs that the forward may keep, whichever way it goes: two for a row of each 256-column tile, or up to
-// eight of each 128-column one, but where a tile is split not more than kMostSplit tiles have of 256 rows with eight a
-// row (few rows: not more than 32 of them have of the CTAs that run at once).  It grows with T and with V, so that a
-// workspace serves smaller batches too.
+// (maximum, sum) pairs that the forward may keep, whichever way it goes: two for a row of each 256-column tile (few
+// rows: one of each 128-column tile).  Where K is split, up to eight of each 128 columns, but not more than kMostSplit
+// tiles have of 256 rows with eight a row (few rows: than 32 of them have of the CTAs that run at once).  It grows with
+// T and with V, so that a workspace serves smaller batches too.
 int64_t pairs_of(int64_t T, int V)
 {
     const int64_t whole = 2 * T * (((int64_t)V + 255) / 256), split = 8 * T * (((int64_t)V + 127) / 128);
     constexpr int64_t kMostPairs = kMostSplit * 256 * 8;
-    static_assert(kMostPairs >= 32 * 8 * 304 && kFewMost<kLse> == 32, "few rows: 304 CTAs on 152 SMs");
+    static_assert(kMostPairs >= kFewMost<kLse> * 304, "few rows: 304 CTAs on 152 SMs");
     const int64_t most = split < kMostPairs ? split : kMostPairs;
     return whole > most ? whole : most;
 }
